@@ -19,6 +19,8 @@ from typing import Sequence
 
 from . import _capi
 from ._capi import PlanInfo, PlanOpts
+from .token_moves import (expert_combine, expert_combine_backward, expert_dispatch, expert_sort, paged_append,
+                          rotary)
 
 __all__ = [
     "BmmcError", "Plan", "bmmc_plan", "bmmc_plan_ex", "bmmc_plan_destroy", "bmmc_plan_info",
@@ -26,6 +28,7 @@ __all__ = [
     "bmmc_permute_host", "bmmc_permute_static_scratch", "transpose2d", "bpc_permute", "bmmc_dims_permute",
     "bmmc_dims_permute_bits", "bmmc_copy", "bmmc_lmad_copy", "bmmc_lmad_bpc", "lmad_copy", "lmad_copy_query", "lmad_copy_tensor", "contiguous", "bmmc_parm_rows", "bmmc_inverse_rows", "bmmc_compose",
     "bmmc_status_string", "bmmc_version", "library_path",
+    "expert_sort", "expert_dispatch", "expert_combine", "expert_combine_backward", "rotary", "paged_append",
 ]
 
 CLASS_NAMES = {0: "identity", 1: "complement", 2: "bp", 3: "bpc", 4: "bmmc"}

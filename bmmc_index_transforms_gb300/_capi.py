@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from . import _build
@@ -20,6 +21,7 @@ u64p = ctypes.POINTER(ctypes.c_uint64)
 intp = ctypes.POINTER(ctypes.c_int)
 i64p = ctypes.POINTER(ctypes.c_int64)
 vp = ctypes.c_void_p
+i64 = ctypes.c_int64
 
 # Status codes (bmmc_status)
 OK = 0
@@ -77,6 +79,18 @@ class LmadCopyInfo(ctypes.Structure):
                 ("block_run_out", ctypes.c_int64), ("block_tiles", ctypes.c_int64)]
 
 
+# bmmc_dtype
+F32, F16, BF16 = range(3)
+EXPERT_MAX_CHOICES = 64
+# rotary_turns_t.flags
+ROTARY_ADJACENT, ROTARY_INVERSE = 0x1, 0x2
+# rotary_args_t and paged_append_args_t, whose fields are all 8 bytes wide, as
+# packed values (made in one call, where a ctypes.Structure stores one field
+# after another)
+ROTARY_ARGS = struct.Struct("=2q10q8q")
+PAGED_APPEND_ARGS = struct.Struct("=2q20q8q3q5q8q")
+
+
 class BoundsReport(ctypes.Structure):
     _fields_ = [("enabled", ctypes.c_int), ("failures", ctypes.c_uint64), ("site", ctypes.c_int),
                 ("bytes", ctypes.c_int), ("address", ctypes.c_uint64), ("lo", ctypes.c_uint64),
@@ -125,6 +139,16 @@ SIGNATURES = {
     "bmmc_compose": (ctypes.c_int, [ctypes.c_int, u64p, u64, u64p, u64, u64p, u64p]),
     "bmmc_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "bmmc_version": (ctypes.c_int, []),
+    "expert_sort_workspace": (ctypes.c_int, [i64, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
+    "expert_sort": (ctypes.c_int, [vp, ctypes.c_int, i64, ctypes.c_int, ctypes.c_int, vp, vp, vp, vp,
+                                   ctypes.c_size_t, vp]),
+    "expert_dispatch": (ctypes.c_int, [vp, i64, vp, i64, ctypes.c_int, i64, ctypes.c_int, vp, i64, i64, vp]),
+    "expert_combine": (ctypes.c_int, [vp, i64, i64, vp, vp, ctypes.c_int, i64, ctypes.c_int, i64, ctypes.c_int, vp,
+                                      i64, vp]),
+    "expert_combine_backward": (ctypes.c_int, [vp, i64, vp, i64, i64, vp, vp, ctypes.c_int, i64, ctypes.c_int, i64,
+                                               ctypes.c_int, vp, i64, vp, vp]),
+    "rotary": (ctypes.c_int, [vp, vp]),
+    "paged_append": (ctypes.c_int, [vp, vp]),
     "bmmc_bounds_report": (ctypes.c_int, [ctypes.POINTER(BoundsReport), ctypes.c_int]),
     "bmmc_bounds_selftest": (ctypes.c_int, [vp, vp]),
 }

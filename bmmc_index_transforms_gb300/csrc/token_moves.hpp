@@ -1,0 +1,86 @@
+// Host-side checks shared by the entry points that move tokens by maps held
+// on the device (experts.cu, rotary.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <initializer_list>
+
+#include "../../include/bmmc.h"
+#include "launch.hpp"
+
+namespace bmmc {
+
+constexpr int64_t kMaxStride = (int64_t)1 << 40;  // elements; with the token limit, byte offsets stay below 2^63
+constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 1;
+
+// Bytes of one element; 0 for an unknown type.
+inline int dtype_bytes(int type) {
+    switch (type) {
+        case BMMC_F32: return 4;
+        case BMMC_F16: case BMMC_BF16: return 2;
+    }
+    return 0;
+}
+
+// An array of `rows` rows, `stride` bytes apart, `span` bytes each.
+struct Rows {
+    const void* base;
+    int64_t rows, stride, span;
+    uintptr_t lo() const { return (uintptr_t)base; }
+    uintptr_t hi() const { return rows < 1 ? lo() : lo() + (uintptr_t)((rows - 1) * stride + span); }
+};
+
+// Whether two arrays may share bytes.  Rows with one common stride that do
+// not run into each other are told apart (slices of one fused projection);
+// any other two whose address ranges meet count as overlapping.
+inline bool may_overlap(const Rows& a, const Rows& b) {
+    if (!a.base || !b.base || a.rows < 1 || b.rows < 1) return false;
+    if (a.hi() <= b.lo() || b.hi() <= a.lo()) return false;
+    if (a.stride != b.stride || a.stride <= 0) return true;
+    const int64_t s = a.stride;
+    int64_t d = (int64_t)(b.lo() - a.lo()) % s;
+    if (d < 0) d += s;
+    return !(d >= a.span && d + b.span <= s);
+}
+
+// Whether the elements of an array with these sizes and strides (elements;
+// the innermost dimension has unit stride) have addresses of their own.
+template <int N>
+bool one_to_one(int64_t inner, const int64_t (&sizes)[N], const int64_t (&strides)[N]) {
+    int order[N];
+    for (int i = 0; i < N; ++i) order[i] = i;
+    std::sort(order, order + N, [&](int x, int y) { return strides[x] < strides[y]; });
+    __int128 span = inner;  // addresses the faster dimensions reach over
+    for (int k = 0; k < N; ++k) {
+        const int i = order[k];
+        if (sizes[i] < 2) continue;
+        if (strides[i] < span) return false;
+        span += (__int128)(sizes[i] - 1) * strides[i];
+    }
+    return true;
+}
+
+// The widest word (16, 8, 4 or 2 bytes, at least one element) that divides
+// every address, stride and length given in bytes.
+inline int word_bytes(int elem, std::initializer_list<uint64_t> all) {
+    uint64_t m = 16;
+    for (uint64_t v : all) m |= v;
+    const int w = (int)(m & (~m + 1));  // lowest set bit: at most 16
+    return w < elem ? elem : w;
+}
+
+inline bmmc_status all_reachable(std::initializer_list<const void*> ps) {
+    for (const void* p : ps)
+        if (p) {
+            const bmmc_status s = pointer_reachable(p);
+            if (s != BMMC_OK) return s;
+        }
+    return BMMC_OK;
+}
+
+inline bmmc_status launched() { return cudaGetLastError() == cudaSuccess ? BMMC_OK : BMMC_ERR_CUDA; }
+
+}  // namespace bmmc

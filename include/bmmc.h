@@ -50,12 +50,15 @@ typedef enum {
     BMMC_ERR_INVALID_ARG = 1,     /* n out of range, stray bits, null pointer, bad option */
     BMMC_ERR_SINGULAR = 2,        /* A is not invertible over F2: the map is no permutation */
     BMMC_ERR_UNSUPPORTED_ELEM = 3,/* elem_size not in {4, 8, 16} ({1, 2, 4, 8, 16} for
-                                     the LMAD copies) */
-    BMMC_ERR_MISALIGNED = 4,      /* a device pointer is not 16-byte aligned */
+                                     the LMAD copies), or an unknown type of the token
+                                     moves */
+    BMMC_ERR_MISALIGNED = 4,      /* a device pointer is not 16-byte aligned (LMAD copies and
+                                     token moves: not aligned to its element) */
     BMMC_ERR_ALIAS = 5,           /* in and out (or scratch) overlap */
     BMMC_ERR_CUDA = 6,            /* a CUDA runtime call or a launch failed */
     BMMC_ERR_TIMEOUT = 7,         /* a bounded device-side wait gave up */
-    BMMC_ERR_NO_SCRATCH = 8,      /* two-factor plan run without scratch memory */
+    BMMC_ERR_NO_SCRATCH = 8,      /* two-factor plan run without scratch memory, or a sort
+                                     without its workspace */
     BMMC_ERR_INTERNAL = 9,        /* a planner self-check failed (a bug; please report) */
     BMMC_ERR_TOO_LARGE = 10       /* array larger than BMMC_STATIC_SCRATCH_BYTES
                                      (bmmc_permute_static_scratch only) */
@@ -525,6 +528,150 @@ bmmc_status bmmc_parm_rows(int n, uint64_t mask, uint64_t *rows_out);
  * practical ceiling a permutation is measured against ("A kernel that is
  * correct", "The ceiling: a copy").  Pointers 16-byte aligned. */
 bmmc_status bmmc_copy(const void *in, void *out, size_t bytes, void *stream);
+
+/* ---- Moves of tokens by maps held on the device --------------------------------
+ * A decoder layer with experts moves the rows of its tokens by maps that are
+ * data: by expert and back, and into the pages of a cache.  The entry points
+ * below read those maps on the device; nothing is copied to the host.  Shared
+ * conventions:
+ *   - `type` is a bmmc_dtype; sums are held in 32 bits and every result is
+ *     rounded once, to nearest even.
+ *   - Strides are in elements of the array's type, >= 0 and at most 2^40; a
+ *     row's elements lie next to each other.  Rows of an input may share
+ *     memory (stride 0), elements of an output have addresses of their own.
+ *   - Pointers are reachable by the GPU as for bmmc_permute and aligned to
+ *     their element (MISALIGNED); 16-byte aligned rows are the fast case.
+ *   - What a map says is checked where it is used: an index outside its array
+ *     moves nothing and reads nothing out of range.
+ *   - Calls enqueue work on `stream`, allocate nothing, can be captured in a
+ *     CUDA graph, and give the same bits every time.
+ * Errors of all of them: INVALID_ARG (a null pointer, a size or stride out of
+ * range, an unknown flag), UNSUPPORTED_ELEM (an unknown type), MISALIGNED,
+ * ALIAS (an output may share bytes with an input or another output; slices
+ * of one array with a common row stride are told apart), CUDA. */
+typedef enum {
+    BMMC_F32 = 0,
+    BMMC_F16 = 1,
+    BMMC_BF16 = 2
+} bmmc_dtype;
+
+#define EXPERT_MAX_CHOICES 64
+
+/* Number the choices of a router by expert.  ids[t * choices + k] (dense,
+ * id_bytes 4 or 8, signed) is the expert of token t's choice k; an id outside
+ * [0, experts) is not routed.  Choices are numbered in the order of their
+ * experts and, for one expert, of t * choices + k; those not routed come
+ * behind all others.  For choice i = t * choices + k with number r:
+ *   slot[i]   = r, or ~r (negative) where the choice is not routed;
+ *   source[r] = i, or ~i (negative) where the choice is not routed;
+ *   offsets[e] = the number of routed choices of experts below e,
+ *                e = 0 .. experts: expert e has rows offsets[e] .. offsets[e+1]-1.
+ * slot and source hold tokens * choices entries, offsets experts + 1.
+ * workspace: what expert_sort_workspace asks for (host only; 0 for small
+ * calls), free to reuse once the call's work is done; NO_SCRATCH where it is
+ * missing.  choices <= EXPERT_MAX_CHOICES, experts <= 4096,
+ * tokens * choices < 2^31. */
+bmmc_status expert_sort_workspace(int64_t tokens, int choices, int experts, size_t *bytes);
+bmmc_status expert_sort(const void *ids, int id_bytes, int64_t tokens, int choices, int experts,
+                        int32_t *slot, int32_t *source, int32_t *offsets, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/* rows[slot[t,k]] = x[t] for every routed choice; the rows of choices that are
+ * not routed (rows[~slot[t,k]]) become zero, so that with n_rows = tokens *
+ * choices every row is written.  n_rows may be smaller: choices numbered
+ * n_rows and above are dropped.  slot is a permutation as expert_sort writes
+ * it (of other maps, rows named twice get one of their tokens and rows not
+ * named keep their contents). */
+bmmc_status expert_dispatch(const void *x, int64_t x_stride, const int32_t *slot, int64_t tokens,
+                            int choices, int64_t hidden, int type, void *rows,
+                            int64_t row_stride, int64_t n_rows, void *stream);
+
+/* out[t] = sum over token t's routed choices with slot[t,k] < n_rows, in the
+ * order of k, of weights[t,k] * rows[slot[t,k]]; zero where there are none.
+ * weights (dense [tokens][choices], of weight_type BMMC_F32 or `type`) NULL:
+ * the plain sum, which is the gradient of expert_dispatch by x. */
+bmmc_status expert_combine(const void *rows, int64_t row_stride, int64_t n_rows,
+                           const int32_t *slot, const void *weights, int weight_type,
+                           int64_t tokens, int choices, int64_t hidden, int type, void *out,
+                           int64_t out_stride, void *stream);
+
+/* The gradients of expert_combine, from grad = the gradient by out:
+ *   grad_rows[slot[t,k]]  = weights[t,k] * grad[t], zero in the rows of choices
+ *                           that are not routed (rows[~slot[t,k]]);
+ *   grad_weights[t,k]     = <rows[slot[t,k]], grad[t]>, zero where the choice is
+ *                           not routed or dropped; of weight_type, dense. */
+bmmc_status expert_combine_backward(const void *grad, int64_t grad_stride, const void *rows,
+                                    int64_t row_stride, int64_t n_rows, const int32_t *slot,
+                                    const void *weights, int weight_type, int64_t tokens,
+                                    int choices, int64_t hidden, int type, void *grad_rows,
+                                    int64_t grad_row_stride, void *grad_weights, void *stream);
+
+/* Heads of tokens: element d of head h of token t at
+ * data[t * token_stride + h * head_stride + d]. */
+typedef struct {
+    void *data;
+    int64_t heads, dim, token_stride, head_stride;
+} token_heads_t;
+
+#define ROTARY_MAX_DIM 8192
+#define ROTARY_ADJACENT 0x1  /* pair i is elements 2i, 2i+1 (else i, i + pairs) */
+#define ROTARY_INVERSE  0x2  /* turn by the opposite angles: the gradient */
+
+/* How heads are turned: pair i of the first 2 * pairs elements of a head by
+ * the angle position * inv_freq[i] (a product in 32 bits), position =
+ * positions[a * axis_stride + t] on the pair's axis a = pair_axes[i]:
+ *   (x, y) -> (x cos - y sin, y cos + x sin).
+ * The rest of a head is copied. */
+typedef struct {
+    const float *inv_freq;      /* [pairs]; NULL (with pairs 0): nothing is turned */
+    const int32_t *pair_axes;   /* [pairs], or NULL: axis 0; a pair whose axis is not
+                                   in [0, axes) is not turned */
+    const void *positions;      /* [axes][axis_stride] signed integers */
+    int64_t position_bytes;     /* 4 or 8 */
+    int64_t axes, axis_stride, pairs, flags;
+} rotary_turns_t;
+
+typedef struct {
+    int64_t tokens, type;
+    token_heads_t x, out;       /* out may be x itself (same data and strides) */
+    rotary_turns_t turns;
+} rotary_args_t;
+
+/* out = x turned by its tokens' positions.  heads * dim <= 2^24. */
+bmmc_status rotary(const rotary_args_t *args, void *stream);
+
+/* A cache of keys or values in pages: element d of head h of the entry `slot`
+ * of page p at data[p * page_stride + slot * slot_stride + h * head_stride + d]. */
+typedef struct {
+    void *data;
+    int64_t page_stride, slot_stride, head_stride;
+} paged_cache_t;
+
+typedef struct {
+    int64_t tokens, type;
+    token_heads_t k, v;          /* new keys and values, the same heads */
+    token_heads_t q, q_out;      /* queries turned with them; data NULL: none */
+    rotary_turns_t turns;        /* of k and q (positions NULL: a token's place in its
+                                    sequence, on axis 0); inverse turns are refused */
+    const int32_t *starts;       /* [sequences + 1]: sequence b has tokens starts[b] ..
+                                    starts[b+1]-1; NULL: token t is sequence t's only one */
+    const int32_t *lengths;      /* [sequences] entries cached before the call */
+    int64_t sequences;
+    const int32_t *table;        /* table[b * table_stride + c]: page of sequence b's
+                                    entries c * page_size .. (c + 1) * page_size - 1 */
+    int64_t table_stride, table_columns, pages, page_size;
+    paged_cache_t k_cache, v_cache;
+} paged_append_args_t;
+
+/* Append: the j-th new token of sequence b is its entry lengths[b] + j; its
+ * keys, turned, and its values are written to that entry's page, and q_out
+ * receives its queries, turned.  lengths is left as it is.  A token that
+ * belongs to no sequence (outside starts), or whose entry has no page (beyond
+ * the table, or a page outside [0, pages), as -1), is written to no cache; its
+ * queries are turned all the same (by its given position, or, without
+ * positions, by its place, which is 0 outside every sequence).  Two sequences
+ * must not name the same entry of a page for their new tokens. */
+bmmc_status paged_append(const paged_append_args_t *args, void *stream);
 
 /* ---- Bounds-checked builds --------------------------------------------------
  * A debugging build of the library (every source compiled with
