@@ -23,8 +23,8 @@ namespace {
 // ---- sort ------------------------------------------------------------------
 
 constexpr int kMaxExperts = 4096;
-constexpr int kSortRounds = 8;       // ids per lane and tile
-constexpr int kMaxSortBlocks = 64;   // blocks of a sort that one block does not cover
+constexpr int kSortRounds = 4;       // ids per lane and tile
+constexpr int kMaxSortBlocks = 152;  // blocks of a sort that one block does not cover: one for each SM
 
 template <class Id>
 __device__ __forceinline__ int key_of(Id id, int experts) {
@@ -61,18 +61,52 @@ __device__ void block_exclusive_scan(int* v, int n, int* tmp) {
     }
 }
 
-// counts[b][e] = choices of block b's part with key e (e = E: not routed).
+// counts[b][e] = choices of block b's part with key e (e = E: not routed);
+// the blocks' rows are `pitch` apart, a multiple of 4, zero past the keys.
 template <class Id>
 __global__ void __launch_bounds__(1024) sort_count_kernel(const Id* __restrict__ ids, int64_t n, int experts,
-                                                          int64_t per_block, int* __restrict__ counts) {
+                                                          int64_t per_block, int pitch, int* __restrict__ counts) {
     extern __shared__ int s_hist[];
-    const int keys = experts + 1;
-    for (int e = threadIdx.x; e < keys; e += blockDim.x) s_hist[e] = 0;
+    cudaTriggerProgrammaticLaunchCompletion();  // the place kernel may rank its first tile meanwhile
+    for (int e = threadIdx.x; e < pitch; e += blockDim.x) s_hist[e] = 0;
     __syncthreads();
     const int64_t lo = (int64_t)blockIdx.x * per_block, hi = min(n, lo + per_block);
-    for (int64_t i = lo + threadIdx.x; i < hi; i += blockDim.x) atomicAdd(&s_hist[key_of(ids[i], experts)], 1);
+    for (int64_t at = lo + threadIdx.x; at < hi; at += (int64_t)blockDim.x * kSortRounds) {
+        int key[kSortRounds];
+#pragma unroll
+        for (int r = 0; r < kSortRounds; ++r) {
+            const int64_t i = at + (int64_t)r * blockDim.x;
+            key[r] = i < hi ? key_of(ids[i], experts) : -1;
+        }
+#pragma unroll
+        for (int r = 0; r < kSortRounds; ++r)
+            if (key[r] >= 0) atomicAdd(&s_hist[key[r]], 1);
+    }
     __syncthreads();
-    for (int e = threadIdx.x; e < keys; e += blockDim.x) counts[(int64_t)blockIdx.x * keys + e] = s_hist[e];
+    for (int e = threadIdx.x; e < pitch; e += blockDim.x) counts[(int64_t)blockIdx.x * pitch + e] = s_hist[e];
+}
+
+// base[e] += the counts of key e over all blocks, before[e] += those over the
+// blocks ahead of this one (both zero in shared memory at the start): four
+// keys a load, the blocks dealt out to groups of threads.
+__device__ __forceinline__ void sum_counts(const int* counts, int pitch, int* base, int* before) {
+    const int quads = pitch >> 2, groups = max(1, (int)blockDim.x / quads);
+    for (int item = threadIdx.x; item < groups * quads; item += blockDim.x) {
+        const int q = item % quads, group = item / quads;
+        int4 all = make_int4(0, 0, 0, 0), ahead = all;
+#pragma unroll 8
+        for (int b = group; b < (int)gridDim.x; b += groups) {
+            const int4 c = __ldcg(reinterpret_cast<const int4*>(counts) + (int64_t)b * quads + q);
+            all.x += c.x, all.y += c.y, all.z += c.z, all.w += c.w;
+            if (b < (int)blockIdx.x) ahead.x += c.x, ahead.y += c.y, ahead.z += c.z, ahead.w += c.w;
+        }
+        const int a4[4] = {all.x, all.y, all.z, all.w}, b4[4] = {ahead.x, ahead.y, ahead.z, ahead.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            atomicAdd(&base[4 * q + i], a4[i]);
+            atomicAdd(&before[4 * q + i], b4[i]);
+        }
+    }
 }
 
 // Each block numbers its part, a tile of blockDim.x * R choices at a time.
@@ -80,49 +114,32 @@ __global__ void __launch_bounds__(1024) sort_count_kernel(const Id* __restrict__
 // 32 keys of a round plus the warp's running count of that key; a column sum
 // over the warps and the block's start for the key complete its place.  The
 // starts come from the counts of all blocks, or (counts == NULL: one block
-// and one tile) from the tile itself.  Integer sums in a fixed order: the
-// result does not depend on timing.
+// and one tile) from the tile itself.  Integer sums: the result does not
+// depend on timing.  The first tile is ranked before the counts are waited
+// for, so that this work runs beside the count kernel.
 template <class Id, int R>
 __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__ ids, int64_t n, int experts,
-                                                          int64_t per_block, const int* __restrict__ counts,
+                                                          int64_t per_block, int pitch, const int* counts,
                                                           int* __restrict__ slot, int* __restrict__ source,
                                                           int* __restrict__ offsets) {
     extern __shared__ int s_mem[];
     const int keys = experts + 1, warps = blockDim.x >> 5;
-    int* hist = s_mem;                // [warps][keys] counts of the tile, then starts inside it
-    int* base = hist + warps * keys;  // [keys] where the block's next choice of each key goes
-    int* total = base + keys;         // [keys] choices of the tile
-    int* tmp = total + keys;          // [32]
+    int* base = s_mem;          // [pitch] where the block's next choice of each key goes
+    int* total = base + pitch;  // [pitch] choices of the tile
+    int* tmp = total + pitch;   // [32]
+    int* hist = tmp + 32;       // [warps][keys] counts of the tile, then starts inside it
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int* mine = hist + warp * keys;
     const int64_t lo = (int64_t)blockIdx.x * per_block, hi = min(n, lo + per_block);
-    if (counts) {
-        for (int e = threadIdx.x; e < keys; e += blockDim.x) {
-            int all = 0, before = 0;
-            for (int b = 0; b < (int)gridDim.x; ++b) {
-                const int c = counts[(int64_t)b * keys + e];
-                all += c;
-                if (b < (int)blockIdx.x) before += c;
-            }
-            base[e] = all;
-            total[e] = before;
-        }
-        __syncthreads();
-        block_exclusive_scan(base, keys, tmp);
-        for (int e = threadIdx.x; e < keys; e += blockDim.x) {
-            if (blockIdx.x == 0) offsets[e] = base[e];
-            base[e] += total[e];
-        }
-    }
     int64_t at = lo;
     do {
-        for (int e = lane; e < keys; e += 32) mine[e] = 0;
         int key[R], rank[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int64_t i = at + ((int64_t)warp * R + r) * 32 + lane;
             key[r] = i < hi ? key_of(ids[i], experts) : -1;
         }
+        for (int e = lane; e < keys; e += 32) mine[e] = 0;
         __syncwarp();
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -132,6 +149,18 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__
             __syncwarp();
             if (key[r] >= 0 && lane == __ffs(same) - 1) mine[key[r]] = before + __popc(same);
             __syncwarp();
+        }
+        if (counts && at == lo) {
+            for (int e = threadIdx.x; e < pitch; e += blockDim.x) base[e] = total[e] = 0;
+            __syncthreads();
+            cudaGridDependencySynchronize();
+            sum_counts(counts, pitch, base, total);
+            __syncthreads();
+            block_exclusive_scan(base, keys, tmp);
+            for (int e = threadIdx.x; e < keys; e += blockDim.x) {
+                if (blockIdx.x == 0) offsets[e] = base[e];
+                base[e] += total[e];
+            }
         }
         __syncthreads();
         for (int e = threadIdx.x; e < keys; e += blockDim.x) {
@@ -158,125 +187,194 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__
             slot[i] = routed ? to : ~to;
             if ((unsigned)to < (unsigned)n) source[to] = routed ? (int)i : ~(int)i;  // also if ids changed meanwhile
         }
+        at += (int64_t)blockDim.x * R;
+        if (at >= hi) break;
         __syncthreads();
         for (int e = threadIdx.x; e < keys; e += blockDim.x) base[e] += total[e];
-        at += (int64_t)blockDim.x * R;
-    } while (at < hi);
+    } while (true);
 }
 
 struct SortShape {
-    int warps, blocks;
+    int warps, blocks, rounds, pitch;
     int64_t per_block;
     size_t smem;  // of the place kernel
 };
 
-// One block where one tile covers all choices, else at most kMaxSortBlocks
-// blocks of whole tiles.  A block has as many warps as their counts of every
-// key leave room for in shared memory.
+constexpr size_t kSortSmem = 200 * 1024;
+
+// One block where one tile covers all choices (of one round a warp where that
+// is enough), else at most kMaxSortBlocks blocks of whole tiles.  A block has
+// as many warps as their counts of every key leave room for.
 SortShape sort_shape(int64_t n, int experts) {
-    const int keys = experts + 1;
     SortShape s;
+    s.pitch = (experts + 4) & ~3;
+    const auto smem = [&](int warps) { return ((size_t)warps * (experts + 1) + 2 * s.pitch + 32) * sizeof(int); };
     s.warps = 32;
-    while (s.warps > 1 && (size_t)(s.warps + 2) * keys * 4 + 128 > (size_t)200 * 1024) s.warps >>= 1;
-    const int64_t tile = (int64_t)s.warps * 32 * kSortRounds;
+    while (smem(s.warps) > kSortSmem) s.warps >>= 1;
+    s.rounds = n <= s.warps * 32 ? 1 : kSortRounds;
+    const int64_t tile = (int64_t)s.warps * 32 * s.rounds;
     const int64_t tiles = n <= tile ? 1 : (n + tile - 1) / tile;
     const int64_t per = (tiles + kMaxSortBlocks - 1) / kMaxSortBlocks;
     s.per_block = per * tile;
     s.blocks = (int)((tiles + per - 1) / per);
-    s.smem = (size_t)(s.warps + 2) * keys * 4 + 128;
+    if (s.blocks == 1) s.warps = n < 32 ? 1 : (int)((n + 32 * s.rounds - 1) / (32 * s.rounds));
+    s.smem = smem(s.warps);
     return s;
 }
 
-template <class Id>
-bmmc_status launch_sort(const void* ids, int64_t n, int experts, int32_t* slot, int32_t* source, int32_t* offsets,
-                        int* counts, cudaStream_t st) {
-    const SortShape s = sort_shape(n, experts);
-    const auto place = sort_place_kernel<Id, kSortRounds>;
-    if (cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024 + 128) != cudaSuccess) {
+template <class Id, int R>
+bmmc_status launch_sort(const SortShape& s, const void* ids_, int64_t n, int experts, int32_t* slot, int32_t* source,
+                        int32_t* offsets, int* counts, cudaStream_t st) {
+    const Id* ids = static_cast<const Id*>(ids_);
+    const auto place = sort_place_kernel<Id, R>;
+    if (s.smem > 48 * 1024 &&
+        cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSortSmem) != cudaSuccess) {
         cudaGetLastError();
         return BMMC_ERR_CUDA;
     }
-    if (s.blocks == 1) counts = nullptr;
-    if (counts) {
-        sort_count_kernel<Id><<<s.blocks, 1024, (size_t)(experts + 1) * 4, st>>>(static_cast<const Id*>(ids), n, experts,
-                                                                                s.per_block, counts);
-        if (launched() != BMMC_OK) return BMMC_ERR_CUDA;
+    const int* none = nullptr;
+    if (s.blocks == 1) {
+        place<<<1, s.warps * 32, s.smem, st>>>(ids, n, experts, s.per_block, s.pitch, none, slot, source, offsets);
+        return launched();
     }
-    place<<<s.blocks, s.warps * 32, s.smem, st>>>(static_cast<const Id*>(ids), n, experts, s.per_block, counts, slot,
-                                                 source, offsets);
-    return launched();
+    sort_count_kernel<Id><<<s.blocks, 1024, s.pitch * sizeof(int), st>>>(ids, n, experts, s.per_block, s.pitch, counts);
+    if (launched() != BMMC_OK) return BMMC_ERR_CUDA;
+    cudaLaunchAttribute early[1];
+    early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(s.blocks);
+    cfg.blockDim = dim3(s.warps * 32);
+    cfg.dynamicSmemBytes = s.smem;
+    cfg.stream = st;
+    cfg.attrs = early;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, place, ids, n, experts, s.per_block, s.pitch, (const int*)counts, slot, source,
+                           offsets) != cudaSuccess) {
+        cudaGetLastError();
+        return BMMC_ERR_CUDA;
+    }
+    return BMMC_OK;
 }
 
 // ---- dispatch ----------------------------------------------------------------
 
-// A block of tx x ty threads takes ty tokens; tx threads walk a token's row.
-dim3 token_block(int words) {
-    int tx = 32;
-    while (tx < words && tx < 256) tx <<= 1;
-    return dim3(tx, 256 / tx);
+// How the words of the tokens' rows are dealt out: blocks of x * y threads
+// take y tokens and x * U words of each, U words a thread, x apart; gridDim.y
+// parts make up a row.
+struct Cover {
+    dim3 grid, block;
+};
+
+Cover cover(int64_t tokens, int words, int U, int most) {
+    const int need = (words + U - 1) / U;  // threads of a row
+    const int parts = (need + most - 1) / most;
+    const int x = ((need + parts - 1) / parts + 31) / 32 * 32;
+    const int y = x >= most ? 1 : most / x;
+    Cover c;
+    c.block = dim3(x, y);
+    c.grid = dim3((unsigned)((tokens + y - 1) / y), (unsigned)((words + x * U - 1) / (x * U)));
+    return c;
 }
 
-unsigned token_grid(int64_t tokens, dim3 block) { return (unsigned)((tokens + block.y - 1) / block.y); }
+// Fewer words than this many: one word a thread, so that the call is spread
+// over the machine and every load is in flight at once.
+constexpr int64_t kFewWords = 152 * 2048;
 
 // Pure movement: each word of a token's row is read once and written to the
 // rows of its choices.
-template <class Word>
+template <class Word, int U>
 __global__ void __launch_bounds__(256) dispatch_kernel(const char* __restrict__ x, int64_t x_stride,
                                                        const int* __restrict__ slot, int64_t tokens, int choices,
                                                        int64_t n_rows, int words, char* __restrict__ rows,
                                                        int64_t row_stride) {
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    if (t >= tokens) return;
+    const int w = blockIdx.y * blockDim.x * U + threadIdx.x;
+    if (t >= tokens || w >= words) return;
     const Word* from = reinterpret_cast<const Word*>(x + t * x_stride);
-    for (int w = threadIdx.x; w < words; w += blockDim.x) {
-        const Word v = from[w];
-        for (int k = 0; k < choices; ++k) {
-            const int s = slot[t * choices + k];
-            const int64_t row = s < 0 ? ~s : s;
-            if (row < n_rows) reinterpret_cast<Word*>(rows + row * row_stride)[w] = s < 0 ? Word{} : v;
-        }
+    Word v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (w + u * (int)blockDim.x < words) v[u] = from[w + u * blockDim.x];
+    slot += t * choices;
+#pragma unroll 4
+    for (int k = 0; k < choices; ++k) {
+        const int s = __ldg(slot + k);
+        const int64_t row = s < 0 ? ~s : s;
+        if (row >= n_rows) continue;
+        Word* to = reinterpret_cast<Word*>(rows + row * row_stride);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (w + u * (int)blockDim.x < words) to[w + u * blockDim.x] = s < 0 ? Word{} : v[u];
     }
 }
 
 // ---- combine -----------------------------------------------------------------
 
-// Each thread holds W sums in 32 bits, adds the choices in order and rounds
-// once.
-template <class T, class Wt, int W>
+// A weight of the rows' type or of 32 bits.
+template <class T>
+__device__ __forceinline__ float weight_at(const void* weights, int in_f32, int64_t i) {
+    return in_f32 ? static_cast<const float*>(weights)[i] : to_f32(static_cast<const T*>(weights)[i]);
+}
+
+// Each thread holds the sums of U words in 32 bits, adds the choices in order,
+// KB of them loaded at a time, and rounds once.
+template <class T, int W, int U, int KB>
 __global__ void __launch_bounds__(256) combine_kernel(const char* __restrict__ rows, int64_t row_stride, int64_t n_rows,
-                                                      const int* __restrict__ slot, const Wt* __restrict__ weights,
-                                                      int64_t tokens, int choices, int words, char* __restrict__ out,
-                                                      int64_t out_stride) {
+                                                      const int* __restrict__ slot, const void* __restrict__ weights,
+                                                      int weights_f32, int64_t tokens, int choices, int words,
+                                                      char* __restrict__ out, int64_t out_stride) {
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    if (t >= tokens) return;
-    for (int w = threadIdx.x; w < words; w += blockDim.x) {
-        float sum[W];
+    const int w = blockIdx.y * blockDim.x * U + threadIdx.x;
+    if (t >= tokens || w >= words) return;
+    float sum[U][W];
 #pragma unroll
-        for (int i = 0; i < W; ++i) sum[i] = 0.0f;
-        for (int k = 0; k < choices; ++k) {
-            const int s = slot[t * choices + k];
-            if (s < 0 || s >= n_rows) continue;
-            Pack<T, W> y;
-            y.load(rows + s * row_stride + (int64_t)w * sizeof(y));
-            const float f = weights ? to_f32(weights[t * choices + k]) : 1.0f;
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < W; ++i) sum[i] = fmaf(f, y.get(i), sum[i]);
+        for (int i = 0; i < W; ++i) sum[u][i] = 0.0f;
+    for (int k0 = 0; k0 < choices; k0 += KB) {
+        int s[KB];
+        float f[KB];
+        Pack<T, W> y[KB][U];
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+            s[j] = k0 + j < choices ? slot[t * choices + k0 + j] : -1;
+            if (s[j] >= n_rows) s[j] = -1;
         }
-        Pack<T, W> o;
 #pragma unroll
-        for (int i = 0; i < W; ++i) o.set(i, sum[i]);
-        o.store(out + t * out_stride + (int64_t)w * sizeof(o));
+        for (int j = 0; j < KB; ++j) {
+            f[j] = 1.0f;
+            if (weights && s[j] >= 0) f[j] = weight_at<T>(weights, weights_f32, t * choices + k0 + j);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (s[j] >= 0 && w + u * (int)blockDim.x < words)
+                    y[j][u].load(rows + s[j] * row_stride + (int64_t)(w + u * (int)blockDim.x) * sizeof(y[j][u]));
+        }
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+            if (s[j] >= 0)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < W; ++i) sum[u][i] = fmaf(f[j], y[j][u].get(i), sum[u][i]);
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (w + u * (int)blockDim.x < words) {
+            Pack<T, W> o;
+            o.set(sum[u]);
+            o.store(out + t * out_stride + (int64_t)(w + u * (int)blockDim.x) * sizeof(o));
+        }
 }
 
 // grad_rows[slot] = w * grad and grad_weights = <rows[slot], grad>, a choice
 // after the other; the products are summed in 32 bits, by lanes and then
 // across them in a fixed order.
-template <class T, class Wt, int W>
+template <class T, int W>
 __global__ void __launch_bounds__(256) combine_backward_kernel(
     const char* __restrict__ grad, int64_t grad_stride, const char* __restrict__ rows, int64_t row_stride,
-    int64_t n_rows, const int* __restrict__ slot, const Wt* __restrict__ weights, int64_t tokens, int choices,
-    int words, char* __restrict__ grad_rows, int64_t grad_row_stride, Wt* __restrict__ grad_weights) {
+    int64_t n_rows, const int* __restrict__ slot, const void* __restrict__ weights, int weights_f32, int64_t tokens,
+    int choices, int words, char* __restrict__ grad_rows, int64_t grad_row_stride, void* __restrict__ grad_weights) {
     __shared__ float s_part[8];
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const bool live = t < tokens;
@@ -287,22 +385,24 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(
         if (live) {
             const int s = slot[t * choices + k];
             const int64_t row = s < 0 ? ~s : s;
-            const float f = s < 0 ? 0.0f : to_f32(weights[t * choices + k]);
+            const float f = s < 0 ? 0.0f : weight_at<T>(weights, weights_f32, t * choices + k);
             if (row < n_rows)
                 for (int w = threadIdx.x; w < words; w += blockDim.x) {
                     Pack<T, W> g, y, o;
+                    float v[W];
                     g.load(grad + t * grad_stride + (int64_t)w * sizeof(g));
                     if (s >= 0) {
                         y.load(rows + row * row_stride + (int64_t)w * sizeof(y));
 #pragma unroll
                         for (int i = 0; i < W; ++i) {
                             dot = fmaf(g.get(i), y.get(i), dot);
-                            o.set(i, f * g.get(i));
+                            v[i] = f * g.get(i);
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < W; ++i) o.set(i, 0.0f);
+                        for (int i = 0; i < W; ++i) v[i] = 0.0f;
                     }
+                    o.set(v);
                     o.store(grad_rows + row * grad_row_stride + (int64_t)w * sizeof(o));
                 }
         }
@@ -312,27 +412,23 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(
         if (live && threadIdx.x == 0) {
             float sum = 0.0f;
             for (int i = 0; i < per; ++i) sum += s_part[warp + i];
-            grad_weights[t * choices + k] = from_f32<Wt>(sum);
+            if (weights_f32) static_cast<float*>(grad_weights)[t * choices + k] = sum;
+            else static_cast<T*>(grad_weights)[t * choices + k] = from_f32<T>(sum);
         }
         __syncthreads();
     }
 }
 
-// Calls f(T{}, weight type{}, elements per word) for the types and width.
+// Calls f(T{}, elements per word) for the type and the word's width.
 template <class F>
-void by_type(int type, int wtype, int bytes, F&& f) {
-    auto weight = [&](auto t, auto w) {
-        using T = decltype(t);
-        if (wtype == type) f(t, T{}, w);
-        else f(t, float{}, w);
-    };
+void by_type(int type, int bytes, F&& f) {
     auto width = [&](auto t) {
         constexpr int es = sizeof(t);
         switch (bytes) {
-            case 16: weight(t, std::integral_constant<int, 16 / es>{}); break;
-            case 8: weight(t, std::integral_constant<int, 8 / es>{}); break;
-            case 4: weight(t, std::integral_constant<int, 4 / es>{}); break;
-            default: weight(t, std::integral_constant<int, 1>{}); break;
+            case 16: f(t, std::integral_constant<int, 16 / es>{}); break;
+            case 8: f(t, std::integral_constant<int, 8 / es>{}); break;
+            case 4: f(t, std::integral_constant<int, 4 / es>{}); break;
+            default: f(t, std::integral_constant<int, 1>{}); break;
         }
     };
     switch (type) {
@@ -367,7 +463,7 @@ bmmc_status expert_sort_workspace(int64_t tokens, int choices, int experts, size
         experts > kMaxExperts)
         return BMMC_ERR_INVALID_ARG;
     const SortShape s = sort_shape(tokens * choices, experts);
-    *bytes = s.blocks > 1 ? (size_t)s.blocks * (experts + 1) * sizeof(int) : 0;
+    *bytes = s.blocks > 1 ? (size_t)s.blocks * s.pitch * sizeof(int) : 0;
     return BMMC_OK;
 }
 
@@ -381,7 +477,7 @@ bmmc_status expert_sort(const void* ids, int id_bytes, int64_t tokens, int choic
     if (!offsets || (n && (!ids || !slot || !source))) return BMMC_ERR_INVALID_ARG;
     if (need && (!workspace || workspace_bytes < need)) return BMMC_ERR_NO_SCRATCH;
     if (misaligned(ids, id_bytes) || misaligned(slot, 4) || misaligned(source, 4) || misaligned(offsets, 4) ||
-        (need && misaligned(workspace, 4)))
+        (need && misaligned(workspace, 16)))
         return BMMC_ERR_MISALIGNED;
     const Rows in{ids, 1, 0, n * id_bytes};
     const Rows o[4] = {{slot, 1, 0, n * 4}, {source, 1, 0, n * 4}, {offsets, 1, 0, (experts + 1) * 4ll},
@@ -394,8 +490,10 @@ bmmc_status expert_sort(const void* ids, int id_bytes, int64_t tokens, int choic
     if ((s = all_reachable({ids, slot, source, offsets, need ? workspace : nullptr})) != BMMC_OK) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int* counts = static_cast<int*>(need ? workspace : nullptr);
-    return id_bytes == 4 ? launch_sort<int32_t>(ids, n, experts, slot, source, offsets, counts, st)
-                         : launch_sort<int64_t>(ids, n, experts, slot, source, offsets, counts, st);
+    const SortShape shape = sort_shape(n, experts);
+    const auto go = [&](auto launch) { return launch(shape, ids, n, experts, slot, source, offsets, counts, st); };
+    if (id_bytes == 4) return shape.rounds == 1 ? go(launch_sort<int32_t, 1>) : go(launch_sort<int32_t, kSortRounds>);
+    return shape.rounds == 1 ? go(launch_sort<int64_t, 1>) : go(launch_sort<int64_t, kSortRounds>);
 }
 
 bmmc_status expert_dispatch(const void* x, int64_t x_stride, const int32_t* slot, int64_t tokens, int choices,
@@ -413,14 +511,15 @@ bmmc_status expert_dispatch(const void* x, int64_t x_stride, const int32_t* slot
     const int wb = word_bytes(es, {(uint64_t)(uintptr_t)x, (uint64_t)(uintptr_t)rows, (uint64_t)(x_stride * es),
                                    (uint64_t)(row_stride * es), (uint64_t)(hidden * es)});
     const int words = (int)(hidden * es / wb);
-    const dim3 block = token_block(words);
-    const unsigned grid = token_grid(tokens, block);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const char* from = static_cast<const char*>(x);
     char* to = static_cast<char*>(rows);
     auto go = [&](auto word) {
-        dispatch_kernel<decltype(word)><<<grid, block, 0, st>>>(from, x_stride * es, slot, tokens, choices, n_rows, words,
-                                                                to, row_stride * es);
+        using Word = decltype(word);
+        const bool few = tokens * words <= kFewWords;
+        const Cover c = few ? cover(tokens, words, 1, 128) : cover(tokens, words, 2, 256);
+        const auto kernel = few ? dispatch_kernel<Word, 1> : dispatch_kernel<Word, 2>;
+        kernel<<<c.grid, c.block, 0, st>>>(from, x_stride * es, slot, tokens, choices, n_rows, words, to, row_stride * es);
     };
     switch (wb) {
         case 16: go(uint4{}); break;
@@ -452,15 +551,16 @@ bmmc_status expert_combine(const void* rows, int64_t row_stride, int64_t n_rows,
     const int wb = word_bytes(es, {(uint64_t)(uintptr_t)rows, (uint64_t)(uintptr_t)out, (uint64_t)(row_stride * es),
                                    (uint64_t)(out_stride * es), (uint64_t)(hidden * es)});
     const int words = (int)(hidden * es / wb);
-    const dim3 block = token_block(words);
-    const unsigned grid = token_grid(tokens, block);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    by_type(type, weights ? weight_type : type, wb, [&](auto t, auto wt, auto w) {
-        using T = decltype(t);
-        using Wt = decltype(wt);
-        combine_kernel<T, Wt, decltype(w)::value><<<grid, block, 0, st>>>(
-            static_cast<const char*>(rows), row_stride * es, n_rows, slot, static_cast<const Wt*>(weights), tokens,
-            choices, words, static_cast<char*>(out), out_stride * es);
+    by_type(type, wb, [&](auto e, auto width) {
+        using T = decltype(e);
+        constexpr int W = decltype(width)::value;
+        const bool few = tokens * words <= kFewWords, two = choices <= 2;
+        const Cover c = few ? cover(tokens, words, 1, 128) : two ? cover(tokens, words, 4, 256) : cover(tokens, words, 2, 256);
+        const auto kernel = few ? combine_kernel<T, W, 1, 8> : two ? combine_kernel<T, W, 4, 2> : combine_kernel<T, W, 2, 4>;
+        kernel<<<c.grid, c.block, 0, st>>>(static_cast<const char*>(rows), row_stride * es, n_rows, slot, weights,
+                                          weight_type == BMMC_F32, tokens, choices, words, static_cast<char*>(out),
+                                          out_stride * es);
     });
     return launched();
 }
@@ -494,16 +594,16 @@ bmmc_status expert_combine_backward(const void* grad, int64_t grad_stride, const
                                    (uint64_t)(grad_stride * es), (uint64_t)(row_stride * es),
                                    (uint64_t)(grad_row_stride * es), (uint64_t)(hidden * es)});
     const int words = (int)(hidden * es / wb);
-    const dim3 block = token_block(words);
-    const unsigned grid = token_grid(tokens, block);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    by_type(type, weight_type, wb, [&](auto t, auto wt, auto w) {
-        using T = decltype(t);
-        using Wt = decltype(wt);
-        combine_backward_kernel<T, Wt, decltype(w)::value><<<grid, block, 0, st>>>(
+    int x = 32;
+    while (x < words && x < 256) x <<= 1;
+    const dim3 block(x, 256 / x);
+    const unsigned blocks = (unsigned)((tokens + block.y - 1) / block.y);
+    by_type(type, wb, [&](auto e, auto width) {
+        combine_backward_kernel<decltype(e), decltype(width)::value><<<blocks, block, 0, st>>>(
             static_cast<const char*>(grad), grad_stride * es, static_cast<const char*>(rows), row_stride * es, n_rows,
-            slot, static_cast<const Wt*>(weights), tokens, choices, words, static_cast<char*>(grad_rows),
-            grad_row_stride * es, static_cast<Wt*>(grad_weights));
+            slot, weights, weight_type == BMMC_F32, tokens, choices, words, static_cast<char*>(grad_rows),
+            grad_row_stride * es, grad_weights);
     });
     return launched();
 }

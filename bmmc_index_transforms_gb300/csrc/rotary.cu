@@ -9,7 +9,9 @@
 // model sees whose positions are turned in 32 bits.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
+#include <cstdlib>
 #include <type_traits>
 
 #include "../../include/bmmc.h"
@@ -20,8 +22,8 @@ using namespace bmmc;
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxTokensPerBlock = 8;
+constexpr int kThreads = 256;           // most threads of a block
+constexpr int kMaxTokensPerBlock = 64;
 
 // Heads of one kind (queries, keys, values): where they lie and where they
 // go.  Strides in bytes.  place: 0 = the token's own place (dst_token apart),
@@ -30,14 +32,16 @@ struct Heads {
     const char* src;
     char* dst;
     int64_t src_token, src_head, dst_token, dst_head;
-    int heads, dim, turned, place;
+    int heads, turned, place;
+    int turning, items;  // words of a head that are turned (pairs of words in halves), and all
+    int across, magic;   // threads side by side on a head's words, and 65536 / across rounded up
 };
 
 struct MoveParams {
     Heads part[3];
     int parts;
     int64_t tokens;
-    int per_block;  // tokens of one block
+    int group_log2;  // threads of a token
     // rotation
     const void* positions;  // NULL: the token's place in its sequence
     int position_bytes, axes, pairs;
@@ -45,17 +49,17 @@ struct MoveParams {
     const float* freq;
     const int* pair_axes;  // NULL: axis 0
     float sign;
-    // places in the cache
+    // places in the cache; page_size 0: there is none
     const int *starts, *lengths, *table;
     int64_t sequences, table_stride, table_columns, pages;
     int page_size;
     int64_t page_stride[2], slot_stride[2];  // of the key and the value cache, bytes
 };
 
-// The last sequence whose start is <= t, by a whole warp, 32 starts at a
-// time; -1 if there is none.  Any starts, in order or not, give an index in
-// range.
-__device__ int64_t find_sequence(const int* starts, int64_t sequences, int64_t t, int lane) {
+// The last sequence whose start is <= t, -1 if there is none: by a whole
+// warp, 32 starts at a time, and by one thread.  Any starts, in order or not,
+// give an index in range.
+__device__ int64_t find_sequence_warp(const int* starts, int64_t sequences, int64_t t, int lane) {
     int64_t lo = 0, n = sequences;  // the answer lies in [lo, lo + n) or is lo - 1
     while (n > 0) {
         const int64_t step = (n + 31) / 32;
@@ -71,49 +75,75 @@ __device__ int64_t find_sequence(const int* starts, int64_t sequences, int64_t t
     return lo - 1;
 }
 
+__device__ int64_t find_sequence(const int* starts, int64_t sequences, int64_t t) {
+    int64_t lo = 0, hi = sequences;  // starts[lo - 1] <= t, starts[hi] > t
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (starts[mid] <= t) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo - 1;
+}
+
+// Token t's position in its sequence b and its byte offsets in the caches.
+struct Place {
+    int64_t at;       // 0 outside every sequence
+    int64_t byte[2];  // -1: no page
+};
+
+__device__ Place place_of(const MoveParams& p, int64_t t, int64_t b) {
+    Place r{0, {-1, -1}};
+    int64_t first = t;
+    if (p.starts) {
+        if (b < 0 || t >= p.starts[b + 1]) return r;
+        first = p.starts[b];
+    } else if (t >= p.sequences) {
+        return r;
+    }
+    r.at = (int64_t)p.lengths[b] + (t - first);
+    if (r.at < 0 || r.at >= (int64_t)1 << 32) return r;  // (more only by starts below zero)
+    const unsigned at = (unsigned)r.at, column = at / p.page_size;
+    if (column >= p.table_columns) return r;
+    const int page = p.table[b * p.table_stride + column];
+    if (page < 0 || page >= p.pages) return r;
+    for (int c = 0; c < 2; ++c)
+        r.byte[c] = page * p.page_stride[c] + (int64_t)(at - column * p.page_size) * p.slot_stride[c];
+    return r;
+}
+
 // Written out, so that every variant rounds alike.
 __device__ __forceinline__ float turned_first(float x, float y, float2 r) { return fmaf(x, r.x, -__fmul_rn(y, r.y)); }
 __device__ __forceinline__ float turned_second(float x, float y, float2 r) { return fmaf(y, r.x, __fmul_rn(x, r.y)); }
 
+// A block takes some tokens, a group of threads each.  Its threads find the
+// tokens' places and put the cosines and sines of their pairs into shared
+// memory, once for all heads; then a thread keeps those of its word of a head
+// in registers and walks over the heads, two at a time.
 template <class T, int W, bool ADJACENT>
-__global__ void __launch_bounds__(kThreads) move_heads_kernel(const __grid_constant__ MoveParams p) {
-    extern __shared__ float2 s_turn[];  // [per_block][pairs] cos, sin
+__global__ void __launch_bounds__(kThreads, 4) move_heads_kernel(const __grid_constant__ MoveParams p) {
+    extern __shared__ float2 s_turn[];  // [tokens of the block][pairs] cos, sin
     __shared__ int64_t s_place[2][kMaxTokensPerBlock];  // byte offsets in the caches, -1 = none
     __shared__ float s_position[kMaxTokensPerBlock];
-    const int64_t t0 = (int64_t)blockIdx.x * p.per_block;
-    const int nt = (int)min((int64_t)p.per_block, p.tokens - t0);
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x, threads = blockDim.x, per_block = threads >> p.group_log2;
+    const int64_t t0 = (int64_t)blockIdx.x * per_block;
+    const int nt = (int)min((int64_t)per_block, p.tokens - t0);
+    // a block of a small call takes one part only
+    const int first_part = gridDim.y > 1 ? blockIdx.y : 0, last_part = gridDim.y > 1 ? first_part + 1 : p.parts;
     if (p.page_size) {
-        for (int i = tid >> 5; i < nt; i += kThreads / 32) {
-            const int64_t t = t0 + i;
-            int64_t b = t, first = t;
-            if (p.starts) {
-                b = find_sequence(p.starts, p.sequences, t, lane);
-                if (b >= 0) {
-                    first = p.starts[b];
-                    if (t >= p.starts[b + 1]) b = -1;
-                }
-            } else if (t >= p.sequences) {
-                b = -1;
+        if (p.starts && per_block <= 8) {
+            for (int i = tid >> 5; i < nt; i += threads >> 5) {
+                const Place r = place_of(p, t0 + i, find_sequence_warp(p.starts, p.sequences, t0 + i, tid & 31));
+                if ((tid & 31) == 0) s_place[0][i] = r.byte[0], s_place[1][i] = r.byte[1], s_position[i] = (float)r.at;
             }
-            int64_t at = 0, page = -1;
-            if (b >= 0) {
-                at = (int64_t)p.lengths[b] + (t - first);
-                const int64_t column = at / p.page_size;
-                if (at >= 0 && column < p.table_columns) page = p.table[b * p.table_stride + column];
-            }
-            if (lane == 0) {
-                const bool in = page >= 0 && page < p.pages;
-                const int64_t row = at % p.page_size;
-                for (int c = 0; c < 2; ++c)
-                    s_place[c][i] = in ? page * p.page_stride[c] + row * p.slot_stride[c] : -1;
-                s_position[i] = (float)at;
-            }
+        } else if (tid < nt) {
+            const int64_t t = t0 + tid;
+            const Place r = place_of(p, t, p.starts ? find_sequence(p.starts, p.sequences, t) : t);
+            s_place[0][tid] = r.byte[0], s_place[1][tid] = r.byte[1], s_position[tid] = (float)r.at;
         }
         __syncthreads();
     }
-    if (p.pairs) {
-        for (int i = tid; i < nt * p.pairs; i += kThreads) {
+    if (p.pairs && p.part[first_part].turned) {
+        for (int i = tid; i < nt * p.pairs; i += threads) {
             const int k = i / p.pairs, pair = i - k * p.pairs;
             const int axis = p.pair_axes ? p.pair_axes[pair] : 0;
             float at = 0.0f;  // an axis that is not there does not turn
@@ -130,97 +160,135 @@ __global__ void __launch_bounds__(kThreads) move_heads_kernel(const __grid_const
         }
         __syncthreads();
     }
-    for (int q = 0; q < p.parts; ++q) {
-        const Heads h = p.part[q];
-        const int pairs = h.turned ? p.pairs : 0;
-        // items of a head: first those that turn (W pairs in halves, or W / 2
-        // pairs side by side, at least one), then W elements each that are copied
-        const int turning = !ADJACENT ? pairs / W : W > 1 ? 2 * pairs / W : pairs;
-        const int per_head = turning + (h.dim - 2 * pairs) / W;
-        for (int idx = tid; idx < nt * h.heads * per_head; idx += kThreads) {
-            const int k = idx / (h.heads * per_head), in = idx - k * (h.heads * per_head);
-            const int head = in / per_head, j = in - head * per_head;
-            int64_t to = (t0 + k) * h.dst_token;
-            if (h.place) {
-                to = s_place[h.place - 1][k];
-                if (to < 0) continue;
-            }
-            const char* src = h.src + (t0 + k) * h.src_token + head * h.src_head;
-            char* dst = h.dst + to + head * h.dst_head;
-            Pack<T, W> a, b;
-            if (j >= turning) {
-                const int64_t at = (int64_t)(2 * pairs + (j - turning) * W) * sizeof(T);
-                a.load(src + at);
-                a.store(dst + at);
-            } else if (ADJACENT && W > 1) {
-                const int64_t at = (int64_t)j * sizeof(a);
-                a.load(src + at);
-#pragma unroll
-                for (int i = 0; i + 1 < W; i += 2) {
-                    const float2 r = s_turn[k * p.pairs + (j * W + i) / 2];
-                    const float x = a.get(i), y = a.get(i + 1);
-                    a.set(i, turned_first(x, y, r));
-                    a.set(i + 1, turned_second(x, y, r));
-                }
-                a.store(dst + at);
+    const int k = tid >> p.group_log2, in = tid & ((1 << p.group_log2) - 1);
+    if (k >= nt) return;
+    for (int q = first_part; q < last_part; ++q) {
+        const Heads& h = p.part[q];
+        const int down = (in * h.magic) >> 16, step = (1 << p.group_log2) / h.across;
+        if (down >= step) continue;
+        int64_t to = (t0 + k) * h.dst_token;
+        if (h.place) {
+            to = s_place[h.place - 1][k];
+            if (to < 0) continue;
+        }
+        const char* const src = h.src + (t0 + k) * h.src_token;
+        char* const dst = h.dst + to;
+        const float2* const turn = s_turn + k * p.pairs;
+        for (int j = in - down * h.across; j < h.items; j += h.across) {
+            const bool turned = j < h.turning;
+            // where the word lies, and its other half
+            int64_t at, half = 0;
+            if (ADJACENT) {
+                at = W > 1 ? (int64_t)j * W : turned ? 2 * j : j + h.turning;
+                half = 1;
             } else {
-                const int64_t at = (int64_t)(ADJACENT ? 2 * j : j * W) * sizeof(T);
-                const int64_t half = (int64_t)(ADJACENT ? 1 : pairs) * sizeof(T);
-                a.load(src + at);
-                b.load(src + at + half);
+                at = turned ? (int64_t)j * W : (int64_t)(j + h.turning) * W;
+                half = p.pairs;
+            }
+            at *= sizeof(T), half *= sizeof(T);
+            constexpr bool kTwo = !ADJACENT || W == 1;  // an item has two words
+            constexpr int kTurns = kTwo ? W : W / 2;
+            float2 r[kTurns];
+            if (turned)
 #pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    const float2 r = s_turn[k * p.pairs + j * W + i];
-                    const float x = a.get(i), y = b.get(i);
-                    a.set(i, turned_first(x, y, r));
-                    b.set(i, turned_second(x, y, r));
-                }
-                a.store(dst + at);
-                b.store(dst + at + half);
+                for (int i = 0; i < kTurns; ++i) r[i] = turn[j * kTurns + i];
+            for (int head = down; head < h.heads; head += 2 * step) {
+                const bool both = head + step < h.heads;
+                Pack<T, W> a[2], b[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    if (u == 0 || both) {
+                        const char* from = src + (head + u * step) * h.src_head + at;
+                        a[u].load(from);
+                        if (kTwo && turned) b[u].load(from + half);
+                    }
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    if (u == 0 || both) {
+                        char* out = dst + (head + u * step) * h.dst_head + at;
+                        if (turned) {
+                            float x[W], y[W];
+                            if constexpr (kTwo) {
+#pragma unroll
+                                for (int i = 0; i < W; ++i) {
+                                    x[i] = turned_first(a[u].get(i), b[u].get(i), r[i]);
+                                    y[i] = turned_second(a[u].get(i), b[u].get(i), r[i]);
+                                }
+                                b[u].set(y);
+                                b[u].store(out + half);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < W; i += 2) {
+                                    x[i] = turned_first(a[u].get(i), a[u].get(i + 1), r[i / 2]);
+                                    x[i + 1] = turned_second(a[u].get(i), a[u].get(i + 1), r[i / 2]);
+                                }
+                            }
+                            a[u].set(x);
+                        }
+                        a[u].store(out);
+                    }
             }
         }
     }
 }
 
-// Tokens of one block: enough items for every thread, while there are blocks
-// enough for the machine.
-int tokens_per_block(const MoveParams& p, int W) {
-    int64_t items = 0;
-    for (int q = 0; q < p.parts; ++q) items += (int64_t)p.part[q].heads * p.part[q].dim / (2 * W);
-    int n = 1;
-    while (n < kMaxTokensPerBlock && n * items < 2 * kThreads && p.tokens / (2 * n) >= 152 * 4 &&
-           2 * n * p.pairs * sizeof(float2) <= 32 * 1024)
-        n *= 2;
-    return n;
+// Threads of a token: as many as the words of its largest part in a small
+// call, a quarter of them in one that fills the machine, so that each thread
+// uses its cosines and sines for several heads.  Returns the block's threads.
+int deal_out(MoveParams& p, const int (&dims)[3], int W, bool adjacent) {
+    int64_t most = 1;
+    for (int q = 0; q < p.parts; ++q) {
+        Heads& h = p.part[q];
+        const int pairs = h.turned ? p.pairs : 0;
+        h.turning = !adjacent ? pairs / W : W > 1 ? 2 * pairs / W : pairs;
+        h.items = h.turning + (dims[q] - 2 * pairs) / W;
+        most = std::max(most, (int64_t)h.heads * h.items);
+    }
+    int full = 2, group;
+    while (full < 8 && (1 << full) < most) ++full;
+    const bool small = (p.tokens << full) <= 152 * 1024;
+    group = small ? full : std::max(2, full - 2);
+    if (!small && most > 1024) group = 8;
+    int threads = small ? std::max(64, 1 << group) : kThreads;
+    while ((threads >> group) > kMaxTokensPerBlock) ++group;
+    while ((threads >> group) > 1 && (threads >> group) * p.pairs * sizeof(float2) > 32 * 1024) ++group;
+    p.group_log2 = group;
+    for (int q = 0; q < p.parts; ++q) {
+        Heads& h = p.part[q];
+        h.across = std::min(h.items, 1 << group);
+        h.magic = (65536 + h.across - 1) / h.across;
+    }
+    return small ? -threads : threads;
 }
 
 template <class T, int W>
-bmmc_status launch_width(MoveParams& p, bool adjacent, cudaStream_t st) {
-    p.per_block = tokens_per_block(p, W);
-    const unsigned grid = (unsigned)((p.tokens + p.per_block - 1) / p.per_block);
-    const size_t smem = (size_t)p.per_block * p.pairs * sizeof(float2);
-    if (adjacent) move_heads_kernel<T, W, true><<<grid, kThreads, smem, st>>>(p);
-    else move_heads_kernel<T, W, false><<<grid, kThreads, smem, st>>>(p);
+bmmc_status launch_width(MoveParams& p, const int (&dims)[3], bool adjacent, cudaStream_t st) {
+    const int dealt = deal_out(p, dims, W, adjacent), threads = std::abs(dealt);
+    const int per_block = threads >> p.group_log2;
+    const dim3 grid((unsigned)((p.tokens + per_block - 1) / per_block), dealt < 0 ? p.parts : 1);
+    const size_t smem = (size_t)per_block * p.pairs * sizeof(float2);
+    if (adjacent) move_heads_kernel<T, W, true><<<grid, threads, smem, st>>>(p);
+    else move_heads_kernel<T, W, false><<<grid, threads, smem, st>>>(p);
     return launched();
 }
 
 template <class T>
-bmmc_status launch_type(MoveParams& p, bool adjacent, int bytes, cudaStream_t st) {
+bmmc_status launch_type(MoveParams& p, const int (&dims)[3], bool adjacent, int bytes, cudaStream_t st) {
     constexpr int es = sizeof(T);
     switch (bytes) {
-        case 16: return launch_width<T, 16 / es>(p, adjacent, st);
-        case 8: return launch_width<T, 8 / es>(p, adjacent, st);
-        case 4: return launch_width<T, 4 / es>(p, adjacent, st);
+        case 16: return launch_width<T, 16 / es>(p, dims, adjacent, st);
+        case 8: return launch_width<T, 8 / es>(p, dims, adjacent, st);
+        case 4: return launch_width<T, 4 / es>(p, dims, adjacent, st);
     }
-    return launch_width<T, 1>(p, adjacent, st);
+    return launch_width<T, 1>(p, dims, adjacent, st);
 }
 
-bmmc_status launch(MoveParams& p, int type, bool adjacent, int bytes, cudaStream_t st) {
+bmmc_status launch(MoveParams& p, const int (&dims)[3], int type, bool adjacent, int bytes, cudaStream_t st) {
     switch (type) {
-        case BMMC_F32: return launch_type<float>(p, adjacent, bytes, st);
-        case BMMC_F16: return launch_type<__half>(p, adjacent, bytes, st);
+        case BMMC_F32: return launch_type<float>(p, dims, adjacent, bytes, st);
+        case BMMC_F16: return launch_type<__half>(p, dims, adjacent, bytes, st);
     }
-    return launch_type<__nv_bfloat16>(p, adjacent, bytes, st);
+    return launch_type<__nv_bfloat16>(p, dims, adjacent, bytes, st);
 }
 
 bool bad_stride(int64_t s) { return s < 0 || s > kMaxStride; }
@@ -289,7 +357,6 @@ Heads heads_of(const token_heads_t& x, int es, int turned) {
     h.src_token = x.token_stride * es;
     h.src_head = x.head_stride * es;
     h.heads = (int)x.heads;
-    h.dim = (int)x.dim;
     h.turned = turned;
     return h;
 }
@@ -320,8 +387,9 @@ bmmc_status rotary(const rotary_args_t* a, void* stream) {
     p.part[0].dst_token = a->out.token_stride * es;
     p.part[0].dst_head = a->out.head_stride * es;
     p.tokens = a->tokens;
+    const int dims[3] = {(int)a->x.dim};
     const int wb = word_bytes(es, {address_bits(a->x, es), address_bits(a->out, es), pair_bits(a->turns, es)});
-    return launch(p, (int)a->type, a->turns.flags & ROTARY_ADJACENT, wb, static_cast<cudaStream_t>(stream));
+    return launch(p, dims, (int)a->type, a->turns.flags & ROTARY_ADJACENT, wb, static_cast<cudaStream_t>(stream));
 }
 
 bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
@@ -405,8 +473,9 @@ bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
     p.table_columns = a->table_columns;
     p.pages = a->pages;
     p.page_size = (int)a->page_size;
+    const int dims[3] = {(int)a->k.dim, (int)a->v.dim, (int)a->q.dim};
     const int wb = word_bytes(es, {bits, pair_bits(a->turns, es)});
-    return launch(p, (int)a->type, a->turns.flags & ROTARY_ADJACENT, wb, static_cast<cudaStream_t>(stream));
+    return launch(p, dims, (int)a->type, a->turns.flags & ROTARY_ADJACENT, wb, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -6,6 +6,10 @@ Argument marshalling for the entry points of the same names in
 that are not given are allocated.  Every element is moved by the library's
 CUDA kernels, on the current stream or the one given; nothing waits for the
 device, so the calls can be captured in a CUDA graph.
+
+The calls of a decoding step take a few microseconds on the device, less than
+a careless binding takes on the host: a check costs no more than its
+comparison here, and what a refusal says is put together when it is raised.
 """
 
 from __future__ import annotations
@@ -16,60 +20,89 @@ from . import _capi
 
 __all__ = ["expert_sort", "expert_dispatch", "expert_combine", "expert_combine_backward", "rotary", "paged_append"]
 
-_types = {}  # torch dtype -> bmmc_dtype
+_torch = None
+_types = {}       # torch dtype -> bmmc_dtype
+_current_device = _raw_stream = _int32 = _int64 = _float32 = None
+_workspaces = {}  # (tokens, choices, experts) -> bytes that expert_sort asks for
 
 
 def _setup():
-    import torch
+    """torch is imported by the first call that gets a tensor."""
+    global _torch, _current_device, _raw_stream, _int32, _int64, _float32
+    if _torch is None:
+        import torch
 
-    if not _types:
         _types.update({torch.float32: _capi.F32, torch.float16: _capi.F16, torch.bfloat16: _capi.BF16})
-    return torch
+        _int32, _int64, _float32 = torch.int32, torch.int64, torch.float32
+        _current_device = torch.cuda.current_device
+        # the handle itself, where torch gives it without a Stream object around it
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if _raw_stream is None:
+            _raw_stream = lambda device: torch.cuda.current_stream(device).cuda_stream  # noqa: E731
+        _torch = torch
+    return _torch
 
 
-def _type(x, where: str, name: str) -> int:
-    t = _types.get(x.dtype)
-    if t is None:
-        raise ValueError(f"{where}: {name} is {x.dtype}; float32, float16 and bfloat16 are supported")
-    return t
+def _no(where: str, message: str):
+    raise ValueError(f"{where}: {message}")
 
 
-def _on_device(torch, where: str, **tensors) -> None:
-    """Every tensor on the current device, where the library launches."""
-    cur = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    for name, x in tensors.items():
-        if x is not None and (not x.is_cuda or x.get_device() != cur):
-            raise ValueError(f"{where}: {name} is on {x.device}, but the current device is cuda:{cur}")
-
-
-def _stream(torch, stream) -> int:
+def _launch(where: str, stream, *tensors) -> int:
+    """The stream to launch on; every tensor has to be on the current device,
+    where the library launches."""
+    device = None
+    for x in tensors:
+        if x is not None:
+            if not x.is_cuda:
+                _no(where, f"a tensor is on {x.device}, but the current device is a CUDA device or none")
+            if device is None:
+                device = _current_device()
+            if x.get_device() != device:
+                _no(where, f"a tensor is on {x.device}, but the current device is cuda:{device}")
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _raw_stream(device)
     return stream if isinstance(stream, int) else int(stream.cuda_stream)
 
 
 def _check(status: int, where: str) -> None:
-    if status != _capi.OK:
+    if status:
         from . import BmmcError
 
         raise BmmcError(status, where)
 
 
-def _need(ok: bool, where: str, message: str) -> None:
-    if not ok:
-        raise ValueError(f"{where}: {message}")
+def _type(x, where: str, name: str) -> int:
+    t = _types.get(x.dtype)
+    if t is None:
+        _no(where, f"{name} is {x.dtype}; float32, float16 and bfloat16 are supported")
+    return t
 
 
-def _matrix(x, where: str, name: str, rows=None, cols=None) -> None:
-    """A 2-D tensor whose rows are dense (any row stride)."""
-    _need(x.dim() == 2 and (x.shape[1] < 2 or x.stride(1) == 1), where, f"{name} must be 2-D with dense rows")
-    _need((rows is None or x.shape[0] == rows) and (cols is None or x.shape[1] == cols), where,
-          f"{name} has shape {tuple(x.shape)}, expected ({rows}, {cols})")
+def _matrix(x, where: str, name: str):
+    """Rows, columns and row stride of a 2-D tensor whose rows are dense."""
+    if x.dim() != 2:
+        _no(where, f"{name} must be 2-D with dense rows")
+    (rows, cols), (stride, inner) = x.shape, x.stride()
+    if inner != 1 and cols > 1:
+        _no(where, f"{name} must be 2-D with dense rows")
+    return rows, cols, stride
 
 
-def _slot(slot, torch, where: str) -> None:
-    _need(slot.dim() == 2 and slot.dtype == torch.int32 and slot.is_contiguous(), where,
-          "slot must be a contiguous int32 tensor [tokens, choices]")
+def _slot(slot, where: str):
+    if slot.dim() != 2 or slot.dtype != _int32 or not slot.is_contiguous():
+        _no(where, "slot must be a contiguous int32 tensor [tokens, choices]")
+    return slot.shape
+
+
+def _output(out, rows: int, cols: int, like, where: str):
+    """`out`, checked, or a new tensor; and its row stride."""
+    if out is None:
+        return like.new_empty((rows, cols)), cols
+    r, c, stride = _matrix(out, where, "out")
+    if r != rows or c != cols or out.dtype != like.dtype:
+        _no(where, f"out has shape {tuple(out.shape)} and type {out.dtype}, expected shape ({rows}, {cols}) and "
+                   f"type {like.dtype}")
+    return out, stride
 
 
 def expert_sort(experts, num_experts: int, stream=None):
@@ -82,51 +115,66 @@ def expert_sort(experts, num_experts: int, stream=None):
     [num_experts + 1]: expert e has rows offsets[e] .. offsets[e + 1] - 1."""
     torch = _setup()
     where = "expert_sort"
-    _need(experts.dim() == 2 and experts.dtype in (torch.int32, torch.int64) and experts.is_contiguous(), where,
-          "experts must be a contiguous int32 or int64 tensor [tokens, choices]")
-    _on_device(torch, where, experts=experts)
+    id_bytes = {_int32: 4, _int64: 8}.get(experts.dtype)
+    if experts.dim() != 2 or id_bytes is None or not experts.is_contiguous():
+        _no(where, "experts must be a contiguous int32 or int64 tensor [tokens, choices]")
+    st = _launch(where, stream, experts)
     T, K = experts.shape
     L = _capi.lib()
-    size = ctypes.c_size_t()
-    _check(L.expert_sort_workspace(T, K, num_experts, size), where)
-    n = T * K
-    # one allocation: source, offsets, then the workspace
-    rest = torch.empty(n + num_experts + 1 + size.value // 4, dtype=torch.int32, device=experts.device)
-    slot = torch.empty((T, K), dtype=torch.int32, device=experts.device)
-    at = rest.data_ptr()
-    _check(L.expert_sort(experts.data_ptr(), experts.element_size(), T, K, num_experts, slot.data_ptr(), at, at + 4 * n,
-                         at + 4 * (n + num_experts + 1), size.value, _stream(torch, stream)), where)
-    return slot, rest[:n], rest[n:n + num_experts + 1]
+    need = _workspaces.get((T, K, num_experts))
+    if need is None:
+        size = ctypes.c_size_t()
+        _check(L.expert_sort_workspace(T, K, num_experts, size), where)
+        if len(_workspaces) > 1000:
+            _workspaces.clear()
+        need = _workspaces[T, K, num_experts] = size.value
+    device = experts.device
+    slot = torch.empty((T, K), dtype=_int32, device=device)
+    source = torch.empty(T * K, dtype=_int32, device=device)
+    offsets = torch.empty(num_experts + 1, dtype=_int32, device=device)
+    work = torch.empty(need // 4, dtype=_int32, device=device) if need else None
+    if stream is not None and need:
+        _used_on(work, stream)
+    _check(L.expert_sort(experts.data_ptr(), id_bytes, T, K, num_experts, slot.data_ptr(), source.data_ptr(),
+                         offsets.data_ptr(), work.data_ptr() if need else None, need, st), where)
+    return slot, source, offsets
+
+
+def _used_on(x, stream) -> None:
+    """Memory that is given back when this call returns stays the stream's
+    until its work is done."""
+    if isinstance(stream, int):
+        stream = _torch.cuda.ExternalStream(stream)
+    x.record_stream(stream)
 
 
 def expert_dispatch(x, slot, num_rows=None, out=None, stream=None):
     """rows[slot[t, k]] = x[t] for every routed choice, zero in the rows of
     the others; [num_rows, hidden], num_rows = tokens * choices unless fewer
     are asked for (choices numbered num_rows and above are dropped)."""
-    torch = _setup()
+    _setup()
     where = "expert_dispatch"
-    _slot(slot, torch, where)
-    T, K = slot.shape
-    _matrix(x, where, "x", rows=T)
+    T, K = _slot(slot, where)
+    tokens, H, x_stride = _matrix(x, where, "x")
+    if tokens != T:
+        _no(where, f"x has shape {tuple(x.shape)} for {T} tokens")
     R = T * K if num_rows is None else int(num_rows)
-    _need(0 <= R <= T * K, where, f"num_rows {R} is outside [0, {T * K}]")
-    H = x.shape[1]
-    if out is None:
-        out = torch.empty((R, H), dtype=x.dtype, device=x.device)
-    else:
-        _matrix(out, where, "out", R, H)
-        _need(out.dtype == x.dtype, where, "out must have the type of x")
-    _on_device(torch, where, x=x, slot=slot, out=out)
-    _check(_capi.lib().expert_dispatch(x.data_ptr(), x.stride(0), slot.data_ptr(), T, K, H, _type(x, where, "x"),
-                                       out.data_ptr(), out.stride(0), R, _stream(torch, stream)), where)
+    if not 0 <= R <= T * K:
+        _no(where, f"num_rows {R} is outside [0, {T * K}]")
+    t = _type(x, where, "x")
+    out, stride = _output(out, R, H, x, where)
+    st = _launch(where, stream, x, slot, out)
+    _check(_capi.lib().expert_dispatch(x.data_ptr(), x_stride, slot.data_ptr(), T, K, H, t, out.data_ptr(), stride, R, st),
+           where)
     return out
 
 
 def _weights(weights, slot, rows, where: str) -> int:
-    _need(tuple(weights.shape) == tuple(slot.shape) and weights.is_contiguous(), where,
-          "weights must be a contiguous tensor of slot's shape")
+    if weights.shape != slot.shape or not weights.is_contiguous():
+        _no(where, "weights must be a contiguous tensor of slot's shape")
     t = _type(weights, where, "weights")
-    _need(t == _capi.F32 or weights.dtype == rows.dtype, where, "weights must be float32 or of the rows' type")
+    if t != _capi.F32 and weights.dtype != rows.dtype:
+        _no(where, "weights must be float32 or of the rows' type")
     return t
 
 
@@ -134,84 +182,97 @@ def expert_combine(rows, slot, weights=None, out=None, stream=None):
     """out[t] = sum over the routed choices k of weights[t, k] *
     rows[slot[t, k]] (weights float32 or of the rows' type); without weights
     the plain sum, which is the gradient of expert_dispatch by x."""
-    torch = _setup()
+    _setup()
     where = "expert_combine"
-    _slot(slot, torch, where)
-    T, K = slot.shape
-    _matrix(rows, where, "rows")
-    R, H = rows.shape
-    _need(R <= T * K, where, f"rows has {R} rows for {T * K} choices")
-    wt = _capi.F32 if weights is None else _weights(weights, slot, rows, where)
-    if out is None:
-        out = torch.empty((T, H), dtype=rows.dtype, device=rows.device)
-    else:
-        _matrix(out, where, "out", T, H)
-        _need(out.dtype == rows.dtype, where, "out must have the type of rows")
-    _on_device(torch, where, rows=rows, slot=slot, weights=weights, out=out)
-    _check(_capi.lib().expert_combine(rows.data_ptr(), rows.stride(0), R, slot.data_ptr(),
-                                      None if weights is None else weights.data_ptr(), wt, T, K, H,
-                                      _type(rows, where, "rows"), out.data_ptr(), out.stride(0),
-                                      _stream(torch, stream)), where)
+    T, K = _slot(slot, where)
+    R, H, row_stride = _matrix(rows, where, "rows")
+    if R > T * K:
+        _no(where, f"rows has {R} rows for {T * K} choices")
+    t = _type(rows, where, "rows")
+    wt, wp = (_capi.F32, None) if weights is None else (_weights(weights, slot, rows, where), weights.data_ptr())
+    out, stride = _output(out, T, H, rows, where)
+    st = _launch(where, stream, rows, slot, weights, out)
+    _check(_capi.lib().expert_combine(rows.data_ptr(), row_stride, R, slot.data_ptr(), wp, wt, T, K, H, t, out.data_ptr(),
+                                      stride, st), where)
     return out
 
 
 def expert_combine_backward(grad, rows, slot, weights, stream=None):
     """(grad_rows, grad_weights) of expert_combine(rows, slot, weights) from
     the gradient of its result."""
-    torch = _setup()
+    _setup()
     where = "expert_combine_backward"
-    _slot(slot, torch, where)
-    T, K = slot.shape
-    _matrix(rows, where, "rows")
-    R, H = rows.shape
-    _need(R <= T * K, where, f"rows has {R} rows for {T * K} choices")
-    _matrix(grad, where, "grad", T, H)
-    _need(grad.dtype == rows.dtype, where, "grad must have the type of rows")
-    wt = _weights(weights, slot, rows, where)
-    _on_device(torch, where, grad=grad, rows=rows, slot=slot, weights=weights)
-    grad_rows = torch.empty((R, H), dtype=rows.dtype, device=rows.device)
-    grad_weights = torch.empty((T, K), dtype=weights.dtype, device=rows.device)
-    _check(_capi.lib().expert_combine_backward(
-        grad.data_ptr(), grad.stride(0), rows.data_ptr(), rows.stride(0), R, slot.data_ptr(), weights.data_ptr(), wt, T, K,
-        H, _type(rows, where, "rows"), grad_rows.data_ptr(), H, grad_weights.data_ptr(), _stream(torch, stream)), where)
+    T, K = _slot(slot, where)
+    R, H, row_stride = _matrix(rows, where, "rows")
+    if R > T * K:
+        _no(where, f"rows has {R} rows for {T * K} choices")
+    tokens, cols, grad_stride = _matrix(grad, where, "grad")
+    if tokens != T or cols != H or grad.dtype != rows.dtype:
+        _no(where, f"grad must have the shape ({T}, {H}) and the type of rows")
+    t, wt = _type(rows, where, "rows"), _weights(weights, slot, rows, where)
+    st = _launch(where, stream, grad, rows, slot, weights)
+    grad_rows, grad_weights = rows.new_empty((R, H)), weights.new_empty((T, K))
+    _check(_capi.lib().expert_combine_backward(grad.data_ptr(), grad_stride, rows.data_ptr(), row_stride, R,
+                                               slot.data_ptr(), weights.data_ptr(), wt, T, K, H, t, grad_rows.data_ptr(), H,
+                                               grad_weights.data_ptr(), st), where)
     return grad_rows, grad_weights
 
 
-def _heads(x, where: str, name: str, like=None):
-    """token_heads_t of a tensor [tokens, heads, dim] with dense heads."""
-    _need(x.dim() == 3 and (x.shape[2] < 2 or x.stride(2) == 1), where,
-          f"{name} must be [tokens, heads, dim] with dense heads")
-    if like is not None:
-        _need(x.dtype == like.dtype and x.shape[0] == like.shape[0], where,
-              f"{name} must have the type and the tokens of the other heads")
-    T, H, D = x.shape
-    return x.data_ptr(), H, D, x.stride(0), x.stride(1)
+def _heads(x, where: str, name: str):
+    """token_heads_t of a tensor [tokens, heads, dim] with dense heads, and
+    its tokens."""
+    if x.dim() != 3:
+        _no(where, f"{name} must be [tokens, heads, dim] with dense heads")
+    (tokens, heads, dim), (token_stride, head_stride, inner) = x.shape, x.stride()
+    if inner != 1 and dim > 1:
+        _no(where, f"{name} must be [tokens, heads, dim] with dense heads")
+    return (x.data_ptr(), heads, dim, token_stride, head_stride), tokens
 
 
 _NO_HEADS = (0, 0, 0, 0, 0)
 
 
-def _turns(torch, tokens, positions, inv_freq, pair_axes, flags, where: str):
+def _alike(x, tokens: int, dtype, where: str, name: str):
+    h, n = _heads(x, where, name)
+    if n != tokens or x.dtype != dtype:
+        _no(where, f"{name} must have the type and the tokens of the other heads")
+    return h
+
+
+def _turned_output(x, X, out, tokens: int, where: str, name: str):
+    """`out`, checked, or a new tensor; and its heads."""
+    if out is None:
+        heads, dim = X[1], X[2]
+        out = x.new_empty((tokens, heads, dim))
+        return out, (out.data_ptr(), heads, dim, heads * dim, dim)
+    O = _alike(out, tokens, x.dtype, where, name)
+    if O[1:3] != X[1:3]:
+        _no(where, f"{name} must have the shape ({tokens}, {X[1]}, {X[2]})")
+    return out, O
+
+
+def _turns(tokens: int, positions, inv_freq, pair_axes, flags: int, where: str):
     """rotary_turns_t"""
     if inv_freq is None:
-        _need(positions is None and pair_axes is None, where, "positions and pair_axes need inv_freq")
+        if positions is not None or pair_axes is not None:
+            _no(where, "positions and pair_axes need inv_freq")
         return 0, 0, 0, 0, 0, 0, 0, flags
-    _need(inv_freq.dim() == 1 and inv_freq.dtype == torch.float32 and inv_freq.is_contiguous(), where,
-          "inv_freq must be a contiguous float32 tensor [pairs]")
+    if inv_freq.dim() != 1 or inv_freq.dtype != _float32 or not inv_freq.is_contiguous():
+        _no(where, "inv_freq must be a contiguous float32 tensor [pairs]")
     pairs = inv_freq.shape[0]
     axes_ptr = 0
     if pair_axes is not None:
-        _need(pair_axes.dtype == torch.int32 and tuple(pair_axes.shape) == (pairs,) and pair_axes.is_contiguous(),
-              where, "pair_axes must be a contiguous int32 tensor [pairs]")
+        if pair_axes.dtype != _int32 or pair_axes.shape != inv_freq.shape or not pair_axes.is_contiguous():
+            _no(where, "pair_axes must be a contiguous int32 tensor [pairs]")
         axes_ptr = pair_axes.data_ptr()
     if positions is None:
         return inv_freq.data_ptr(), axes_ptr, 0, 0, 0, 0, pairs, flags
+    width = 4 if positions.dtype == _int32 else 8 if positions.dtype == _int64 else 0
     d = positions.dim()
-    _need(d in (1, 2) and positions.shape[-1] == tokens and positions.dtype in (torch.int32, torch.int64)
-          and (tokens < 2 or positions.stride(-1) == 1), where,
-          "positions must be an int32 or int64 tensor [tokens] or [axes, tokens] with dense rows")
+    if not width or d not in (1, 2) or positions.shape[-1] != tokens or (tokens > 1 and positions.stride(-1) != 1):
+        _no(where, "positions must be an int32 or int64 tensor [tokens] or [axes, tokens] with dense rows")
     axes, stride = (1, 0) if d == 1 else (positions.shape[0], positions.stride(0))
-    return (inv_freq.data_ptr(), axes_ptr, positions.data_ptr(), positions.element_size(), axes, stride, pairs, flags)
+    return inv_freq.data_ptr(), axes_ptr, positions.data_ptr(), width, axes, stride, pairs, flags
 
 
 def rotary(x, positions, inv_freq, pair_axes=None, *, interleaved: bool = False, inverse: bool = False, out=None,
@@ -223,21 +284,32 @@ def rotary(x, positions, inv_freq, pair_axes=None, *, interleaved: bool = False,
     without pair_axes; no turn for an axis that is not there).  Elements from
     2 * pairs on are copied.  inverse turns back, which is the gradient.  out
     may be x."""
-    torch = _setup()
+    _setup()
     where = "rotary"
-    X = _heads(x, where, "x")
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    O = _heads(out, where, "out", x)
-    _need(X[1:3] == O[1:3], where, "out must have the shape of x")
-    _need(positions is not None and inv_freq is not None, where, "positions and inv_freq are needed")
+    X, T = _heads(x, where, "x")
+    t = _type(x, where, "x")
+    if positions is None or inv_freq is None:
+        _no(where, "positions and inv_freq are needed")
     flags = (_capi.ROTARY_ADJACENT if interleaved else 0) | (_capi.ROTARY_INVERSE if inverse else 0)
-    T = x.shape[0]
-    turns = _turns(torch, T, positions, inv_freq, pair_axes, flags, where)
-    _on_device(torch, where, x=x, out=out, positions=positions, inv_freq=inv_freq, pair_axes=pair_axes)
-    _check(_capi.lib().rotary(_capi.ROTARY_ARGS.pack(T, _type(x, where, "x"), *X, *O, *turns), _stream(torch, stream)),
-           where)
+    turns = _turns(T, positions, inv_freq, pair_axes, flags, where)
+    out, O = _turned_output(x, X, out, T, where, "out")
+    st = _launch(where, stream, x, out, positions, inv_freq, pair_axes)
+    _check(_capi.lib().rotary(_capi.ROTARY_ARGS.pack(T, t, *X, *O, *turns), st), where)
     return out
+
+
+def _cache(c, X, dtype, head_major: bool, where: str, name: str):
+    """(pages, page_size) and paged_cache_t of a cache."""
+    if c.dim() != 4 or c.dtype != dtype:
+        _no(where, f"{name} must be 4-D of k's type with dense heads")
+    (pages, page, heads, dim), (page_stride, slot_stride, head_stride, inner) = c.shape, c.stride()
+    if inner != 1 and dim > 1:
+        _no(where, f"{name} must be 4-D of k's type with dense heads")
+    if head_major:
+        page, heads, slot_stride, head_stride = heads, page, head_stride, slot_stride
+    if heads != X[1] or dim != X[2]:
+        _no(where, f"{name} has shape {tuple(c.shape)}, which does not fit the new heads")
+    return (pages, page), (c.data_ptr(), page_stride, slot_stride, head_stride)
 
 
 def paged_append(k, v, k_cache, v_cache, page_table, lengths, *, starts=None, q=None, q_out=None, positions=None,
@@ -254,49 +326,37 @@ def paged_append(k, v, k_cache, v_cache, page_table, lengths, *, starts=None, q=
     written.  Without positions a token's position is its entry's number.
     Returns the queries q [tokens, q_heads, dim] turned alike (in q_out, which
     may be q), or None without q.  lengths is left as it is."""
-    torch = _setup()
+    _setup()
     where = "paged_append"
-    T = k.shape[0] if k.dim() else 0
-    K, V = _heads(k, where, "k"), _heads(v, where, "v", k)
-    _need(K[1] == V[1], where, "k and v must have the same heads")
-    caches, geometry = [], None
-    for name, c, X in (("k_cache", k_cache, K), ("v_cache", v_cache, V)):
-        _need(c.dim() == 4 and c.dtype == k.dtype and (c.shape[3] < 2 or c.stride(3) == 1), where,
-              f"{name} must be 4-D of k's type with dense heads")
-        pages, page, heads, dim = c.shape
-        s = c.stride()
-        page_stride, slot_stride, head_stride = s[0], s[1], s[2]
-        if head_major:
-            page, heads, slot_stride, head_stride = heads, page, head_stride, slot_stride
-        _need(heads == X[1] and dim == X[2] and geometry in (None, (pages, page)), where,
-              f"{name} has shape {tuple(c.shape)}, which does not fit the new heads or the other cache")
-        geometry = (pages, page)
-        caches += [c.data_ptr(), page_stride, slot_stride, head_stride]
+    K, T = _heads(k, where, "k")
+    dtype = k.dtype
+    t = _type(k, where, "k")
+    V = _alike(v, T, dtype, where, "v")
+    if K[1] != V[1]:
+        _no(where, "k and v must have the same heads")
+    geometry, k_at = _cache(k_cache, K, dtype, head_major, where, "k_cache")
+    other, v_at = _cache(v_cache, V, dtype, head_major, where, "v_cache")
+    if geometry != other:
+        _no(where, f"v_cache has shape {tuple(v_cache.shape)}, which does not fit k_cache's pages")
+    B, columns, table_stride = _matrix(page_table, where, "page_table")
+    if page_table.dtype != _int32:
+        _no(where, "page_table must be an int32 tensor [sequences, columns]")
+    if lengths.dtype != _int32 or lengths.shape != (B,) or not lengths.is_contiguous():
+        _no(where, "lengths must be a contiguous int32 tensor [sequences]")
+    if starts is None:
+        if T != B:
+            _no(where, f"{T} tokens for {B} sequences need starts")
+    elif starts.dtype != _int32 or starts.shape != (B + 1,) or not starts.is_contiguous():
+        _no(where, "starts must be a contiguous int32 tensor [sequences + 1]")
+    turns = _turns(T, positions, inv_freq, pair_axes, _capi.ROTARY_ADJACENT if interleaved else 0, where)
     Q = O = _NO_HEADS
     if q is not None:
-        Q = _heads(q, where, "q", k)
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        O = _heads(q_out, where, "q_out", k)
-        _need(Q[1:3] == O[1:3], where, "q_out must have the shape of q")
-    else:
-        _need(q_out is None, where, "q_out without q")
-    _need(page_table.dim() == 2 and page_table.dtype == torch.int32
-          and (page_table.shape[1] < 2 or page_table.stride(1) == 1), where,
-          "page_table must be an int32 tensor [sequences, columns] with dense rows")
-    B, columns = page_table.shape
-    _need(lengths.dtype == torch.int32 and tuple(lengths.shape) == (B,) and lengths.is_contiguous(), where,
-          "lengths must be a contiguous int32 tensor [sequences]")
-    if starts is None:
-        _need(T == B, where, f"{T} tokens for {B} sequences need starts")
-    else:
-        _need(starts.dtype == torch.int32 and tuple(starts.shape) == (B + 1,) and starts.is_contiguous(), where,
-              "starts must be a contiguous int32 tensor [sequences + 1]")
-    turns = _turns(torch, T, positions, inv_freq, pair_axes, _capi.ROTARY_ADJACENT if interleaved else 0, where)
-    _on_device(torch, where, k=k, v=v, k_cache=k_cache, v_cache=v_cache, page_table=page_table, lengths=lengths,
-               starts=starts, q=q, q_out=q_out, positions=positions, inv_freq=inv_freq, pair_axes=pair_axes)
-    args = _capi.PAGED_APPEND_ARGS.pack(
-        T, _type(k, where, "k"), *K, *V, *Q, *O, *turns, 0 if starts is None else starts.data_ptr(), lengths.data_ptr(), B,
-        page_table.data_ptr(), page_table.stride(0), columns, *geometry, *caches)
-    _check(_capi.lib().paged_append(args, _stream(torch, stream)), where)
+        Q = _alike(q, T, dtype, where, "q")
+        q_out, O = _turned_output(q, Q, q_out, T, where, "q_out")
+    elif q_out is not None:
+        _no(where, "q_out without q")
+    st = _launch(where, stream, k, v, k_cache, v_cache, page_table, lengths, starts, q, q_out, positions, inv_freq, pair_axes)
+    _check(_capi.lib().paged_append(_capi.PAGED_APPEND_ARGS.pack(
+        T, t, *K, *V, *Q, *O, *turns, 0 if starts is None else starts.data_ptr(), lengths.data_ptr(), B,
+        page_table.data_ptr(), table_stride, columns, *geometry, *k_at, *v_at), st), where)
     return q_out
