@@ -472,6 +472,7 @@ bmmc_status expert_sort(const void* ids, int id_bytes, int64_t tokens, int choic
     size_t need = 0;
     bmmc_status s = expert_sort_workspace(tokens, choices, experts, &need);
     if (s != BMMC_OK) return s;
+    const bool checked = pointers_checked(id_bytes);
     if (id_bytes != 4 && id_bytes != 8) return BMMC_ERR_UNSUPPORTED_ELEM;
     const int64_t n = tokens * choices;
     if (!offsets || (n && (!ids || !slot || !source))) return BMMC_ERR_INVALID_ARG;
@@ -487,7 +488,7 @@ bmmc_status expert_sort(const void* ids, int id_bytes, int64_t tokens, int choic
         for (int j = 0; j < i; ++j)
             if (may_overlap(o[i], o[j])) return BMMC_ERR_ALIAS;
     }
-    if ((s = all_reachable({ids, slot, source, offsets, need ? workspace : nullptr})) != BMMC_OK) return s;
+    if ((s = all_reachable(checked, {ids, slot, source, offsets, need ? workspace : nullptr})) != BMMC_OK) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int* counts = static_cast<int*>(need ? workspace : nullptr);
     const SortShape shape = sort_shape(n, experts);
@@ -499,6 +500,7 @@ bmmc_status expert_sort(const void* ids, int id_bytes, int64_t tokens, int choic
 bmmc_status expert_dispatch(const void* x, int64_t x_stride, const int32_t* slot, int64_t tokens, int choices,
                             int64_t hidden, int type, void* rows, int64_t row_stride, int64_t n_rows, void* stream) {
     int es = 0;
+    const bool checked = pointers_checked(type);
     bmmc_status s = check_moves(tokens, choices, hidden, n_rows, type, &es);
     if (s != BMMC_OK) return s;
     if (bad_stride(x_stride, 0, tokens) || bad_stride(row_stride, hidden, n_rows)) return BMMC_ERR_INVALID_ARG;
@@ -507,7 +509,7 @@ bmmc_status expert_dispatch(const void* x, int64_t x_stride, const int32_t* slot
     if (misaligned(x, es) || misaligned(rows, es) || misaligned(slot, 4)) return BMMC_ERR_MISALIGNED;
     const Rows in{x, tokens, x_stride * es, hidden * es}, out{rows, n_rows, row_stride * es, hidden * es};
     if (may_overlap(in, out) || may_overlap({slot, 1, 0, tokens * choices * 4}, out)) return BMMC_ERR_ALIAS;
-    if ((s = all_reachable({x, slot, rows})) != BMMC_OK) return s;
+    if ((s = all_reachable(checked, {x, slot, rows})) != BMMC_OK) return s;
     const int wb = word_bytes(es, {(uint64_t)(uintptr_t)x, (uint64_t)(uintptr_t)rows, (uint64_t)(x_stride * es),
                                    (uint64_t)(row_stride * es), (uint64_t)(hidden * es)});
     const int words = (int)(hidden * es / wb);
@@ -534,6 +536,7 @@ bmmc_status expert_combine(const void* rows, int64_t row_stride, int64_t n_rows,
                            const void* weights, int weight_type, int64_t tokens, int choices, int64_t hidden, int type,
                            void* out, int64_t out_stride, void* stream) {
     int es = 0;
+    const bool checked = pointers_checked(type);
     bmmc_status s = check_moves(tokens, choices, hidden, n_rows, type, &es);
     if (s != BMMC_OK) return s;
     if (weights && weight_type != BMMC_F32 && weight_type != type) return BMMC_ERR_UNSUPPORTED_ELEM;
@@ -547,7 +550,7 @@ bmmc_status expert_combine(const void* rows, int64_t row_stride, int64_t n_rows,
     if (may_overlap({rows, n_rows, row_stride * es, hidden * es}, to) ||
         may_overlap({slot, 1, 0, tokens * choices * 4}, to) || may_overlap({weights, 1, 0, tokens * choices * ws}, to))
         return BMMC_ERR_ALIAS;
-    if ((s = all_reachable({rows, slot, weights, out})) != BMMC_OK) return s;
+    if ((s = all_reachable(checked, {rows, slot, weights, out})) != BMMC_OK) return s;
     const int wb = word_bytes(es, {(uint64_t)(uintptr_t)rows, (uint64_t)(uintptr_t)out, (uint64_t)(row_stride * es),
                                    (uint64_t)(out_stride * es), (uint64_t)(hidden * es)});
     const int words = (int)(hidden * es / wb);
@@ -555,9 +558,10 @@ bmmc_status expert_combine(const void* rows, int64_t row_stride, int64_t n_rows,
     by_type(type, wb, [&](auto e, auto width) {
         using T = decltype(e);
         constexpr int W = decltype(width)::value;
+        constexpr int U = W * sizeof(T) > 4 ? 2 : 4;  // short words: more of them in flight
         const bool few = tokens * words <= kFewWords, two = choices <= 2;
-        const Cover c = few ? cover(tokens, words, 1, 128) : two ? cover(tokens, words, 4, 256) : cover(tokens, words, 2, 256);
-        const auto kernel = few ? combine_kernel<T, W, 1, 8> : two ? combine_kernel<T, W, 4, 2> : combine_kernel<T, W, 2, 4>;
+        const Cover c = cover(tokens, words, few ? 1 : two ? 2 * U : U, few ? 128 : 256);
+        const auto kernel = few ? combine_kernel<T, W, 1, 8> : two ? combine_kernel<T, W, 2 * U, 2> : combine_kernel<T, W, U, 4>;
         kernel<<<c.grid, c.block, 0, st>>>(static_cast<const char*>(rows), row_stride * es, n_rows, slot, weights,
                                           weight_type == BMMC_F32, tokens, choices, words, static_cast<char*>(out),
                                           out_stride * es);
@@ -570,6 +574,7 @@ bmmc_status expert_combine_backward(const void* grad, int64_t grad_stride, const
                                     int64_t tokens, int choices, int64_t hidden, int type, void* grad_rows,
                                     int64_t grad_row_stride, void* grad_weights, void* stream) {
     int es = 0;
+    const bool checked = pointers_checked(type);
     bmmc_status s = check_moves(tokens, choices, hidden, n_rows, type, &es);
     if (s != BMMC_OK) return s;
     if (weight_type != BMMC_F32 && weight_type != type) return BMMC_ERR_UNSUPPORTED_ELEM;
@@ -589,7 +594,7 @@ bmmc_status expert_combine_backward(const void* grad, int64_t grad_stride, const
     for (const Rows& r : in)
         if (may_overlap(r, gr) || may_overlap(r, gw)) return BMMC_ERR_ALIAS;
     if (may_overlap(gr, gw)) return BMMC_ERR_ALIAS;
-    if ((s = all_reachable({grad, rows, slot, weights, grad_rows, grad_weights})) != BMMC_OK) return s;
+    if ((s = all_reachable(checked, {grad, rows, slot, weights, grad_rows, grad_weights})) != BMMC_OK) return s;
     const int wb = word_bytes(es, {(uint64_t)(uintptr_t)grad, (uint64_t)(uintptr_t)rows, (uint64_t)(uintptr_t)grad_rows,
                                    (uint64_t)(grad_stride * es), (uint64_t)(row_stride * es),
                                    (uint64_t)(grad_row_stride * es), (uint64_t)(hidden * es)});

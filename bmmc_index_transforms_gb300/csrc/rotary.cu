@@ -11,7 +11,6 @@
 
 #include <algorithm>
 #include <cstdint>
-#include <cstdlib>
 #include <type_traits>
 
 #include "../../include/bmmc.h"
@@ -35,6 +34,7 @@ struct Heads {
     int heads, turned, place;
     int turning, items;  // words of a head that are turned (pairs of words in halves), and all
     int across, magic;   // threads side by side on a head's words, and 65536 / across rounded up
+    unsigned ahead;      // bytes of a token's heads to fetch ahead; 0: they do not lie in one run of 16-byte words
 };
 
 struct MoveParams {
@@ -129,6 +129,15 @@ __global__ void __launch_bounds__(kThreads, 4) move_heads_kernel(const __grid_co
     const int nt = (int)min((int64_t)per_block, p.tokens - t0);
     // a block of a small call takes one part only
     const int first_part = gridDim.y > 1 ? blockIdx.y : 0, last_part = gridDim.y > 1 ? first_part + 1 : p.parts;
+    // The heads are on their way to L2 while the places and the turns are worked out.
+    if (tid < nt * (last_part - first_part)) {
+        const Heads& h = p.part[first_part + tid / nt];
+        if (h.ahead)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                             __cvta_generic_to_global(h.src + (t0 + tid % nt) * h.src_token)),
+                         "r"(h.ahead)
+                         : "memory");
+    }
     if (p.page_size) {
         if (p.starts && per_block <= 8) {
             for (int i = tid >> 5; i < nt; i += threads >> 5) {
@@ -234,8 +243,10 @@ __global__ void __launch_bounds__(kThreads, 4) move_heads_kernel(const __grid_co
 
 // Threads of a token: as many as the words of its largest part in a small
 // call, a quarter of them in one that fills the machine, so that each thread
-// uses its cosines and sines for several heads.  Returns the block's threads.
-int deal_out(MoveParams& p, const int (&dims)[3], int W, bool adjacent) {
+// uses its cosines and sines for several heads.  *split: the parts go to
+// blocks of their own, where all of these still run at once.  Returns the
+// block's threads.
+int deal_out(MoveParams& p, const int (&dims)[3], int W, int es, bool adjacent, bool* split) {
     int64_t most = 1;
     for (int q = 0; q < p.parts; ++q) {
         Heads& h = p.part[q];
@@ -257,15 +268,19 @@ int deal_out(MoveParams& p, const int (&dims)[3], int W, bool adjacent) {
         Heads& h = p.part[q];
         h.across = std::min(h.items, 1 << group);
         h.magic = (65536 + h.across - 1) / h.across;
+        const bool dense = W * es == 16 && (h.heads < 2 || h.src_head == (int64_t)dims[q] * es);
+        h.ahead = dense ? (unsigned)(h.heads * dims[q] * es) : 0u;
     }
-    return small ? -threads : threads;
+    *split = p.parts > 1 && p.tokens / (threads >> group) * p.parts * threads <= 152 * 1024;
+    return threads;
 }
 
 template <class T, int W>
 bmmc_status launch_width(MoveParams& p, const int (&dims)[3], bool adjacent, cudaStream_t st) {
-    const int dealt = deal_out(p, dims, W, adjacent), threads = std::abs(dealt);
+    bool split;
+    const int threads = deal_out(p, dims, W, sizeof(T), adjacent, &split);
     const int per_block = threads >> p.group_log2;
-    const dim3 grid((unsigned)((p.tokens + per_block - 1) / per_block), dealt < 0 ? p.parts : 1);
+    const dim3 grid((unsigned)((p.tokens + per_block - 1) / per_block), split ? p.parts : 1);
     const size_t smem = (size_t)per_block * p.pairs * sizeof(float2);
     if (adjacent) move_heads_kernel<T, W, true><<<grid, threads, smem, st>>>(p);
     else move_heads_kernel<T, W, false><<<grid, threads, smem, st>>>(p);
@@ -323,8 +338,8 @@ uint64_t address_bits(const token_heads_t& x, int es) {
            (uint64_t)(x.dim * es);
 }
 
-// The rotation's arguments, checked and put into p; tokens > 0.
-bmmc_status set_turns(MoveParams& p, const rotary_turns_t& r, int64_t tokens, bool need_positions) {
+// The rotation's arguments, checked and put into p.
+bmmc_status set_turns(MoveParams& p, const rotary_turns_t& r, bool checked, bool need_positions) {
     p.pairs = 0;
     if (r.flags & ~(int64_t)(ROTARY_ADJACENT | ROTARY_INVERSE)) return BMMC_ERR_INVALID_ARG;
     if (!r.inv_freq) return r.pairs || r.positions || r.pair_axes ? BMMC_ERR_INVALID_ARG : BMMC_OK;
@@ -343,7 +358,7 @@ bmmc_status set_turns(MoveParams& p, const rotary_turns_t& r, int64_t tokens, bo
     p.freq = r.inv_freq;
     p.pair_axes = r.pair_axes;
     p.sign = r.flags & ROTARY_INVERSE ? -1.0f : 1.0f;
-    return all_reachable({r.inv_freq, r.pair_axes, r.positions});
+    return all_reachable(checked, {r.inv_freq, r.pair_axes, r.positions});
 }
 
 // The bits that a word's size has to divide on account of the pairs.
@@ -367,7 +382,9 @@ extern "C" {
 
 bmmc_status rotary(const rotary_args_t* a, void* stream) {
     if (!a || a->tokens < 0 || a->tokens > kMaxTokens) return BMMC_ERR_INVALID_ARG;
-    const int es = dtype_bytes((int)a->type);
+    int type = a->type < 0 || a->type > 0xfff ? -1 : (int)a->type;
+    const bool checked = pointers_checked(type);
+    const int es = dtype_bytes(type);
     if (!es) return BMMC_ERR_UNSUPPORTED_ELEM;
     if (!a->tokens) return BMMC_OK;
     bmmc_status s = check_heads(a->x, es);
@@ -379,8 +396,8 @@ bmmc_status rotary(const rotary_args_t* a, void* stream) {
     if (!same_place(a->x, a->out, a->tokens) && may_overlap(rows_of(a->x, a->tokens, es), rows_of(a->out, a->tokens, es)))
         return BMMC_ERR_ALIAS;
     MoveParams p{};
-    if ((s = set_turns(p, a->turns, a->tokens, true)) != BMMC_OK) return s;
-    if ((s = all_reachable({a->x.data, a->out.data})) != BMMC_OK) return s;
+    if ((s = set_turns(p, a->turns, checked, true)) != BMMC_OK) return s;
+    if ((s = all_reachable(checked, {a->x.data, a->out.data})) != BMMC_OK) return s;
     p.parts = 1;
     p.part[0] = heads_of(a->x, es, 1);
     p.part[0].dst = static_cast<char*>(a->out.data);
@@ -389,12 +406,14 @@ bmmc_status rotary(const rotary_args_t* a, void* stream) {
     p.tokens = a->tokens;
     const int dims[3] = {(int)a->x.dim};
     const int wb = word_bytes(es, {address_bits(a->x, es), address_bits(a->out, es), pair_bits(a->turns, es)});
-    return launch(p, dims, (int)a->type, a->turns.flags & ROTARY_ADJACENT, wb, static_cast<cudaStream_t>(stream));
+    return launch(p, dims, type, a->turns.flags & ROTARY_ADJACENT, wb, static_cast<cudaStream_t>(stream));
 }
 
 bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
     if (!a || a->tokens < 0 || a->tokens > kMaxTokens) return BMMC_ERR_INVALID_ARG;
-    const int es = dtype_bytes((int)a->type);
+    int type = a->type < 0 || a->type > 0xfff ? -1 : (int)a->type;
+    const bool checked = pointers_checked(type);
+    const int es = dtype_bytes(type);
     if (!es) return BMMC_ERR_UNSUPPORTED_ELEM;
     if (!a->tokens) return BMMC_OK;
     const bool with_q = a->q.data || a->q_out.data;
@@ -444,8 +463,8 @@ bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
             (!same_place(a->q, a->q_out, a->tokens) && may_overlap(q, to)))
             return BMMC_ERR_ALIAS;
     }
-    if ((s = set_turns(p, a->turns, a->tokens, false)) != BMMC_OK) return s;
-    if ((s = all_reachable({a->k.data, a->v.data, a->q.data, a->q_out.data, a->k_cache.data, a->v_cache.data, a->starts,
+    if ((s = set_turns(p, a->turns, checked, false)) != BMMC_OK) return s;
+    if ((s = all_reachable(checked, {a->k.data, a->v.data, a->q.data, a->q_out.data, a->k_cache.data, a->v_cache.data, a->starts,
                             a->lengths, a->table})) != BMMC_OK)
         return s;
     for (int c = 0; c < 2; ++c) {
@@ -475,7 +494,7 @@ bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
     p.page_size = (int)a->page_size;
     const int dims[3] = {(int)a->k.dim, (int)a->v.dim, (int)a->q.dim};
     const int wb = word_bytes(es, {bits, pair_bits(a->turns, es)});
-    return launch(p, dims, (int)a->type, a->turns.flags & ROTARY_ADJACENT, wb, static_cast<cudaStream_t>(stream));
+    return launch(p, dims, type, a->turns.flags & ROTARY_ADJACENT, wb, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -20,45 +20,43 @@ from . import _capi
 
 __all__ = ["expert_sort", "expert_dispatch", "expert_combine", "expert_combine_backward", "rotary", "paged_append"]
 
-_torch = None
-_types = {}       # torch dtype -> bmmc_dtype
-_current_device = _raw_stream = _int32 = _int64 = _float32 = None
+_torch = _empty = _library = _raw_stream = _current_device = _int32 = _int64 = _float32 = None
+_types = {}       # torch dtype -> bmmc_dtype, with the pointers known to be the device's
+_widths = {}      # integer torch dtype -> its bytes
 _workspaces = {}  # (tokens, choices, experts) -> bytes that expert_sort asks for
+_CHECKED = _capi.POINTERS_CHECKED
+_F32 = _capi.F32 | _CHECKED
 
 
 def _setup():
     """torch is imported by the first call that gets a tensor."""
-    global _torch, _current_device, _raw_stream, _int32, _int64, _float32
-    if _torch is None:
-        import torch
+    global _torch, _empty, _library, _raw_stream, _current_device, _int32, _int64, _float32
+    import torch
 
-        _types.update({torch.float32: _capi.F32, torch.float16: _capi.F16, torch.bfloat16: _capi.BF16})
-        _int32, _int64, _float32 = torch.int32, torch.int64, torch.float32
-        _current_device = torch.cuda.current_device
-        # the handle itself, where torch gives it without a Stream object around it
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if _raw_stream is None:
-            _raw_stream = lambda device: torch.cuda.current_stream(device).cuda_stream  # noqa: E731
-        _torch = torch
-    return _torch
+    _types.update({torch.float32: _F32, torch.float16: _capi.F16 | _CHECKED, torch.bfloat16: _capi.BF16 | _CHECKED})
+    _int32, _int64, _float32 = torch.int32, torch.int64, torch.float32
+    _widths.update({_int32: 4, _int64: 8})
+    _empty, _current_device = torch.empty, torch.cuda.current_device
+    # the handle itself, where torch gives it without a Stream object around it
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if _raw_stream is None:
+        _raw_stream = lambda device: torch.cuda.current_stream(device).cuda_stream  # noqa: E731
+    _library, _torch = _capi.lib(), torch
 
 
 def _no(where: str, message: str):
     raise ValueError(f"{where}: {message}")
 
 
-def _launch(where: str, stream, *tensors) -> int:
-    """The stream to launch on; every tensor has to be on the current device,
-    where the library launches."""
-    device = None
+def _stream(device: int, stream, where: str, *tensors) -> int:
+    """The stream to launch on, given the first tensor's device; every tensor
+    has to be on the current device, where the library launches.  (It is
+    asked with the pointers checked: none but the device's get past here.)"""
+    if device < 0 or device != _current_device():
+        _no(where, f"a tensor is on {'the host' if device < 0 else f'cuda:{device}'}, not on the current device")
     for x in tensors:
-        if x is not None:
-            if not x.is_cuda:
-                _no(where, f"a tensor is on {x.device}, but the current device is a CUDA device or none")
-            if device is None:
-                device = _current_device()
-            if x.get_device() != device:
-                _no(where, f"a tensor is on {x.device}, but the current device is cuda:{device}")
+        if x is not None and x.get_device() != device:
+            _no(where, f"a tensor is on {x.device}, but the current device is cuda:{device}")
     if stream is None:
         return _raw_stream(device)
     return stream if isinstance(stream, int) else int(stream.cuda_stream)
@@ -71,11 +69,8 @@ def _check(status: int, where: str) -> None:
         raise BmmcError(status, where)
 
 
-def _type(x, where: str, name: str) -> int:
-    t = _types.get(x.dtype)
-    if t is None:
-        _no(where, f"{name} is {x.dtype}; float32, float16 and bfloat16 are supported")
-    return t
+def _no_type(x, where: str, name: str):
+    _no(where, f"{name} is {x.dtype}; float32, float16 and bfloat16 are supported")
 
 
 def _matrix(x, where: str, name: str):
@@ -89,20 +84,19 @@ def _matrix(x, where: str, name: str):
 
 
 def _slot(slot, where: str):
-    if slot.dim() != 2 or slot.dtype != _int32 or not slot.is_contiguous():
+    if slot.dtype is not _int32 or slot.dim() != 2 or not slot.is_contiguous():
         _no(where, "slot must be a contiguous int32 tensor [tokens, choices]")
     return slot.shape
 
 
-def _output(out, rows: int, cols: int, like, where: str):
-    """`out`, checked, or a new tensor; and its row stride."""
-    if out is None:
-        return like.new_empty((rows, cols)), cols
+def _output(out, rows: int, cols: int, like, where: str) -> int:
+    """The row stride of `out`, which has to be a [rows, cols] tensor of
+    like's type."""
     r, c, stride = _matrix(out, where, "out")
     if r != rows or c != cols or out.dtype != like.dtype:
         _no(where, f"out has shape {tuple(out.shape)} and type {out.dtype}, expected shape ({rows}, {cols}) and "
                    f"type {like.dtype}")
-    return out, stride
+    return stride
 
 
 def expert_sort(experts, num_experts: int, stream=None):
@@ -113,46 +107,44 @@ def expert_sort(experts, num_experts: int, stream=None):
     expert (stable), or ~row where it is not routed; ``source`` [tokens *
     choices]: the flat choice of each row, or its complement; ``offsets``
     [num_experts + 1]: expert e has rows offsets[e] .. offsets[e + 1] - 1."""
-    torch = _setup()
+    if _torch is None:
+        _setup()
     where = "expert_sort"
-    id_bytes = {_int32: 4, _int64: 8}.get(experts.dtype)
-    if experts.dim() != 2 or id_bytes is None or not experts.is_contiguous():
+    width = _widths.get(experts.dtype)
+    if width is None or experts.dim() != 2 or not experts.is_contiguous():
         _no(where, "experts must be a contiguous int32 or int64 tensor [tokens, choices]")
-    st = _launch(where, stream, experts)
+    st = _stream(experts.get_device(), stream, where)
     T, K = experts.shape
-    L = _capi.lib()
     need = _workspaces.get((T, K, num_experts))
     if need is None:
         size = ctypes.c_size_t()
-        _check(L.expert_sort_workspace(T, K, num_experts, size), where)
+        _check(_library.expert_sort_workspace(T, K, num_experts, size), where)
         if len(_workspaces) > 1000:
             _workspaces.clear()
         need = _workspaces[T, K, num_experts] = size.value
     device = experts.device
-    slot = torch.empty((T, K), dtype=_int32, device=device)
-    source = torch.empty(T * K, dtype=_int32, device=device)
-    offsets = torch.empty(num_experts + 1, dtype=_int32, device=device)
-    work = torch.empty(need // 4, dtype=_int32, device=device) if need else None
-    if stream is not None and need:
-        _used_on(work, stream)
-    _check(L.expert_sort(experts.data_ptr(), id_bytes, T, K, num_experts, slot.data_ptr(), source.data_ptr(),
-                         offsets.data_ptr(), work.data_ptr() if need else None, need, st), where)
+    slot = _empty((T, K), dtype=_int32, device=device)
+    source = _empty(T * K, dtype=_int32, device=device)
+    offsets = _empty(num_experts + 1, dtype=_int32, device=device)
+    work_ptr = None
+    if need:
+        work = _empty(need // 4, dtype=_int32, device=device)
+        work_ptr = work.data_ptr()
+        if stream is not None:  # it is given back when this call returns, and stays that stream's until the work is done
+            work.record_stream(_torch.cuda.ExternalStream(st) if isinstance(stream, int) else stream)
+    status = _library.expert_sort(experts.data_ptr(), width | _CHECKED, T, K, num_experts, slot.data_ptr(),
+                                  source.data_ptr(), offsets.data_ptr(), work_ptr, need, st)
+    if status:
+        _check(status, where)
     return slot, source, offsets
-
-
-def _used_on(x, stream) -> None:
-    """Memory that is given back when this call returns stays the stream's
-    until its work is done."""
-    if isinstance(stream, int):
-        stream = _torch.cuda.ExternalStream(stream)
-    x.record_stream(stream)
 
 
 def expert_dispatch(x, slot, num_rows=None, out=None, stream=None):
     """rows[slot[t, k]] = x[t] for every routed choice, zero in the rows of
     the others; [num_rows, hidden], num_rows = tokens * choices unless fewer
     are asked for (choices numbered num_rows and above are dropped)."""
-    _setup()
+    if _torch is None:
+        _setup()
     where = "expert_dispatch"
     T, K = _slot(slot, where)
     tokens, H, x_stride = _matrix(x, where, "x")
@@ -161,46 +153,63 @@ def expert_dispatch(x, slot, num_rows=None, out=None, stream=None):
     R = T * K if num_rows is None else int(num_rows)
     if not 0 <= R <= T * K:
         _no(where, f"num_rows {R} is outside [0, {T * K}]")
-    t = _type(x, where, "x")
-    out, stride = _output(out, R, H, x, where)
-    st = _launch(where, stream, x, slot, out)
-    _check(_capi.lib().expert_dispatch(x.data_ptr(), x_stride, slot.data_ptr(), T, K, H, t, out.data_ptr(), stride, R, st),
-           where)
+    t = _types.get(x.dtype)
+    if t is None:
+        _no_type(x, where, "x")
+    if out is None:
+        st = _stream(x.get_device(), stream, where, slot)
+        out, stride = _empty((R, H), dtype=x.dtype, device=x.device), H
+    else:
+        st = _stream(x.get_device(), stream, where, slot, out)
+        stride = _output(out, R, H, x, where)
+    status = _library.expert_dispatch(x.data_ptr(), x_stride, slot.data_ptr(), T, K, H, t, out.data_ptr(), stride, R, st)
+    if status:
+        _check(status, where)
     return out
 
 
 def _weights(weights, slot, rows, where: str) -> int:
     if weights.shape != slot.shape or not weights.is_contiguous():
         _no(where, "weights must be a contiguous tensor of slot's shape")
-    t = _type(weights, where, "weights")
-    if t != _capi.F32 and weights.dtype != rows.dtype:
+    if weights.dtype is not _float32 and weights.dtype != rows.dtype:
         _no(where, "weights must be float32 or of the rows' type")
-    return t
+    return _types[weights.dtype] & ~_CHECKED
 
 
 def expert_combine(rows, slot, weights=None, out=None, stream=None):
     """out[t] = sum over the routed choices k of weights[t, k] *
     rows[slot[t, k]] (weights float32 or of the rows' type); without weights
     the plain sum, which is the gradient of expert_dispatch by x."""
-    _setup()
+    if _torch is None:
+        _setup()
     where = "expert_combine"
     T, K = _slot(slot, where)
     R, H, row_stride = _matrix(rows, where, "rows")
     if R > T * K:
         _no(where, f"rows has {R} rows for {T * K} choices")
-    t = _type(rows, where, "rows")
-    wt, wp = (_capi.F32, None) if weights is None else (_weights(weights, slot, rows, where), weights.data_ptr())
-    out, stride = _output(out, T, H, rows, where)
-    st = _launch(where, stream, rows, slot, weights, out)
-    _check(_capi.lib().expert_combine(rows.data_ptr(), row_stride, R, slot.data_ptr(), wp, wt, T, K, H, t, out.data_ptr(),
-                                      stride, st), where)
+    t = _types.get(rows.dtype)
+    if t is None:
+        _no_type(rows, where, "rows")
+    wt, wp = 0, None
+    if weights is not None:
+        wt, wp = _weights(weights, slot, rows, where), weights.data_ptr()
+    st = _stream(rows.get_device(), stream, where, slot, weights, out)
+    if out is None:
+        out, stride = _empty((T, H), dtype=rows.dtype, device=rows.device), H
+    else:
+        stride = _output(out, T, H, rows, where)
+    status = _library.expert_combine(rows.data_ptr(), row_stride, R, slot.data_ptr(), wp, wt, T, K, H, t, out.data_ptr(),
+                                     stride, st)
+    if status:
+        _check(status, where)
     return out
 
 
 def expert_combine_backward(grad, rows, slot, weights, stream=None):
     """(grad_rows, grad_weights) of expert_combine(rows, slot, weights) from
     the gradient of its result."""
-    _setup()
+    if _torch is None:
+        _setup()
     where = "expert_combine_backward"
     T, K = _slot(slot, where)
     R, H, row_stride = _matrix(rows, where, "rows")
@@ -209,12 +218,19 @@ def expert_combine_backward(grad, rows, slot, weights, stream=None):
     tokens, cols, grad_stride = _matrix(grad, where, "grad")
     if tokens != T or cols != H or grad.dtype != rows.dtype:
         _no(where, f"grad must have the shape ({T}, {H}) and the type of rows")
-    t, wt = _type(rows, where, "rows"), _weights(weights, slot, rows, where)
-    st = _launch(where, stream, grad, rows, slot, weights)
-    grad_rows, grad_weights = rows.new_empty((R, H)), weights.new_empty((T, K))
-    _check(_capi.lib().expert_combine_backward(grad.data_ptr(), grad_stride, rows.data_ptr(), row_stride, R,
-                                               slot.data_ptr(), weights.data_ptr(), wt, T, K, H, t, grad_rows.data_ptr(), H,
-                                               grad_weights.data_ptr(), st), where)
+    t = _types.get(rows.dtype)
+    if t is None:
+        _no_type(rows, where, "rows")
+    wt = _weights(weights, slot, rows, where)
+    st = _stream(rows.get_device(), stream, where, grad, slot, weights)
+    device = rows.device
+    grad_rows = _empty((R, H), dtype=rows.dtype, device=device)
+    grad_weights = _empty((T, K), dtype=weights.dtype, device=device)
+    status = _library.expert_combine_backward(grad.data_ptr(), grad_stride, rows.data_ptr(), row_stride, R,
+                                              slot.data_ptr(), weights.data_ptr(), wt, T, K, H, t, grad_rows.data_ptr(), H,
+                                              grad_weights.data_ptr(), st)
+    if status:
+        _check(status, where)
     return grad_rows, grad_weights
 
 
@@ -241,13 +257,13 @@ def _alike(x, tokens: int, dtype, where: str, name: str):
 
 def _turned_output(x, X, out, tokens: int, where: str, name: str):
     """`out`, checked, or a new tensor; and its heads."""
+    heads, dim = X[1], X[2]
     if out is None:
-        heads, dim = X[1], X[2]
-        out = x.new_empty((tokens, heads, dim))
+        out = _empty((tokens, heads, dim), dtype=x.dtype, device=x.device)
         return out, (out.data_ptr(), heads, dim, heads * dim, dim)
     O = _alike(out, tokens, x.dtype, where, name)
     if O[1:3] != X[1:3]:
-        _no(where, f"{name} must have the shape ({tokens}, {X[1]}, {X[2]})")
+        _no(where, f"{name} must have the shape ({tokens}, {heads}, {dim})")
     return out, O
 
 
@@ -257,21 +273,21 @@ def _turns(tokens: int, positions, inv_freq, pair_axes, flags: int, where: str):
         if positions is not None or pair_axes is not None:
             _no(where, "positions and pair_axes need inv_freq")
         return 0, 0, 0, 0, 0, 0, 0, flags
-    if inv_freq.dim() != 1 or inv_freq.dtype != _float32 or not inv_freq.is_contiguous():
+    if inv_freq.dtype is not _float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         _no(where, "inv_freq must be a contiguous float32 tensor [pairs]")
     pairs = inv_freq.shape[0]
     axes_ptr = 0
     if pair_axes is not None:
-        if pair_axes.dtype != _int32 or pair_axes.shape != inv_freq.shape or not pair_axes.is_contiguous():
+        if pair_axes.dtype is not _int32 or pair_axes.shape != inv_freq.shape or not pair_axes.is_contiguous():
             _no(where, "pair_axes must be a contiguous int32 tensor [pairs]")
         axes_ptr = pair_axes.data_ptr()
     if positions is None:
         return inv_freq.data_ptr(), axes_ptr, 0, 0, 0, 0, pairs, flags
-    width = 4 if positions.dtype == _int32 else 8 if positions.dtype == _int64 else 0
-    d = positions.dim()
-    if not width or d not in (1, 2) or positions.shape[-1] != tokens or (tokens > 1 and positions.stride(-1) != 1):
+    width = _widths.get(positions.dtype)
+    shape, strides = positions.shape, positions.stride()
+    if width is None or len(shape) not in (1, 2) or shape[-1] != tokens or (tokens > 1 and strides[-1] != 1):
         _no(where, "positions must be an int32 or int64 tensor [tokens] or [axes, tokens] with dense rows")
-    axes, stride = (1, 0) if d == 1 else (positions.shape[0], positions.stride(0))
+    axes, stride = (1, 0) if len(shape) == 1 else (shape[0], strides[0])
     return inv_freq.data_ptr(), axes_ptr, positions.data_ptr(), width, axes, stride, pairs, flags
 
 
@@ -284,17 +300,22 @@ def rotary(x, positions, inv_freq, pair_axes=None, *, interleaved: bool = False,
     without pair_axes; no turn for an axis that is not there).  Elements from
     2 * pairs on are copied.  inverse turns back, which is the gradient.  out
     may be x."""
-    _setup()
+    if _torch is None:
+        _setup()
     where = "rotary"
     X, T = _heads(x, where, "x")
-    t = _type(x, where, "x")
+    t = _types.get(x.dtype)
+    if t is None:
+        _no_type(x, where, "x")
     if positions is None or inv_freq is None:
         _no(where, "positions and inv_freq are needed")
     flags = (_capi.ROTARY_ADJACENT if interleaved else 0) | (_capi.ROTARY_INVERSE if inverse else 0)
     turns = _turns(T, positions, inv_freq, pair_axes, flags, where)
+    st = _stream(x.get_device(), stream, where, positions, inv_freq, pair_axes, out)
     out, O = _turned_output(x, X, out, T, where, "out")
-    st = _launch(where, stream, x, out, positions, inv_freq, pair_axes)
-    _check(_capi.lib().rotary(_capi.ROTARY_ARGS.pack(T, t, *X, *O, *turns), st), where)
+    status = _library.rotary(_capi.ROTARY_ARGS.pack(T, t, *X, *O, *turns), st)
+    if status:
+        _check(status, where)
     return out
 
 
@@ -326,11 +347,14 @@ def paged_append(k, v, k_cache, v_cache, page_table, lengths, *, starts=None, q=
     written.  Without positions a token's position is its entry's number.
     Returns the queries q [tokens, q_heads, dim] turned alike (in q_out, which
     may be q), or None without q.  lengths is left as it is."""
-    _setup()
+    if _torch is None:
+        _setup()
     where = "paged_append"
     K, T = _heads(k, where, "k")
     dtype = k.dtype
-    t = _type(k, where, "k")
+    t = _types.get(dtype)
+    if t is None:
+        _no_type(k, where, "k")
     V = _alike(v, T, dtype, where, "v")
     if K[1] != V[1]:
         _no(where, "k and v must have the same heads")
@@ -339,24 +363,30 @@ def paged_append(k, v, k_cache, v_cache, page_table, lengths, *, starts=None, q=
     if geometry != other:
         _no(where, f"v_cache has shape {tuple(v_cache.shape)}, which does not fit k_cache's pages")
     B, columns, table_stride = _matrix(page_table, where, "page_table")
-    if page_table.dtype != _int32:
+    if page_table.dtype is not _int32:
         _no(where, "page_table must be an int32 tensor [sequences, columns]")
-    if lengths.dtype != _int32 or lengths.shape != (B,) or not lengths.is_contiguous():
+    if lengths.dtype is not _int32 or lengths.shape != (B,) or not lengths.is_contiguous():
         _no(where, "lengths must be a contiguous int32 tensor [sequences]")
+    starts_ptr = 0
     if starts is None:
         if T != B:
             _no(where, f"{T} tokens for {B} sequences need starts")
-    elif starts.dtype != _int32 or starts.shape != (B + 1,) or not starts.is_contiguous():
+    elif starts.dtype is not _int32 or starts.shape != (B + 1,) or not starts.is_contiguous():
         _no(where, "starts must be a contiguous int32 tensor [sequences + 1]")
+    else:
+        starts_ptr = starts.data_ptr()
     turns = _turns(T, positions, inv_freq, pair_axes, _capi.ROTARY_ADJACENT if interleaved else 0, where)
+    st = _stream(k.get_device(), stream, where, v, k_cache, v_cache, page_table, lengths, starts, q, q_out, positions,
+                 inv_freq, pair_axes)
     Q = O = _NO_HEADS
     if q is not None:
         Q = _alike(q, T, dtype, where, "q")
         q_out, O = _turned_output(q, Q, q_out, T, where, "q_out")
     elif q_out is not None:
         _no(where, "q_out without q")
-    st = _launch(where, stream, k, v, k_cache, v_cache, page_table, lengths, starts, q, q_out, positions, inv_freq, pair_axes)
-    _check(_capi.lib().paged_append(_capi.PAGED_APPEND_ARGS.pack(
-        T, t, *K, *V, *Q, *O, *turns, 0 if starts is None else starts.data_ptr(), lengths.data_ptr(), B,
-        page_table.data_ptr(), table_stride, columns, *geometry, *k_at, *v_at), st), where)
+    status = _library.paged_append(_capi.PAGED_APPEND_ARGS.pack(
+        T, t, *K, *V, *Q, *O, *turns, starts_ptr, lengths.data_ptr(), B, page_table.data_ptr(), table_stride, columns,
+        *geometry, *k_at, *v_at), st)
+    if status:
+        _check(status, where)
     return q_out

@@ -555,6 +555,11 @@ typedef enum {
     BMMC_BF16 = 2
 } bmmc_dtype;
 
+/* Or'ed into `type` (into `id_bytes` of expert_sort): the caller has made sure
+ * that the GPU can reach every pointer, and none of them is asked for, which
+ * takes 0.4 us of a call's host time for each. */
+#define BMMC_POINTERS_CHECKED 0x100
+
 #define EXPERT_MAX_CHOICES 64
 
 /* Number the choices of a router by expert.  ids[t * choices + k] (dense,

@@ -650,3 +650,12 @@ def test_tensors_elsewhere_are_refused():
     with pytest.raises(bm.BmmcError, match="overlap"):
         y = torch.zeros(20, 8, device="cuda")
         bm.expert_combine(y[:8], slot, out=y[6:10])
+    x = x.cuda()
+    with pytest.raises(ValueError, match="shape"):
+        bm.expert_dispatch(x, slot, out=x.half())
+    h, at, f = torch.zeros(3, 2, 8, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(4, device="cuda")
+    with pytest.raises(ValueError, match="type"):
+        bm.rotary(h, at, f, out=h.half())
+    cache, table = torch.zeros(5, 4, 2, 8, device="cuda"), torch.zeros(3, 2, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="without q"):
+        bm.paged_append(h, h, cache, cache.clone(), table, at, q_out=h.clone())

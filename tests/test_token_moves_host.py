@@ -170,7 +170,7 @@ def test_binding_refusals():
         (lambda: bm.expert_sort(slot.float(), 4), "experts must be"), (lambda: bm.expert_sort(slot.t(), 4), "experts must be"),
         (lambda: bm.expert_sort(slot, 4), "current device"), (lambda: bm.expert_dispatch(x, slot.long()), "slot must be"),
         (lambda: bm.expert_dispatch(x[:3], slot), "shape"), (lambda: bm.expert_dispatch(x.t(), slot), "dense rows"),
-        (lambda: bm.expert_dispatch(x, slot, 9), "num_rows"), (lambda: bm.expert_dispatch(x, slot, out=x.half()), "shape"),
+        (lambda: bm.expert_dispatch(x, slot, 9), "num_rows"),
         (lambda: bm.expert_dispatch(x, slot), "current device"), (lambda: bm.expert_combine(torch.zeros(9, 8), slot), "9 rows"),
         (lambda: bm.expert_combine(torch.zeros(8, 8), slot, torch.zeros(4, 3)), "slot's shape"),
         (lambda: bm.expert_combine(torch.zeros(8, 8), slot, torch.zeros(4, 2).half()), "float32 or of the rows' type"),
@@ -181,7 +181,7 @@ def test_binding_refusals():
         (lambda: bm.rotary(h[0], at, f), "tokens, heads, dim"), (lambda: bm.rotary(h, at[:2], f), "positions must"),
         (lambda: bm.rotary(h, at.float(), f), "positions must"), (lambda: bm.rotary(h, at, f.double()), "inv_freq must"),
         (lambda: bm.rotary(h, at, f, torch.zeros(3, dtype=torch.int32)), "pair_axes must"),
-        (lambda: bm.rotary(h, at, f, out=h.half()), "type"), (lambda: bm.rotary(h, None, f), "needed"), (lambda: bm.rotary(h, at, f), "current device"),
+        (lambda: bm.rotary(h, None, f), "needed"), (lambda: bm.rotary(h, at, f), "current device"),
     ]
     cache, table, n = torch.zeros(5, 4, 2, 8), torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
     call = bm.paged_append
@@ -190,7 +190,7 @@ def test_binding_refusals():
         (lambda: call(h, h, cache, cache[:4], table, n), "does not fit"), (lambda: call(h, h, cache, cache, table, n, head_major=True), "does not fit"),
         (lambda: call(h, h, cache, cache, table.long(), n), "page_table must"), (lambda: call(h, h, cache, cache, table, n[:2]), "lengths must"),
         (lambda: call(h, h, cache, cache, table[:2], n[:2]), "need starts"), (lambda: call(h, h, cache, cache, table, n, starts=n), "starts must"),
-        (lambda: call(h, h, cache, cache, table, n, q_out=h), "without q"), (lambda: call(h, h, cache, cache, table, n, positions=at), "need inv_freq"),
+        (lambda: call(h, h, cache, cache, table, n, positions=at), "need inv_freq"),
         (lambda: call(h, h, cache, cache, table, n), "current device"),
     ]
     for refused, message in cases:
