@@ -260,52 +260,80 @@ bmmc_status launch_sort(const SortShape& s, const void* ids_, int64_t n, int exp
 // ---- dispatch ----------------------------------------------------------------
 
 // How the words of the tokens' rows are dealt out: blocks of x * y threads
-// take y tokens and x * U words of each, U words a thread, x apart; gridDim.y
-// parts make up a row.
+// take y tokens and x words of each; gridDim.y parts make up a row.
 struct Cover {
     dim3 grid, block;
 };
 
-Cover cover(int64_t tokens, int words, int U, int most) {
-    const int need = (words + U - 1) / U;  // threads of a row
-    const int parts = (need + most - 1) / most;
-    const int x = ((need + parts - 1) / parts + 31) / 32 * 32;
+// Up to this many words (one for every thread of the machine) the blocks are
+// smaller, so that more of the machine takes part.
+constexpr int64_t kFewWords = 152 * 2048;
+
+Cover cover(int64_t tokens, int words, int most) {
+    const int parts = (words + most - 1) / most, need = (words + parts - 1) / parts;
+    int x = 4;
+    while (x < 32 && x < need) x <<= 1;
+    if (x < need) x = (need + 31) / 32 * 32;
     const int y = x >= most ? 1 : most / x;
     Cover c;
     c.block = dim3(x, y);
-    c.grid = dim3((unsigned)((tokens + y - 1) / y), (unsigned)((words + x * U - 1) / (x * U)));
+    c.grid = dim3((unsigned)((tokens + y - 1) / y), (unsigned)((words + x - 1) / x));
     return c;
 }
 
-// Fewer words than this many: one word a thread, so that the call is spread
-// over the machine and every load is in flight at once.
-constexpr int64_t kFewWords = 152 * 2048;
-
-// Pure movement: each word of a token's row is read once and written to the
-// rows of its choices.
-template <class Word, int U>
-__global__ void __launch_bounds__(256) dispatch_kernel(const char* __restrict__ x, int64_t x_stride,
-                                                       const int* __restrict__ slot, int64_t tokens, int choices,
-                                                       int64_t n_rows, int words, char* __restrict__ rows,
-                                                       int64_t row_stride) {
+// Pure movement: a token's row is read once and written to the rows of its
+// choices.
+template <class Word>
+__global__ void __launch_bounds__(256, 8) dispatch_kernel(const char* __restrict__ x, int64_t x_stride,
+                                                          const int* __restrict__ slot, int64_t tokens, int choices,
+                                                          int64_t n_rows, int words, char* __restrict__ rows,
+                                                          int64_t row_stride) {
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    const int w = blockIdx.y * blockDim.x * U + threadIdx.x;
+    const int w = blockIdx.y * blockDim.x + threadIdx.x;
     if (t >= tokens || w >= words) return;
-    const Word* from = reinterpret_cast<const Word*>(x + t * x_stride);
-    Word v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (w + u * (int)blockDim.x < words) v[u] = from[w + u * blockDim.x];
+    const Word v = __ldg(reinterpret_cast<const Word*>(x + t * x_stride) + w);
     slot += t * choices;
 #pragma unroll 4
     for (int k = 0; k < choices; ++k) {
         const int s = __ldg(slot + k);
         const int64_t row = s < 0 ? ~s : s;
+        if (row < n_rows) reinterpret_cast<Word*>(rows + row * row_stride)[w] = s < 0 ? Word{} : v;
+    }
+}
+
+// The same for rows at any element-aligned address.  Thread w holds the row's
+// aligned words w - 1 and w, whatever row they go to: of a row that lies
+// `to` bytes behind its granule (the source `from` bytes behind its own), the
+// words w - 1 and w cover granule w - 1 where from >= to, else granule w.
+template <class T>
+__global__ void __launch_bounds__(256, 6) dispatch_across_kernel(const char* __restrict__ x, int64_t x_stride,
+                                                                 const int* __restrict__ slot, int64_t tokens,
+                                                                 int choices, int64_t n_rows, int length,
+                                                                 char* __restrict__ rows, int64_t row_stride) {
+    constexpr int W = 16 / sizeof(T);
+    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int w = blockIdx.y * blockDim.x + threadIdx.x;
+    if (t >= tokens) return;
+    const char* const row_x = x + t * x_stride;
+    const int from = (int)((unsigned)reinterpret_cast<uintptr_t>(row_x) & 15u);
+    const int bytes = length * (int)sizeof(T);
+    uint4 a, b;  // bytes [w * 16 - 16 - from, + 32) of the row
+    load_if(w > 0 && w * 16 - 16 - from < bytes, a, row_x + (int64_t)w * 16 - 16 - from);
+    load_if(w * 16 - from < bytes, b, row_x + (int64_t)w * 16 - from);
+    slot += t * choices;
+#pragma unroll 2
+    for (int k = 0; k < choices; ++k) {
+        const int s = __ldg(slot + k);
+        const int64_t row = s < 0 ? ~s : s;
         if (row >= n_rows) continue;
-        Word* to = reinterpret_cast<Word*>(rows + row * row_stride);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (w + u * (int)blockDim.x < words) to[w + u * blockDim.x] = s < 0 ? Word{} : v[u];
+        char* const out = rows + row * row_stride;
+        const Walk<T, W, true> walk(length, out);
+        const int to = (int)((unsigned)reinterpret_cast<uintptr_t>(out) & 15u);
+        const int g = from >= to ? w - 1 : w;
+        if (g < 0 || !walk.in(g)) continue;
+        Pack<T, W> o;
+        o.word = s < 0 ? uint4{} : cut(a, b, (from - to) & 15);
+        walk.store(o, out, g);
     }
 }
 
@@ -317,124 +345,185 @@ __device__ __forceinline__ float weight_at(const void* weights, int in_f32, int6
     return in_f32 ? static_cast<const float*>(weights)[i] : to_f32(static_cast<const T*>(weights)[i]);
 }
 
-// Each thread holds the sums of U words in 32 bits, adds the choices in order,
-// KB of them loaded at a time, and rounds once.
-template <class T, int W, int U, int KB>
-__global__ void __launch_bounds__(256) combine_kernel(const char* __restrict__ rows, int64_t row_stride, int64_t n_rows,
+// Each thread holds the sums of a word in 32 bits, adds the choices in order,
+// KB of them loaded at a time, and rounds once.  A choice that is not there
+// adds zero times zero.
+template <class T, int W, int KB, bool ACROSS>
+__global__ void __launch_bounds__(256, KB > 2 ? 4 : ACROSS && sizeof(T) == 2 ? 6 : 8) combine_kernel(const char* __restrict__ rows, int64_t row_stride, int64_t n_rows,
                                                       const int* __restrict__ slot, const void* __restrict__ weights,
-                                                      int weights_f32, int64_t tokens, int choices, int words,
+                                                      int weights_f32, int64_t tokens, int choices, int length,
                                                       char* __restrict__ out, int64_t out_stride) {
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    const int w = blockIdx.y * blockDim.x * U + threadIdx.x;
-    if (t >= tokens || w >= words) return;
-    float sum[U][W];
+    const int w = blockIdx.y * blockDim.x + threadIdx.x;
+    if (t >= tokens) return;
+    char* const to = out + t * out_stride;
+    using Way = Walk<T, W, ACROSS>;
+    const Way walk(length, to);
+    if (!walk.in(w)) return;
+    float sum[W];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < W; ++i) sum[u][i] = 0.0f;
+    for (int i = 0; i < W; ++i) sum[i] = 0.0f;
     for (int k0 = 0; k0 < choices; k0 += KB) {
         int s[KB];
         float f[KB];
-        Pack<T, W> y[KB][U];
+        typename Way::Fetch y[KB];
 #pragma unroll
         for (int j = 0; j < KB; ++j) {
-            s[j] = k0 + j < choices ? slot[t * choices + k0 + j] : -1;
-            if (s[j] >= n_rows) s[j] = -1;
+            const bool there = k0 + j < choices;
+            const int64_t at = t * choices + k0 + j;
+            s[j] = there ? slot[at] : -1;
+            f[j] = there && weights ? weight_at<T>(weights, weights_f32, at) : 1.0f;
         }
 #pragma unroll
         for (int j = 0; j < KB; ++j) {
-            f[j] = 1.0f;
-            if (weights && s[j] >= 0) f[j] = weight_at<T>(weights, weights_f32, t * choices + k0 + j);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (s[j] >= 0 && w + u * (int)blockDim.x < words)
-                    y[j][u].load(rows + s[j] * row_stride + (int64_t)(w + u * (int)blockDim.x) * sizeof(y[j][u]));
+            const bool want = s[j] >= 0 && s[j] < n_rows;
+            walk.fetch(y[j], want, rows + s[j] * row_stride, w);
+            if (!want) f[j] = 0.0f;
         }
 #pragma unroll
-        for (int j = 0; j < KB; ++j)
-            if (s[j] >= 0)
+        for (int j = 0; j < KB; ++j) {
+            const Pack<T, W> v = walk.get(y[j]);
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int i = 0; i < W; ++i) sum[u][i] = fmaf(f[j], y[j][u].get(i), sum[u][i]);
+            for (int i = 0; i < W; ++i) sum[i] = fmaf(f[j], v.get(i), sum[i]);
+        }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (w + u * (int)blockDim.x < words) {
-            Pack<T, W> o;
-            o.set(sum[u]);
-            o.store(out + t * out_stride + (int64_t)(w + u * (int)blockDim.x) * sizeof(o));
-        }
+    Pack<T, W> o;
+    o.set(sum);
+    walk.store(o, to, w);
 }
 
-// grad_rows[slot] = w * grad and grad_weights = <rows[slot], grad>, a choice
-// after the other; the products are summed in 32 bits, by lanes and then
-// across them in a fixed order.
-template <class T, int W>
-__global__ void __launch_bounds__(256) combine_backward_kernel(
+// The sums of v[0..N) over groups of `lanes` lanes (a power of two), in a
+// fixed order; every lane gets all of them.
+template <int N>
+__device__ __forceinline__ void sum_lanes(float (&v)[N], int lanes) {
+    for (int d = lanes >> 1; d; d >>= 1)
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] += __shfl_xor_sync(~0u, v[j], d);
+}
+
+// grad_rows[slot] = w * grad and grad_weights = <rows[slot], grad>, KB choices
+// at a time; the products are summed in 32 bits, by lanes and then across
+// them in a fixed order.  x threads (a power of two, or whole warps) walk a
+// token's row.
+template <class T, int W, int KB, bool ACROSS>
+__global__ void __launch_bounds__(256, KB <= 2 ? 6 : 4) combine_backward_kernel(
     const char* __restrict__ grad, int64_t grad_stride, const char* __restrict__ rows, int64_t row_stride,
     int64_t n_rows, const int* __restrict__ slot, const void* __restrict__ weights, int weights_f32, int64_t tokens,
-    int choices, int words, char* __restrict__ grad_rows, int64_t grad_row_stride, void* __restrict__ grad_weights) {
-    __shared__ float s_part[8];
+    int choices, int length, char* __restrict__ grad_rows, int64_t grad_row_stride, void* __restrict__ grad_weights) {
+    __shared__ float s_part[8][KB];
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const bool live = t < tokens;
-    const int lane = threadIdx.x & 31, per = blockDim.x >> 5;
-    const int warp = threadIdx.y * per + (threadIdx.x >> 5);
-    for (int k = 0; k < choices; ++k) {
-        float dot = 0.0f;
-        if (live) {
-            const int s = slot[t * choices + k];
-            const int64_t row = s < 0 ? ~s : s;
-            const float f = s < 0 ? 0.0f : weight_at<T>(weights, weights_f32, t * choices + k);
-            if (row < n_rows)
-                for (int w = threadIdx.x; w < words; w += blockDim.x) {
-                    Pack<T, W> g, y, o;
-                    float v[W];
-                    g.load(grad + t * grad_stride + (int64_t)w * sizeof(g));
-                    if (s >= 0) {
-                        y.load(rows + row * row_stride + (int64_t)w * sizeof(y));
+    const int x = blockDim.x, tid = threadIdx.y * x + threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    using Way = Walk<T, W, ACROSS>;
+    constexpr int JB = ACROSS ? 1 : KB;  // choices whose words are in flight at once
+    const char* const g_row = grad + t * grad_stride;
+    for (int k0 = 0; k0 < choices; k0 += KB) {
+        float dot[KB];
+        int s[KB];
+        float f[KB];
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+            const bool there = live && k0 + j < choices;
+            const int64_t at = t * choices + k0 + j;
+            dot[j] = 0.0f;
+            s[j] = there ? slot[at] : -1 - (int)n_rows;
+            f[j] = there ? weight_at<T>(weights, weights_f32, at) : 0.0f;
+            if (s[j] < 0) f[j] = 0.0f;
+        }
+#pragma unroll
+        for (int j0 = 0; j0 < KB; j0 += JB) {
+            for (int w = threadIdx.x; w * W < length + (ACROSS ? W - 1 : 0); w += x) {
+                typename Way::Fetch fg[ACROSS ? JB : 1], fy[JB];
+                if (!ACROSS) Way(length, nullptr).fetch(fg[0], live, g_row, w);
+#pragma unroll
+                for (int j = 0; j < JB; ++j) {
+                    const int slot_j = s[j0 + j];
+                    const int64_t row = slot_j < 0 ? ~slot_j : slot_j;
+                    const Way walk(length, grad_rows + row * grad_row_stride);
+                    const bool want = slot_j >= 0 && row < n_rows && walk.in(w);
+                    if (ACROSS) walk.fetch(fg[j], want, g_row, w);
+                    walk.fetch(fy[j], want, rows + row * row_stride, w);
+                }
+#pragma unroll
+                for (int j = 0; j < JB; ++j) {
+                    const int slot_j = s[j0 + j];
+                    const int64_t row = slot_j < 0 ? ~slot_j : slot_j;
+                    char* const to = grad_rows + row * grad_row_stride;
+                    const Way walk(length, to);
+                    if (row >= n_rows || !walk.in(w)) continue;
+                    Pack<T, W> o;
+                    o.word = {};
+                    if (slot_j >= 0) {
+                        Pack<T, W> g = walk.get(fg[ACROSS ? j : 0]), y = walk.get(fy[j]);
+                        walk.trim(g, w);
+                        walk.trim(y, w);
+                        float v[W];
 #pragma unroll
                         for (int i = 0; i < W; ++i) {
-                            dot = fmaf(g.get(i), y.get(i), dot);
-                            v[i] = f * g.get(i);
+                            dot[j0 + j] = fmaf(g.get(i), y.get(i), dot[j0 + j]);
+                            v[i] = f[j0 + j] * g.get(i);
                         }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < W; ++i) v[i] = 0.0f;
+                        o.set(v);
                     }
-                    o.set(v);
-                    o.store(grad_rows + row * grad_row_stride + (int64_t)w * sizeof(o));
+                    walk.store(o, to, w);
                 }
+            }
         }
-        for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(~0u, dot, d);
-        if (lane == 0) s_part[warp] = dot;
-        __syncthreads();
-        if (live && threadIdx.x == 0) {
-            float sum = 0.0f;
-            for (int i = 0; i < per; ++i) sum += s_part[warp + i];
-            if (weights_f32) static_cast<float*>(grad_weights)[t * choices + k] = sum;
-            else static_cast<T*>(grad_weights)[t * choices + k] = from_f32<T>(sum);
+        sum_lanes(dot, x < 32 ? x : 32);
+        if (x > 32) {
+            if (k0) __syncthreads();
+            if (lane == 0)
+#pragma unroll
+                for (int j = 0; j < KB; ++j) s_part[warp][j] = dot[j];
+            __syncthreads();
+            const int first = threadIdx.y * (x >> 5);
+#pragma unroll
+            for (int j = 0; j < KB; ++j) {
+                dot[j] = 0.0f;
+                for (int i = 0; i < x >> 5; ++i) dot[j] += s_part[first + i][j];
+            }
         }
-        __syncthreads();
+        if (live && threadIdx.x == 0)
+#pragma unroll
+            for (int j = 0; j < KB; ++j)
+                if (k0 + j < choices) {
+                    const int64_t at = t * choices + k0 + j;
+                    if (weights_f32) static_cast<float*>(grad_weights)[at] = dot[j];
+                    else static_cast<T*>(grad_weights)[at] = from_f32<T>(dot[j]);
+                }
     }
 }
 
-// Calls f(T{}, elements per word) for the type and the word's width.
+// How rows of `hidden` elements are walked: in words of 16 or 8 bytes where
+// all addresses, strides and lengths (or'ed into `bits`, in bytes) are
+// multiples of them, else across the words' bounds.
+struct Way {
+    int bytes;   // 16, 8 or 0: across
+    int words;   // of a row; across: at most
+};
+
+Way way_of(int64_t hidden, int es, std::initializer_list<uint64_t> bits) {
+    const int wb = word_bytes(es, bits);
+    if (wb >= 8) return {wb, (int)(hidden * es / wb)};
+    const int W = 16 / es;
+    return {0, (int)((hidden + 2 * (W - 1)) / W)};
+}
+
+// Calls f(T{}, elements per word, across).
+template <class T, class F>
+void by_way(const Way& way, F&& f) {
+    constexpr int es = sizeof(T);
+    if (way.bytes == 16) f(T{}, std::integral_constant<int, 16 / es>{}, std::false_type{});
+    else if (way.bytes == 8) f(T{}, std::integral_constant<int, 8 / es>{}, std::false_type{});
+    else f(T{}, std::integral_constant<int, 16 / es>{}, std::true_type{});
+}
+
 template <class F>
-void by_type(int type, int bytes, F&& f) {
-    auto width = [&](auto t) {
-        constexpr int es = sizeof(t);
-        switch (bytes) {
-            case 16: f(t, std::integral_constant<int, 16 / es>{}); break;
-            case 8: f(t, std::integral_constant<int, 8 / es>{}); break;
-            case 4: f(t, std::integral_constant<int, 4 / es>{}); break;
-            default: f(t, std::integral_constant<int, 1>{}); break;
-        }
-    };
+void by_type(int type, const Way& way, F&& f) {
     switch (type) {
-        case BMMC_F32: width(float{}); break;
-        case BMMC_F16: width(__half{}); break;
-        default: width(__nv_bfloat16{}); break;
+        case BMMC_F32: by_way<float>(way, f); break;
+        case BMMC_F16: by_way<__half>(way, f); break;
+        default: by_way<__nv_bfloat16>(way, f); break;
     }
 }
 
@@ -510,25 +599,27 @@ bmmc_status expert_dispatch(const void* x, int64_t x_stride, const int32_t* slot
     const Rows in{x, tokens, x_stride * es, hidden * es}, out{rows, n_rows, row_stride * es, hidden * es};
     if (may_overlap(in, out) || may_overlap({slot, 1, 0, tokens * choices * 4}, out)) return BMMC_ERR_ALIAS;
     if ((s = all_reachable(checked, {x, slot, rows})) != BMMC_OK) return s;
-    const int wb = word_bytes(es, {(uint64_t)(uintptr_t)x, (uint64_t)(uintptr_t)rows, (uint64_t)(x_stride * es),
+    const Way way = way_of(hidden, es, {(uint64_t)(uintptr_t)x, (uint64_t)(uintptr_t)rows, (uint64_t)(x_stride * es),
                                    (uint64_t)(row_stride * es), (uint64_t)(hidden * es)});
-    const int words = (int)(hidden * es / wb);
+    const int words = way.words;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const char* from = static_cast<const char*>(x);
     char* to = static_cast<char*>(rows);
-    auto go = [&](auto word) {
-        using Word = decltype(word);
-        const bool few = tokens * words <= kFewWords;
-        const Cover c = few ? cover(tokens, words, 1, 128) : cover(tokens, words, 2, 256);
-        const auto kernel = few ? dispatch_kernel<Word, 1> : dispatch_kernel<Word, 2>;
-        kernel<<<c.grid, c.block, 0, st>>>(from, x_stride * es, slot, tokens, choices, n_rows, words, to, row_stride * es);
+    const int most = tokens * words <= kFewWords ? 128 : 256;
+    const auto copy = [&](auto word) {
+        const Cover c = cover(tokens, words, most);
+        dispatch_kernel<decltype(word)><<<c.grid, c.block, 0, st>>>(from, x_stride * es, slot, tokens, choices, n_rows, words,
+                                                                    to, row_stride * es);
     };
-    switch (wb) {
-        case 16: go(uint4{}); break;
-        case 8: go(uint2{}); break;
-        case 4: go(uint32_t{}); break;
-        default: go(uint16_t{}); break;
-    }
+    const auto across = [&](auto e) {
+        const Cover c = cover(tokens, words + 1, most);  // one more: thread 0 holds no word w - 1
+        dispatch_across_kernel<decltype(e)><<<c.grid, c.block, 0, st>>>(from, x_stride * es, slot, tokens, choices, n_rows,
+                                                                        (int)hidden, to, row_stride * es);
+    };
+    if (way.bytes == 16) copy(uint4{});
+    else if (way.bytes == 8) copy(uint2{});
+    else if (es == 4) across(uint32_t{});
+    else across(uint16_t{});
     return launched();
 }
 
@@ -551,19 +642,20 @@ bmmc_status expert_combine(const void* rows, int64_t row_stride, int64_t n_rows,
         may_overlap({slot, 1, 0, tokens * choices * 4}, to) || may_overlap({weights, 1, 0, tokens * choices * ws}, to))
         return BMMC_ERR_ALIAS;
     if ((s = all_reachable(checked, {rows, slot, weights, out})) != BMMC_OK) return s;
-    const int wb = word_bytes(es, {(uint64_t)(uintptr_t)rows, (uint64_t)(uintptr_t)out, (uint64_t)(row_stride * es),
+    const Way way = way_of(hidden, es, {(uint64_t)(uintptr_t)rows, (uint64_t)(uintptr_t)out, (uint64_t)(row_stride * es),
                                    (uint64_t)(out_stride * es), (uint64_t)(hidden * es)});
-    const int words = (int)(hidden * es / wb);
+    const int words = way.words;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    by_type(type, wb, [&](auto e, auto width) {
+    by_type(type, way, [&](auto e, auto width, auto across) {
         using T = decltype(e);
         constexpr int W = decltype(width)::value;
-        constexpr int U = W * sizeof(T) > 4 ? 2 : 4;  // short words: more of them in flight
-        const bool few = tokens * words <= kFewWords, two = choices <= 2;
-        const Cover c = cover(tokens, words, few ? 1 : two ? 2 * U : U, few ? 128 : 256);
-        const auto kernel = few ? combine_kernel<T, W, 1, 8> : two ? combine_kernel<T, W, 2 * U, 2> : combine_kernel<T, W, U, 4>;
+        constexpr bool A = decltype(across)::value;
+        const Cover c = cover(tokens, words, 128);
+        auto kernel = combine_kernel<T, W, 2, A>;
+        if constexpr (!A)
+            if (choices > 2) kernel = choices <= 4 ? combine_kernel<T, W, 4, A> : combine_kernel<T, W, 8, A>;
         kernel<<<c.grid, c.block, 0, st>>>(static_cast<const char*>(rows), row_stride * es, n_rows, slot, weights,
-                                          weight_type == BMMC_F32, tokens, choices, words, static_cast<char*>(out),
+                                          weight_type == BMMC_F32, tokens, choices, (int)hidden, static_cast<char*>(out),
                                           out_stride * es);
     });
     return launched();
@@ -595,20 +687,26 @@ bmmc_status expert_combine_backward(const void* grad, int64_t grad_stride, const
         if (may_overlap(r, gr) || may_overlap(r, gw)) return BMMC_ERR_ALIAS;
     if (may_overlap(gr, gw)) return BMMC_ERR_ALIAS;
     if ((s = all_reachable(checked, {grad, rows, slot, weights, grad_rows, grad_weights})) != BMMC_OK) return s;
-    const int wb = word_bytes(es, {(uint64_t)(uintptr_t)grad, (uint64_t)(uintptr_t)rows, (uint64_t)(uintptr_t)grad_rows,
+    const Way way = way_of(hidden, es, {(uint64_t)(uintptr_t)grad, (uint64_t)(uintptr_t)rows, (uint64_t)(uintptr_t)grad_rows,
                                    (uint64_t)(grad_stride * es), (uint64_t)(row_stride * es),
                                    (uint64_t)(grad_row_stride * es), (uint64_t)(hidden * es)});
-    const int words = (int)(hidden * es / wb);
+    const int words = way.words;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    int x = 32;
-    while (x < words && x < 256) x <<= 1;
+    const int most = choices <= 2 || !way.bytes ? 128 : 256;
+    int x = 4;
+    while (x < words && x < most) x <<= 1;
     const dim3 block(x, 256 / x);
     const unsigned blocks = (unsigned)((tokens + block.y - 1) / block.y);
-    by_type(type, wb, [&](auto e, auto width) {
-        combine_backward_kernel<decltype(e), decltype(width)::value><<<blocks, block, 0, st>>>(
-            static_cast<const char*>(grad), grad_stride * es, static_cast<const char*>(rows), row_stride * es, n_rows,
-            slot, weights, weight_type == BMMC_F32, tokens, choices, words, static_cast<char*>(grad_rows),
-            grad_row_stride * es, grad_weights);
+    by_type(type, way, [&](auto e, auto width, auto across) {
+        using T = decltype(e);
+        constexpr int W = decltype(width)::value;
+        constexpr bool A = decltype(across)::value;
+        auto kernel = combine_backward_kernel<T, W, 2, A>;
+        if constexpr (!A)
+            if (choices > 2) kernel = combine_backward_kernel<T, W, 4, A>;
+        kernel<<<blocks, block, 0, st>>>(static_cast<const char*>(grad), grad_stride * es, static_cast<const char*>(rows),
+                                        row_stride * es, n_rows, slot, weights, weight_type == BMMC_F32, tokens, choices,
+                                        (int)hidden, static_cast<char*>(grad_rows), grad_row_stride * es, grad_weights);
     });
     return launched();
 }

@@ -21,8 +21,10 @@ using namespace bmmc;
 
 namespace {
 
-constexpr int kThreads = 256;           // most threads of a block
+constexpr int kThreads = 128;           // threads of a block, at most (one token may take 256)
+constexpr int kMostThreads = 256;
 constexpr int kMaxTokensPerBlock = 64;
+constexpr int kHeadsAtOnce = 2;         // heads whose words a thread has in flight
 
 // Heads of one kind (queries, keys, values): where they lie and where they
 // go.  Strides in bytes.  place: 0 = the token's own place (dst_token apart),
@@ -120,7 +122,7 @@ __device__ __forceinline__ float turned_second(float x, float y, float2 r) { ret
 // memory, once for all heads; then a thread keeps those of its word of a head
 // in registers and walks over the heads, two at a time.
 template <class T, int W, bool ADJACENT>
-__global__ void __launch_bounds__(kThreads, 4) move_heads_kernel(const __grid_constant__ MoveParams p) {
+__global__ void __launch_bounds__(kMostThreads, 4) move_heads_kernel(const __grid_constant__ MoveParams p) {
     extern __shared__ float2 s_turn[];  // [tokens of the block][pairs] cos, sin
     __shared__ int64_t s_place[2][kMaxTokensPerBlock];  // byte offsets in the caches, -1 = none
     __shared__ float s_position[kMaxTokensPerBlock];
@@ -129,7 +131,15 @@ __global__ void __launch_bounds__(kThreads, 4) move_heads_kernel(const __grid_co
     const int nt = (int)min((int64_t)per_block, p.tokens - t0);
     // a block of a small call takes one part only
     const int first_part = gridDim.y > 1 ? blockIdx.y : 0, last_part = gridDim.y > 1 ? first_part + 1 : p.parts;
-    // The heads are on their way to L2 while the places and the turns are worked out.
+    // The first turn's frequency, and all the heads (to L2), are on their way
+    // while the places and the turns are worked out.
+    float first_freq = 0.0f;
+    int first_axis = 0;
+    if (tid < nt * p.pairs) {
+        const int pair = tid % p.pairs;
+        first_freq = p.freq[pair];
+        if (p.pair_axes) first_axis = p.pair_axes[pair];
+    }
     if (tid < nt * (last_part - first_part)) {
         const Heads& h = p.part[first_part + tid / nt];
         if (h.ahead)
@@ -154,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 4) move_heads_kernel(const __grid_co
     if (p.pairs && p.part[first_part].turned) {
         for (int i = tid; i < nt * p.pairs; i += threads) {
             const int k = i / p.pairs, pair = i - k * p.pairs;
-            const int axis = p.pair_axes ? p.pair_axes[pair] : 0;
+            const int axis = i == tid ? first_axis : p.pair_axes ? p.pair_axes[pair] : 0;
             float at = 0.0f;  // an axis that is not there does not turn
             if (!p.positions) {
                 if (axis == 0) at = s_position[k];
@@ -164,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 4) move_heads_kernel(const __grid_co
                                            : (float)static_cast<const int64_t*>(p.positions)[j];
             }
             float s, c;
-            sincosf(at * p.freq[pair], &s, &c);
+            sincosf(at * (i == tid ? first_freq : p.freq[pair]), &s, &c);
             s_turn[i] = make_float2(c, p.sign * s);
         }
         __syncthreads();
@@ -201,19 +211,18 @@ __global__ void __launch_bounds__(kThreads, 4) move_heads_kernel(const __grid_co
             if (turned)
 #pragma unroll
                 for (int i = 0; i < kTurns; ++i) r[i] = turn[j * kTurns + i];
-            for (int head = down; head < h.heads; head += 2 * step) {
-                const bool both = head + step < h.heads;
-                Pack<T, W> a[2], b[2];
+            for (int head = down; head < h.heads; head += kHeadsAtOnce * step) {
+                Pack<T, W> a[kHeadsAtOnce], b[kHeadsAtOnce];
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    if (u == 0 || both) {
+                for (int u = 0; u < kHeadsAtOnce; ++u)
+                    if (u == 0 || head + u * step < h.heads) {
                         const char* from = src + (head + u * step) * h.src_head + at;
                         a[u].load(from);
                         if (kTwo && turned) b[u].load(from + half);
                     }
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    if (u == 0 || both) {
+                for (int u = 0; u < kHeadsAtOnce; ++u)
+                    if (u == 0 || head + u * step < h.heads) {
                         char* out = dst + (head + u * step) * h.dst_head + at;
                         if (turned) {
                             float x[W], y[W];
@@ -258,9 +267,8 @@ int deal_out(MoveParams& p, const int (&dims)[3], int W, int es, bool adjacent, 
     int full = 2, group;
     while (full < 8 && (1 << full) < most) ++full;
     const bool small = (p.tokens << full) <= 152 * 1024;
-    group = small ? full : std::max(2, full - 2);
-    if (!small && most > 1024) group = 8;
-    int threads = small ? std::max(64, 1 << group) : kThreads;
+    group = small ? std::min(full, 7) : most > 1024 ? full : std::max(2, full - 2);
+    int threads = small ? std::max(64, 1 << group) : std::max(kThreads, 1 << group);
     while ((threads >> group) > kMaxTokensPerBlock) ++group;
     while ((threads >> group) > 1 && (threads >> group) * p.pairs * sizeof(float2) > 32 * 1024) ++group;
     p.group_log2 = group;
