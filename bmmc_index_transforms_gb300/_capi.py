@@ -81,7 +81,7 @@ class LmadCopyInfo(ctypes.Structure):
 
 # bmmc_dtype
 F32, F16, BF16 = range(3)
-POINTERS_CHECKED = 0x100
+DEVICE_POINTERS = 0x100
 EXPERT_MAX_CHOICES = 64
 # rotary_turns_t.flags
 ROTARY_ADJACENT, ROTARY_INVERSE = 0x1, 0x2

@@ -561,7 +561,7 @@ bmmc_status expert_sort(const void* ids, int id_bytes, int64_t tokens, int choic
     size_t need = 0;
     bmmc_status s = expert_sort_workspace(tokens, choices, experts, &need);
     if (s != BMMC_OK) return s;
-    const bool checked = pointers_checked(id_bytes);
+    const bool device = device_pointers(id_bytes);
     if (id_bytes != 4 && id_bytes != 8) return BMMC_ERR_UNSUPPORTED_ELEM;
     const int64_t n = tokens * choices;
     if (!offsets || (n && (!ids || !slot || !source))) return BMMC_ERR_INVALID_ARG;
@@ -577,7 +577,7 @@ bmmc_status expert_sort(const void* ids, int id_bytes, int64_t tokens, int choic
         for (int j = 0; j < i; ++j)
             if (may_overlap(o[i], o[j])) return BMMC_ERR_ALIAS;
     }
-    if ((s = all_reachable(checked, {ids, slot, source, offsets, need ? workspace : nullptr})) != BMMC_OK) return s;
+    if ((s = all_reachable(device, {ids, slot, source, offsets, need ? workspace : nullptr})) != BMMC_OK) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int* counts = static_cast<int*>(need ? workspace : nullptr);
     const SortShape shape = sort_shape(n, experts);
@@ -589,7 +589,7 @@ bmmc_status expert_sort(const void* ids, int id_bytes, int64_t tokens, int choic
 bmmc_status expert_dispatch(const void* x, int64_t x_stride, const int32_t* slot, int64_t tokens, int choices,
                             int64_t hidden, int type, void* rows, int64_t row_stride, int64_t n_rows, void* stream) {
     int es = 0;
-    const bool checked = pointers_checked(type);
+    const bool device = device_pointers(type);
     bmmc_status s = check_moves(tokens, choices, hidden, n_rows, type, &es);
     if (s != BMMC_OK) return s;
     if (bad_stride(x_stride, 0, tokens) || bad_stride(row_stride, hidden, n_rows)) return BMMC_ERR_INVALID_ARG;
@@ -598,7 +598,7 @@ bmmc_status expert_dispatch(const void* x, int64_t x_stride, const int32_t* slot
     if (misaligned(x, es) || misaligned(rows, es) || misaligned(slot, 4)) return BMMC_ERR_MISALIGNED;
     const Rows in{x, tokens, x_stride * es, hidden * es}, out{rows, n_rows, row_stride * es, hidden * es};
     if (may_overlap(in, out) || may_overlap({slot, 1, 0, tokens * choices * 4}, out)) return BMMC_ERR_ALIAS;
-    if ((s = all_reachable(checked, {x, slot, rows})) != BMMC_OK) return s;
+    if ((s = all_reachable(device, {x, slot, rows})) != BMMC_OK) return s;
     const Way way = way_of(hidden, es, {(uint64_t)(uintptr_t)x, (uint64_t)(uintptr_t)rows, (uint64_t)(x_stride * es),
                                    (uint64_t)(row_stride * es), (uint64_t)(hidden * es)});
     const int words = way.words;
@@ -627,7 +627,7 @@ bmmc_status expert_combine(const void* rows, int64_t row_stride, int64_t n_rows,
                            const void* weights, int weight_type, int64_t tokens, int choices, int64_t hidden, int type,
                            void* out, int64_t out_stride, void* stream) {
     int es = 0;
-    const bool checked = pointers_checked(type);
+    const bool device = device_pointers(type);
     bmmc_status s = check_moves(tokens, choices, hidden, n_rows, type, &es);
     if (s != BMMC_OK) return s;
     if (weights && weight_type != BMMC_F32 && weight_type != type) return BMMC_ERR_UNSUPPORTED_ELEM;
@@ -641,7 +641,7 @@ bmmc_status expert_combine(const void* rows, int64_t row_stride, int64_t n_rows,
     if (may_overlap({rows, n_rows, row_stride * es, hidden * es}, to) ||
         may_overlap({slot, 1, 0, tokens * choices * 4}, to) || may_overlap({weights, 1, 0, tokens * choices * ws}, to))
         return BMMC_ERR_ALIAS;
-    if ((s = all_reachable(checked, {rows, slot, weights, out})) != BMMC_OK) return s;
+    if ((s = all_reachable(device, {rows, slot, weights, out})) != BMMC_OK) return s;
     const Way way = way_of(hidden, es, {(uint64_t)(uintptr_t)rows, (uint64_t)(uintptr_t)out, (uint64_t)(row_stride * es),
                                    (uint64_t)(out_stride * es), (uint64_t)(hidden * es)});
     const int words = way.words;
@@ -666,7 +666,7 @@ bmmc_status expert_combine_backward(const void* grad, int64_t grad_stride, const
                                     int64_t tokens, int choices, int64_t hidden, int type, void* grad_rows,
                                     int64_t grad_row_stride, void* grad_weights, void* stream) {
     int es = 0;
-    const bool checked = pointers_checked(type);
+    const bool device = device_pointers(type);
     bmmc_status s = check_moves(tokens, choices, hidden, n_rows, type, &es);
     if (s != BMMC_OK) return s;
     if (weight_type != BMMC_F32 && weight_type != type) return BMMC_ERR_UNSUPPORTED_ELEM;
@@ -686,7 +686,7 @@ bmmc_status expert_combine_backward(const void* grad, int64_t grad_stride, const
     for (const Rows& r : in)
         if (may_overlap(r, gr) || may_overlap(r, gw)) return BMMC_ERR_ALIAS;
     if (may_overlap(gr, gw)) return BMMC_ERR_ALIAS;
-    if ((s = all_reachable(checked, {grad, rows, slot, weights, grad_rows, grad_weights})) != BMMC_OK) return s;
+    if ((s = all_reachable(device, {grad, rows, slot, weights, grad_rows, grad_weights})) != BMMC_OK) return s;
     const Way way = way_of(hidden, es, {(uint64_t)(uintptr_t)grad, (uint64_t)(uintptr_t)rows, (uint64_t)(uintptr_t)grad_rows,
                                    (uint64_t)(grad_stride * es), (uint64_t)(row_stride * es),
                                    (uint64_t)(grad_row_stride * es), (uint64_t)(hidden * es)});

@@ -44,6 +44,7 @@ struct MoveParams {
     int parts;
     int64_t tokens;
     int group_log2;  // threads of a token
+    bool device;     // the heads are the device's own memory and may be fetched ahead
     // rotation
     const void* positions;  // NULL: the token's place in its sequence
     int position_bytes, axes, pairs;
@@ -97,12 +98,14 @@ __device__ Place place_of(const MoveParams& p, int64_t t, int64_t b) {
     Place r{0, {-1, -1}};
     int64_t first = t;
     if (p.starts) {
-        if (b < 0 || t >= p.starts[b + 1]) return r;
+        if (b < 0) return r;
         first = p.starts[b];
     } else if (t >= p.sequences) {
         return r;
     }
-    r.at = (int64_t)p.lengths[b] + (t - first);
+    const int length = p.lengths[b], next = p.starts ? p.starts[b + 1] : 0;  // on their way together
+    if (p.starts && t >= next) return r;
+    r.at = (int64_t)length + (t - first);
     if (r.at < 0 || r.at >= (int64_t)1 << 32) return r;  // (more only by starts below zero)
     const unsigned at = (unsigned)r.at, column = at / p.page_size;
     if (column >= p.table_columns) return r;
@@ -131,15 +134,28 @@ __global__ void __launch_bounds__(kMostThreads, 4) move_heads_kernel(const __gri
     const int nt = (int)min((int64_t)per_block, p.tokens - t0);
     // a block of a small call takes one part only
     const int first_part = gridDim.y > 1 ? blockIdx.y : 0, last_part = gridDim.y > 1 ? first_part + 1 : p.parts;
-    // The first turn's frequency, and all the heads (to L2), are on their way
-    // while the places and the turns are worked out.
-    float first_freq = 0.0f;
-    int first_axis = 0;
-    if (tid < nt * p.pairs) {
-        const int pair = tid % p.pairs;
-        first_freq = p.freq[pair];
-        if (p.pair_axes) first_axis = p.pair_axes[pair];
-    }
+    const bool turning = p.pairs && p.part[first_part].turned;
+    // A thread's first turns (what they need but for a position that follows
+    // from the place), and all the heads (to L2), are on their way while the
+    // places are worked out.
+    constexpr int kAhead = 2;
+    float freq[kAhead] = {}, position[kAhead] = {};
+    bool by_place[kAhead] = {};
+    const auto start_turn = [&](int i, float& f, float& at, bool& from_place) {
+        const int k = i / p.pairs, pair = i - k * p.pairs;
+        const int axis = p.pair_axes ? p.pair_axes[pair] : 0;
+        f = p.freq[pair];
+        at = 0.0f;  // an axis that is not there does not turn
+        from_place = !p.positions && axis == 0;
+        if (p.positions && axis >= 0 && axis < p.axes) {
+            const int64_t j = axis * p.axis_stride + t0 + k;
+            at = p.position_bytes == 4 ? (float)static_cast<const int32_t*>(p.positions)[j]
+                                       : (float)static_cast<const int64_t*>(p.positions)[j];
+        }
+    };
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+        if (turning && tid + u * threads < nt * p.pairs) start_turn(tid + u * threads, freq[u], position[u], by_place[u]);
     if (tid < nt * (last_part - first_part)) {
         const Heads& h = p.part[first_part + tid / nt];
         if (h.ahead)
@@ -159,26 +175,26 @@ __global__ void __launch_bounds__(kMostThreads, 4) move_heads_kernel(const __gri
             const Place r = place_of(p, t, p.starts ? find_sequence(p.starts, p.sequences, t) : t);
             s_place[0][tid] = r.byte[0], s_place[1][tid] = r.byte[1], s_position[tid] = (float)r.at;
         }
-        __syncthreads();
+        if (!p.positions) __syncthreads();
     }
-    if (p.pairs && p.part[first_part].turned) {
-        for (int i = tid; i < nt * p.pairs; i += threads) {
-            const int k = i / p.pairs, pair = i - k * p.pairs;
-            const int axis = i == tid ? first_axis : p.pair_axes ? p.pair_axes[pair] : 0;
-            float at = 0.0f;  // an axis that is not there does not turn
-            if (!p.positions) {
-                if (axis == 0) at = s_position[k];
-            } else if (axis >= 0 && axis < p.axes) {
-                const int64_t j = axis * p.axis_stride + t0 + k;
-                at = p.position_bytes == 4 ? (float)static_cast<const int32_t*>(p.positions)[j]
-                                           : (float)static_cast<const int64_t*>(p.positions)[j];
-            }
+    if (turning) {
+        const auto end_turn = [&](int i, float f, float at, bool from_place) {
+            if (from_place) at = s_position[i / p.pairs];
             float s, c;
-            sincosf(at * (i == tid ? first_freq : p.freq[pair]), &s, &c);
+            sincosf(at * f, &s, &c);
             s_turn[i] = make_float2(c, p.sign * s);
+        };
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (tid + u * threads < nt * p.pairs) end_turn(tid + u * threads, freq[u], position[u], by_place[u]);
+        for (int i = tid + kAhead * threads; i < nt * p.pairs; i += threads) {
+            float f, at;
+            bool from_place;
+            start_turn(i, f, at, from_place);
+            end_turn(i, f, at, from_place);
         }
-        __syncthreads();
     }
+    __syncthreads();
     const int k = tid >> p.group_log2, in = tid & ((1 << p.group_log2) - 1);
     if (k >= nt) return;
     for (int q = first_part; q < last_part; ++q) {
@@ -276,8 +292,8 @@ int deal_out(MoveParams& p, const int (&dims)[3], int W, int es, bool adjacent, 
         Heads& h = p.part[q];
         h.across = std::min(h.items, 1 << group);
         h.magic = (65536 + h.across - 1) / h.across;
-        const bool dense = W * es == 16 && (h.heads < 2 || h.src_head == (int64_t)dims[q] * es);
-        h.ahead = dense ? (unsigned)(h.heads * dims[q] * es) : 0u;
+        const bool dense = p.device && W * es == 16 && (h.heads < 2 || h.src_head == (int64_t)dims[q] * es);
+        h.ahead = dense ? std::min((unsigned)(h.heads * dims[q] * es), 65536u) : 0u;
     }
     *split = p.parts > 1 && p.tokens / (threads >> group) * p.parts * threads <= 152 * 1024;
     return threads;
@@ -347,7 +363,7 @@ uint64_t address_bits(const token_heads_t& x, int es) {
 }
 
 // The rotation's arguments, checked and put into p.
-bmmc_status set_turns(MoveParams& p, const rotary_turns_t& r, bool checked, bool need_positions) {
+bmmc_status set_turns(MoveParams& p, const rotary_turns_t& r, bool device, bool need_positions) {
     p.pairs = 0;
     if (r.flags & ~(int64_t)(ROTARY_ADJACENT | ROTARY_INVERSE)) return BMMC_ERR_INVALID_ARG;
     if (!r.inv_freq) return r.pairs || r.positions || r.pair_axes ? BMMC_ERR_INVALID_ARG : BMMC_OK;
@@ -366,7 +382,7 @@ bmmc_status set_turns(MoveParams& p, const rotary_turns_t& r, bool checked, bool
     p.freq = r.inv_freq;
     p.pair_axes = r.pair_axes;
     p.sign = r.flags & ROTARY_INVERSE ? -1.0f : 1.0f;
-    return all_reachable(checked, {r.inv_freq, r.pair_axes, r.positions});
+    return all_reachable(device, {r.inv_freq, r.pair_axes, r.positions});
 }
 
 // The bits that a word's size has to divide on account of the pairs.
@@ -391,7 +407,7 @@ extern "C" {
 bmmc_status rotary(const rotary_args_t* a, void* stream) {
     if (!a || a->tokens < 0 || a->tokens > kMaxTokens) return BMMC_ERR_INVALID_ARG;
     int type = a->type < 0 || a->type > 0xfff ? -1 : (int)a->type;
-    const bool checked = pointers_checked(type);
+    const bool device = device_pointers(type);
     const int es = dtype_bytes(type);
     if (!es) return BMMC_ERR_UNSUPPORTED_ELEM;
     if (!a->tokens) return BMMC_OK;
@@ -404,8 +420,9 @@ bmmc_status rotary(const rotary_args_t* a, void* stream) {
     if (!same_place(a->x, a->out, a->tokens) && may_overlap(rows_of(a->x, a->tokens, es), rows_of(a->out, a->tokens, es)))
         return BMMC_ERR_ALIAS;
     MoveParams p{};
-    if ((s = set_turns(p, a->turns, checked, true)) != BMMC_OK) return s;
-    if ((s = all_reachable(checked, {a->x.data, a->out.data})) != BMMC_OK) return s;
+    if ((s = set_turns(p, a->turns, device, true)) != BMMC_OK) return s;
+    if ((s = all_reachable(device, {a->x.data, a->out.data})) != BMMC_OK) return s;
+    p.device = device;
     p.parts = 1;
     p.part[0] = heads_of(a->x, es, 1);
     p.part[0].dst = static_cast<char*>(a->out.data);
@@ -420,7 +437,7 @@ bmmc_status rotary(const rotary_args_t* a, void* stream) {
 bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
     if (!a || a->tokens < 0 || a->tokens > kMaxTokens) return BMMC_ERR_INVALID_ARG;
     int type = a->type < 0 || a->type > 0xfff ? -1 : (int)a->type;
-    const bool checked = pointers_checked(type);
+    const bool device = device_pointers(type);
     const int es = dtype_bytes(type);
     if (!es) return BMMC_ERR_UNSUPPORTED_ELEM;
     if (!a->tokens) return BMMC_OK;
@@ -444,6 +461,7 @@ bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
     const token_heads_t* from[2] = {&a->k, &a->v};
     Rows cache_rows[2];
     MoveParams p{};
+    p.device = device;
     uint64_t bits = 0;
     for (int c = 0; c < 2; ++c) {
         const paged_cache_t& m = *cache[c];
@@ -471,8 +489,8 @@ bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
             (!same_place(a->q, a->q_out, a->tokens) && may_overlap(q, to)))
             return BMMC_ERR_ALIAS;
     }
-    if ((s = set_turns(p, a->turns, checked, false)) != BMMC_OK) return s;
-    if ((s = all_reachable(checked, {a->k.data, a->v.data, a->q.data, a->q_out.data, a->k_cache.data, a->v_cache.data, a->starts,
+    if ((s = set_turns(p, a->turns, device, false)) != BMMC_OK) return s;
+    if ((s = all_reachable(device, {a->k.data, a->v.data, a->q.data, a->q_out.data, a->k_cache.data, a->v_cache.data, a->starts,
                             a->lengths, a->table})) != BMMC_OK)
         return s;
     for (int c = 0; c < 2; ++c) {

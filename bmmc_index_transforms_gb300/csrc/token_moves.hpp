@@ -73,14 +73,14 @@ inline int word_bytes(int elem, std::initializer_list<uint64_t> all) {
 }
 
 // Takes the flag off a call's type (or width of ids).
-inline bool pointers_checked(int& type) {
-    const bool checked = type >= 0 && (type & BMMC_POINTERS_CHECKED);
-    if (checked) type &= ~BMMC_POINTERS_CHECKED;
-    return checked;
+inline bool device_pointers(int& type) {
+    const bool device = type >= 0 && (type & BMMC_DEVICE_POINTERS);
+    if (device) type &= ~BMMC_DEVICE_POINTERS;
+    return device;
 }
 
-inline bmmc_status all_reachable(bool checked, std::initializer_list<const void*> ps) {
-    if (checked) return BMMC_OK;
+inline bmmc_status all_reachable(bool device, std::initializer_list<const void*> ps) {
+    if (device) return BMMC_OK;
     for (const void* p : ps)
         if (p) {
             const bmmc_status s = pointer_reachable(p);

@@ -21,11 +21,11 @@ from . import _capi
 __all__ = ["expert_sort", "expert_dispatch", "expert_combine", "expert_combine_backward", "rotary", "paged_append"]
 
 _torch = _empty = _library = _raw_stream = _current_device = _int32 = _int64 = _float32 = None
-_types = {}       # torch dtype -> bmmc_dtype, with the pointers known to be the device's
+_types = {}       # torch dtype -> bmmc_dtype, with the flag of device pointers
 _widths = {}      # integer torch dtype -> its bytes
 _workspaces = {}  # (tokens, choices, experts) -> bytes that expert_sort asks for
-_CHECKED = _capi.POINTERS_CHECKED
-_F32 = _capi.F32 | _CHECKED
+_DEVICE = _capi.DEVICE_POINTERS
+_F32 = _capi.F32 | _DEVICE
 
 
 def _setup():
@@ -33,7 +33,7 @@ def _setup():
     global _torch, _empty, _library, _raw_stream, _current_device, _int32, _int64, _float32
     import torch
 
-    _types.update({torch.float32: _F32, torch.float16: _capi.F16 | _CHECKED, torch.bfloat16: _capi.BF16 | _CHECKED})
+    _types.update({torch.float32: _F32, torch.float16: _capi.F16 | _DEVICE, torch.bfloat16: _capi.BF16 | _DEVICE})
     _int32, _int64, _float32 = torch.int32, torch.int64, torch.float32
     _widths.update({_int32: 4, _int64: 8})
     _empty, _current_device = torch.empty, torch.cuda.current_device
@@ -50,8 +50,8 @@ def _no(where: str, message: str):
 
 def _stream(device: int, stream, where: str, *tensors) -> int:
     """The stream to launch on, given the first tensor's device; every tensor
-    has to be on the current device, where the library launches.  (It is
-    asked with the pointers checked: none but the device's get past here.)"""
+    has to be on the current device, where the library launches (and which it
+    is told: it does not ask for the pointers again)."""
     if device < 0 or device != _current_device():
         _no(where, f"a tensor is on {'the host' if device < 0 else f'cuda:{device}'}, not on the current device")
     for x in tensors:
@@ -132,7 +132,7 @@ def expert_sort(experts, num_experts: int, stream=None):
         work_ptr = work.data_ptr()
         if stream is not None:  # it is given back when this call returns, and stays that stream's until the work is done
             work.record_stream(_torch.cuda.ExternalStream(st) if isinstance(stream, int) else stream)
-    status = _library.expert_sort(experts.data_ptr(), width | _CHECKED, T, K, num_experts, slot.data_ptr(),
+    status = _library.expert_sort(experts.data_ptr(), width | _DEVICE, T, K, num_experts, slot.data_ptr(),
                                   source.data_ptr(), offsets.data_ptr(), work_ptr, need, st)
     if status:
         _check(status, where)
@@ -173,7 +173,7 @@ def _weights(weights, slot, rows, where: str) -> int:
         _no(where, "weights must be a contiguous tensor of slot's shape")
     if weights.dtype is not _float32 and weights.dtype != rows.dtype:
         _no(where, "weights must be float32 or of the rows' type")
-    return _types[weights.dtype] & ~_CHECKED
+    return _types[weights.dtype] & ~_DEVICE
 
 
 def expert_combine(rows, slot, weights=None, out=None, stream=None):

@@ -556,9 +556,10 @@ typedef enum {
 } bmmc_dtype;
 
 /* Or'ed into `type` (into `id_bytes` of expert_sort): the caller has made sure
- * that the GPU can reach every pointer, and none of them is asked for, which
- * takes 0.4 us of a call's host time for each. */
-#define BMMC_POINTERS_CHECKED 0x100
+ * that every pointer is memory of the current device.  None of them is asked
+ * for, which takes 0.4 us of a call's host time for each, and the kernels may
+ * fetch their inputs ahead. */
+#define BMMC_DEVICE_POINTERS 0x100
 
 #define EXPERT_MAX_CHOICES 64
 
