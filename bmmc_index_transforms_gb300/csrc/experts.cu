@@ -9,6 +9,7 @@
 // map stays a permutation and every row of the sorted array has one writer.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -109,25 +110,42 @@ __device__ __forceinline__ void sum_counts(const int* counts, int pitch, int* ba
     }
 }
 
+// The lanes with the same key, from one ballot for each bit of the keys
+// (`bits` of them); faster here than the match instruction, whose rate is one
+// in about 30 cycles.
+__device__ __forceinline__ unsigned same_key(int key, int bits) {
+    unsigned same = ~0u;
+    for (int b = 0; b < bits; ++b) {
+        const bool one = (key >> b) & 1;
+        const unsigned ones = __ballot_sync(~0u, one);
+        same &= one ? ones : ~ones;
+    }
+    return same;
+}
+
 // Each block numbers its part, a tile of blockDim.x * R choices at a time.
-// Inside a warp a choice's rank among equal keys comes from a match of the
-// 32 keys of a round plus the warp's running count of that key; a column sum
+// Inside a warp a choice's rank among equal keys comes from the lanes of a
+// round with its key plus the warp's running count of that key; a column sum
 // over the warps and the block's start for the key complete its place.  The
 // starts come from the counts of all blocks, or (counts == NULL: one block
 // and one tile) from the tile itself.  Integer sums: the result does not
 // depend on timing.  The first tile is ranked before the counts are waited
-// for, so that this work runs beside the count kernel.
+// for, so that this work runs beside the count kernel; a tile of many blocks
+// is put in order in shared memory, so that source is written in runs.
 template <class Id, int R>
 __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__ ids, int64_t n, int experts,
-                                                          int64_t per_block, int pitch, const int* counts,
+                                                          int64_t per_block, int pitch, int bits, const int* counts,
                                                           int* __restrict__ slot, int* __restrict__ source,
                                                           int* __restrict__ offsets) {
     extern __shared__ int s_mem[];
-    const int keys = experts + 1, warps = blockDim.x >> 5;
-    int* base = s_mem;          // [pitch] where the block's next choice of each key goes
-    int* total = base + pitch;  // [pitch] choices of the tile
-    int* tmp = total + pitch;   // [32]
-    int* hist = tmp + 32;       // [warps][keys] counts of the tile, then starts inside it
+    const int keys = experts + 1, warps = blockDim.x >> 5, none = (1 << bits) - 1;
+    int* base = s_mem;           // [pitch] where the block's next choice of each key goes
+    int* total = base + pitch;   // [pitch] choices of the tile
+    int* start = total + pitch;  // [pitch] the tile's first choice of each key, in order (counts only)
+    int* tmp = start + pitch;    // [32]
+    int* hist = tmp + 32;        // [warps][keys] counts of the tile, then starts inside the key
+    int* order = hist + warps * keys;                                        // [blockDim.x * R] the tile in order,
+    unsigned short* order_key = reinterpret_cast<unsigned short*>(order + blockDim.x * R);  // and its keys (counts only)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int* mine = hist + warp * keys;
     const int64_t lo = (int64_t)blockIdx.x * per_block, hi = min(n, lo + per_block);
@@ -137,17 +155,18 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int64_t i = at + ((int64_t)warp * R + r) * 32 + lane;
-            key[r] = i < hi ? key_of(ids[i], experts) : -1;
+            key[r] = i < hi ? key_of(ids[i], experts) : none;  // none: a key past all others
         }
         for (int e = lane; e < keys; e += 32) mine[e] = 0;
         __syncwarp();
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const unsigned same = __match_any_sync(~0u, key[r]);
-            const int before = key[r] < 0 ? 0 : mine[key[r]];
+            const unsigned same = same_key(key[r], bits);
+            const bool there = key[r] < keys;
+            const int before = there ? mine[key[r]] : 0;
             rank[r] = before + __popc(same & ((1u << lane) - 1));
             __syncwarp();
-            if (key[r] >= 0 && lane == __ffs(same) - 1) mine[key[r]] = before + __popc(same);
+            if (there && lane == __ffs(same) - 1) mine[key[r]] = before + __popc(same);
             __syncwarp();
         }
         if (counts && at == lo) {
@@ -165,37 +184,50 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__
         __syncthreads();
         for (int e = threadIdx.x; e < keys; e += blockDim.x) {
             int run = 0;
+#pragma unroll 4
             for (int w = 0; w < warps; ++w) {
                 const int c = hist[w * keys + e];
                 hist[w * keys + e] = run;
                 run += c;
             }
             total[e] = run;
-            if (!counts) base[e] = run;
+            (counts ? start : base)[e] = run;
         }
         __syncthreads();
-        if (!counts) {
-            block_exclusive_scan(base, keys, tmp);
+        block_exclusive_scan(counts ? start : base, keys, tmp);
+        if (!counts)
             for (int e = threadIdx.x; e < keys; e += blockDim.x) offsets[e] = base[e];
-        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            if (key[r] < 0) continue;
-            const int64_t i = at + ((int64_t)warp * R + r) * 32 + lane;
-            const int to = base[key[r]] + mine[key[r]] + rank[r];
+            if (key[r] >= keys) continue;
+            const int in_tile = ((warp * R) + r) * 32 + lane, in_key = mine[key[r]] + rank[r];
+            const int64_t i = at + in_tile;
+            const int to = base[key[r]] + in_key;
             const bool routed = key[r] < experts;
             slot[i] = routed ? to : ~to;
-            if ((unsigned)to < (unsigned)n) source[to] = routed ? (int)i : ~(int)i;  // also if ids changed meanwhile
+            if (counts) {
+                order[start[key[r]] + in_key] = in_tile;
+                order_key[start[key[r]] + in_key] = (unsigned short)key[r];
+            } else {
+                source[to] = routed ? (int)i : ~(int)i;
+            }
+        }
+        if (!counts) return;
+        __syncthreads();
+        const int here = (int)min((int64_t)blockDim.x * R, hi - at);
+        for (int j = threadIdx.x; j < here; j += blockDim.x) {
+            const int k = order_key[j], i = (int)at + order[j], to = base[k] + j - start[k];
+            if ((unsigned)to < (unsigned)n) source[to] = k < experts ? i : ~i;  // also if ids changed meanwhile
         }
         at += (int64_t)blockDim.x * R;
-        if (at >= hi) break;
+        if (at >= hi) return;
         __syncthreads();
         for (int e = threadIdx.x; e < keys; e += blockDim.x) base[e] += total[e];
     } while (true);
 }
 
 struct SortShape {
-    int warps, blocks, rounds, pitch;
+    int warps, blocks, rounds, pitch, bits;
     int64_t per_block;
     size_t smem;  // of the place kernel
 };
@@ -208,7 +240,11 @@ constexpr size_t kSortSmem = 200 * 1024;
 SortShape sort_shape(int64_t n, int experts) {
     SortShape s;
     s.pitch = (experts + 4) & ~3;
-    const auto smem = [&](int warps) { return ((size_t)warps * (experts + 1) + 2 * s.pitch + 32) * sizeof(int); };
+    s.bits = 1;  // of the keys 0 .. experts and one past them
+    while ((1 << s.bits) < experts + 2) ++s.bits;
+    const auto smem = [&](int warps) {
+        return ((size_t)warps * (experts + 1) + 3 * s.pitch + 32) * sizeof(int) + (size_t)warps * 32 * kSortRounds * 6;
+    };
     s.warps = 32;
     while (smem(s.warps) > kSortSmem) s.warps >>= 1;
     s.rounds = n <= s.warps * 32 ? 1 : kSortRounds;
@@ -227,14 +263,24 @@ bmmc_status launch_sort(const SortShape& s, const void* ids_, int64_t n, int exp
                         int32_t* offsets, int* counts, cudaStream_t st) {
     const Id* ids = static_cast<const Id*>(ids_);
     const auto place = sort_place_kernel<Id, R>;
-    if (s.smem > 48 * 1024 &&
-        cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSortSmem) != cudaSuccess) {
-        cudaGetLastError();
-        return BMMC_ERR_CUDA;
+    if (s.smem > 48 * 1024) {
+        static std::atomic<uint64_t> allowed{0};  // devices that were told, bit by bit (others are told every time)
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) {
+            cudaGetLastError();
+            return BMMC_ERR_CUDA;
+        }
+        if (dev >= 64 || !(allowed.load(std::memory_order_relaxed) >> dev & 1)) {
+            if (cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSortSmem) != cudaSuccess) {
+                cudaGetLastError();
+                return BMMC_ERR_CUDA;
+            }
+            if (dev < 64) allowed.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+        }
     }
     const int* none = nullptr;
     if (s.blocks == 1) {
-        place<<<1, s.warps * 32, s.smem, st>>>(ids, n, experts, s.per_block, s.pitch, none, slot, source, offsets);
+        place<<<1, s.warps * 32, s.smem, st>>>(ids, n, experts, s.per_block, s.pitch, s.bits, none, slot, source, offsets);
         return launched();
     }
     sort_count_kernel<Id><<<s.blocks, 1024, s.pitch * sizeof(int), st>>>(ids, n, experts, s.per_block, s.pitch, counts);
@@ -249,7 +295,7 @@ bmmc_status launch_sort(const SortShape& s, const void* ids_, int64_t n, int exp
     cfg.stream = st;
     cfg.attrs = early;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, place, ids, n, experts, s.per_block, s.pitch, (const int*)counts, slot, source,
+    if (cudaLaunchKernelEx(&cfg, place, ids, n, experts, s.per_block, s.pitch, s.bits, (const int*)counts, slot, source,
                            offsets) != cudaSuccess) {
         cudaGetLastError();
         return BMMC_ERR_CUDA;

@@ -642,6 +642,57 @@ def test_stream_argument():
     assert torch.equal(out, want)
 
 
+def test_no_tokens():
+    """Calls without any token write nothing and give empty results."""
+    slot = torch.empty(0, 4, dtype=torch.int32, device="cuda")
+    x = torch.empty(0, 8, device="cuda")
+    assert bm.expert_dispatch(x, slot).shape == (0, 8)
+    assert bm.expert_combine(x, slot).shape == (0, 8)
+    grad_rows, grad_w = bm.expert_combine_backward(x, x, slot, torch.empty(0, 4, device="cuda"))
+    assert grad_rows.shape == (0, 8) and grad_w.shape == (0, 4)
+    out = bm.rotary(torch.empty(0, 2, 8, device="cuda"), torch.empty(0, dtype=torch.int64, device="cuda"), _freq(4))
+    assert out.shape == (0, 2, 8)
+    # tokens, but no row that is kept
+    slot = bm.expert_sort(torch.zeros(5, 2, dtype=torch.int32, device="cuda"), 3)[0]
+    assert not bm.expert_combine(torch.empty(0, 8, device="cuda"), slot).any()
+    assert not bm.expert_combine_backward(torch.ones(5, 8, device="cuda"), torch.empty(0, 8, device="cuda"), slot,
+                                          torch.ones(5, 2, device="cuda"))[1].any()
+
+
+def test_pinned_host_memory():
+    """The C entry points take pinned host memory, as those of the permutes do."""
+    from bmmc_index_transforms_gb300 import _capi
+
+    L = _capi.lib()
+    g = _gen(12)
+    T, K, H = 37, 3, 136
+    ids = torch.randint(-1, 5, (T, K), generator=g, device="cuda", dtype=torch.int32)
+    x, w = _randn(g, T, H, dtype=BF16), torch.rand(T, K, generator=g, device="cuda")
+    slot = bm.expert_sort(ids, 5)[0]
+    rows = bm.expert_dispatch(x, slot)
+    host = lambda v: v.cpu().pin_memory()  # noqa: E731
+    h_ids, h_x, h_w = host(ids), host(x), host(w)
+    new = lambda *s, dtype: torch.zeros(*s, dtype=dtype).pin_memory()  # noqa: E731
+    h_slot, h_source, h_offsets = new(T, K, dtype=torch.int32), new(T * K, dtype=torch.int32), new(6, dtype=torch.int32)
+    h_rows, h_out = new(T * K, H, dtype=BF16), new(T, H, dtype=BF16)
+    st = torch.cuda.current_stream().cuda_stream
+    assert L.expert_sort(h_ids.data_ptr(), 4, T, K, 5, h_slot.data_ptr(), h_source.data_ptr(), h_offsets.data_ptr(), None, 0,
+                         st) == _capi.OK
+    assert L.expert_dispatch(h_x.data_ptr(), H, h_slot.data_ptr(), T, K, H, _capi.BF16, h_rows.data_ptr(), H, T * K,
+                             st) == _capi.OK
+    assert L.expert_combine(h_rows.data_ptr(), H, T * K, h_slot.data_ptr(), h_w.data_ptr(), _capi.F32, T, K, H, _capi.BF16,
+                            h_out.data_ptr(), H, st) == _capi.OK
+    at, f = torch.arange(T, device="cuda"), _freq(4)
+    h_at, h_f, h_turned = host(at), host(f), new(T, 17, 8, dtype=BF16)
+    args = _capi.ROTARY_ARGS.pack(T, _capi.BF16, h_x.data_ptr(), 17, 8, H, 8, h_turned.data_ptr(), 17, 8, H, 8, h_f.data_ptr(),
+                                  0, h_at.data_ptr(), 8, 1, 0, 4, 0)
+    assert L.rotary(args, st) == _capi.OK
+    torch.cuda.synchronize()
+    assert torch.equal(h_slot, slot.cpu()) and torch.equal(h_rows, rows.cpu())
+    assert torch.equal(h_out, bm.expert_combine(rows, slot, w).cpu())
+    assert torch.equal(h_turned, bm.rotary(x.view(T, 17, 8), at, f).cpu())
+
+
 def test_tensors_elsewhere_are_refused():
     x = torch.zeros(4, 8)
     slot = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
