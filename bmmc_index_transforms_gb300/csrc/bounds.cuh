@@ -10,7 +10,9 @@
 //     must start on a multiple of its size and overlap the source buffer:
 //     such a word lies in the page of a byte of the buffer;
 //   - a shared-memory access must lie inside one of the shared arrays the
-//     kernel registered on entry.
+//     kernel registered on entry;
+//   - kernels with several sources and destinations (the token moves) pass
+//     the byte ranges of each in place of the two.
 // An access that fails is skipped (a load yields zero), and the failure is
 // counted in a device record of this translation unit: the number of
 // failures and, for the first one, the site (file tag * 100000 + source
@@ -42,6 +44,14 @@ struct Bounds {
 __host__ __device__ inline Bounds bounds(const void* in, uint64_t in_bytes, const void* out, uint64_t out_bytes) {
     return Bounds{{(uintptr_t)in, (uintptr_t)in + in_bytes}, {(uintptr_t)out, (uintptr_t)out + out_bytes}};
 }
+
+// The buffers a launch with more than one source or destination may read and
+// may write (experts.cu, rotary.cu).
+constexpr int kMaxSpans = 12;
+struct Spans {
+    Span rd[kMaxSpans], wr[kMaxSpans];
+    int n_rd, n_wr;
+};
 
 // Slots of the device record.
 enum { kFailures = 0, kSite, kAddress, kLo, kHi, kBytes, kRecordWords };
@@ -119,6 +129,39 @@ __device__ __forceinline__ bool sh_ok(const void* p, unsigned bytes, int site) {
     return false;
 }
 
+// The same for a launch that was given spans.
+static __shared__ Spans s_spans;
+
+__device__ __forceinline__ void enter_spans(const Spans& b, const void* s0 = nullptr, uint32_t n0 = 0,
+                                            const void* s1 = nullptr, uint32_t n1 = 0, const void* s2 = nullptr,
+                                            uint32_t n2 = 0) {
+    s_spans = b;
+    enter(Bounds{}, s0, n0, s1, n1, s2, n2);
+}
+
+__device__ __forceinline__ bool inside_one(const void* p, unsigned bytes, const Span* s, int n, int site) {
+    const uintptr_t a = (uintptr_t)p;
+    for (int i = 0; i < n; ++i)
+        if (a >= s[i].lo && a <= s[i].hi && bytes <= s[i].hi - a) return true;
+    fail(site, a, n ? s[0].lo : 0, n ? s[0].hi : 0, bytes);
+    return false;
+}
+
+__device__ __forceinline__ bool rd_ok(const void* p, unsigned bytes, int site) {
+    return inside_one(p, bytes, s_spans.rd, s_spans.n_rd, site);
+}
+__device__ __forceinline__ bool wr_ok(const void* p, unsigned bytes, int site) {
+    return inside_one(p, bytes, s_spans.wr, s_spans.n_wr, site);
+}
+__device__ __forceinline__ bool rd_word_ok(const void* p, unsigned bytes, int site) {
+    const uintptr_t a = (uintptr_t)p;
+    if ((a & (bytes - 1)) == 0)
+        for (int i = 0; i < s_spans.n_rd; ++i)
+            if (a < s_spans.rd[i].hi && a + bytes > s_spans.rd[i].lo) return true;
+    fail(site, a, s_spans.rd[0].lo, s_spans.rd[0].hi, bytes);
+    return false;
+}
+
 // Host: copy this translation unit's record out and optionally clear it.
 static inline cudaError_t read_record(unsigned long long out[kRecordWords], bool clear) {
     cudaError_t e = cudaMemcpyFromSymbol(out, g_record, sizeof(unsigned long long) * kRecordWords);
@@ -147,6 +190,14 @@ __device__ __forceinline__ uint32_t dyn_smem_bytes() {
 #define BMMC_OUT_OK(p, n) ::bmmc::chk::out_ok((p), (unsigned)(n), BMMC_CHK_SITE)
 #define BMMC_SH_OK(p, n) ::bmmc::chk::sh_ok((p), (unsigned)(n), BMMC_CHK_SITE)
 
+#define BMMC_SPANS_PARAM , const __grid_constant__ ::bmmc::chk::Spans bmmc_spans
+#define BMMC_SPANS_ARG(s) , (s)
+#define BMMC_SPANS_ENTER(...) ::bmmc::chk::enter_spans(bmmc_spans, __VA_ARGS__)
+#define BMMC_SPANS_ENTER_GLOBAL() ::bmmc::chk::enter_spans(bmmc_spans)
+#define BMMC_RD_OK(p, n) ::bmmc::chk::rd_ok((p), (unsigned)(n), BMMC_CHK_SITE)
+#define BMMC_RD_WORD_OK(p, n) ::bmmc::chk::rd_word_ok((p), (unsigned)(n), BMMC_CHK_SITE)
+#define BMMC_WR_OK(p, n) ::bmmc::chk::wr_ok((p), (unsigned)(n), BMMC_CHK_SITE)
+
 #else  // !BMMC_BOUNDS_CHECK
 
 constexpr bool kEnabled = false;
@@ -165,6 +216,13 @@ static inline cudaError_t read_record(unsigned long long out[kRecordWords], bool
 #define BMMC_IN_WORD_OK(p, n) true
 #define BMMC_OUT_OK(p, n) true
 #define BMMC_SH_OK(p, n) true
+#define BMMC_SPANS_PARAM
+#define BMMC_SPANS_ARG(s)
+#define BMMC_SPANS_ENTER(...) ((void)0)
+#define BMMC_SPANS_ENTER_GLOBAL() ((void)0)
+#define BMMC_RD_OK(p, n) true
+#define BMMC_RD_WORD_OK(p, n) true
+#define BMMC_WR_OK(p, n) true
 
 #endif  // BMMC_BOUNDS_CHECK
 

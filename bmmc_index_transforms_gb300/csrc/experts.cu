@@ -14,6 +14,8 @@
 #include <type_traits>
 
 #include "../../include/bmmc.h"
+#define BMMC_CHK_FILE 6  // site tag of this file in bounds-checked builds
+#include "bounds.cuh"
 #include "token_moves.hpp"
 #include "token_words.cuh"
 
@@ -26,6 +28,10 @@ namespace {
 constexpr int kMaxExperts = 4096;
 constexpr int kSortRounds = 4;       // ids per lane and tile
 constexpr int kMaxSortBlocks = 152;  // blocks of a sort that one block does not cover: one for each SM
+
+#ifdef BMMC_BOUNDS_CHECK
+__device__ __forceinline__ uint32_t chk_dynamic_bytes() { return chk::dyn_smem_bytes(); }
+#endif
 
 template <class Id>
 __device__ __forceinline__ int key_of(Id id, int experts) {
@@ -66,8 +72,10 @@ __device__ void block_exclusive_scan(int* v, int n, int* tmp) {
 // the blocks' rows are `pitch` apart, a multiple of 4, zero past the keys.
 template <class Id>
 __global__ void __launch_bounds__(1024) sort_count_kernel(const Id* __restrict__ ids, int64_t n, int experts,
-                                                          int64_t per_block, int pitch, int* __restrict__ counts) {
+                                                          int64_t per_block, int pitch, int* __restrict__ counts
+                                                              BMMC_SPANS_PARAM) {
     extern __shared__ int s_hist[];
+    BMMC_SPANS_ENTER(s_hist, chk_dynamic_bytes());
     cudaTriggerProgrammaticLaunchCompletion();  // the place kernel may rank its first tile meanwhile
     for (int e = threadIdx.x; e < pitch; e += blockDim.x) s_hist[e] = 0;
     __syncthreads();
@@ -77,14 +85,15 @@ __global__ void __launch_bounds__(1024) sort_count_kernel(const Id* __restrict__
 #pragma unroll
         for (int r = 0; r < kSortRounds; ++r) {
             const int64_t i = at + (int64_t)r * blockDim.x;
-            key[r] = i < hi ? key_of(ids[i], experts) : -1;
+            key[r] = i < hi && BMMC_RD_OK(ids + i, sizeof(Id)) ? key_of(ids[i], experts) : -1;
         }
 #pragma unroll
         for (int r = 0; r < kSortRounds; ++r)
-            if (key[r] >= 0) atomicAdd(&s_hist[key[r]], 1);
+            if (key[r] >= 0 && BMMC_SH_OK(s_hist + key[r], 4)) atomicAdd(&s_hist[key[r]], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < pitch; e += blockDim.x) counts[(int64_t)blockIdx.x * pitch + e] = s_hist[e];
+    for (int e = threadIdx.x; e < pitch; e += blockDim.x)
+        if (BMMC_WR_OK(counts + (int64_t)blockIdx.x * pitch + e, 4)) counts[(int64_t)blockIdx.x * pitch + e] = s_hist[e];
 }
 
 // base[e] += the counts of key e over all blocks, before[e] += those over the
@@ -97,7 +106,8 @@ __device__ __forceinline__ void sum_counts(const int* counts, int pitch, int* ba
         int4 all = make_int4(0, 0, 0, 0), ahead = all;
 #pragma unroll 8
         for (int b = group; b < (int)gridDim.x; b += groups) {
-            const int4 c = __ldcg(reinterpret_cast<const int4*>(counts) + (int64_t)b * quads + q);
+            const int4* const from = reinterpret_cast<const int4*>(counts) + (int64_t)b * quads + q;
+            const int4 c = BMMC_RD_OK(from, 16) ? __ldcg(from) : make_int4(0, 0, 0, 0);
             all.x += c.x, all.y += c.y, all.z += c.z, all.w += c.w;
             if (b < (int)blockIdx.x) ahead.x += c.x, ahead.y += c.y, ahead.z += c.z, ahead.w += c.w;
         }
@@ -136,8 +146,9 @@ template <class Id, int R>
 __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__ ids, int64_t n, int experts,
                                                           int64_t per_block, int pitch, int bits, const int* counts,
                                                           int* __restrict__ slot, int* __restrict__ source,
-                                                          int* __restrict__ offsets) {
+                                                          int* __restrict__ offsets BMMC_SPANS_PARAM) {
     extern __shared__ int s_mem[];
+    BMMC_SPANS_ENTER(s_mem, chk_dynamic_bytes());
     const int keys = experts + 1, warps = blockDim.x >> 5, none = (1 << bits) - 1;
     int* base = s_mem;           // [pitch] where the block's next choice of each key goes
     int* total = base + pitch;   // [pitch] choices of the tile
@@ -155,14 +166,14 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int64_t i = at + ((int64_t)warp * R + r) * 32 + lane;
-            key[r] = i < hi ? key_of(ids[i], experts) : none;  // none: a key past all others
+            key[r] = i < hi && BMMC_RD_OK(ids + i, sizeof(Id)) ? key_of(ids[i], experts) : none;  // none: a key past all others
         }
         for (int e = lane; e < keys; e += 32) mine[e] = 0;
         __syncwarp();
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const unsigned same = same_key(key[r], bits);
-            const bool there = key[r] < keys;
+            const bool there = key[r] < keys && BMMC_SH_OK(mine + key[r], 4);
             const int before = there ? mine[key[r]] : 0;
             rank[r] = before + __popc(same & ((1u << lane) - 1));
             __syncwarp();
@@ -177,7 +188,7 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__
             __syncthreads();
             block_exclusive_scan(base, keys, tmp);
             for (int e = threadIdx.x; e < keys; e += blockDim.x) {
-                if (blockIdx.x == 0) offsets[e] = base[e];
+                if (blockIdx.x == 0 && BMMC_WR_OK(offsets + e, 4)) offsets[e] = base[e];
                 base[e] += total[e];
             }
         }
@@ -196,7 +207,8 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__
         __syncthreads();
         block_exclusive_scan(counts ? start : base, keys, tmp);
         if (!counts)
-            for (int e = threadIdx.x; e < keys; e += blockDim.x) offsets[e] = base[e];
+            for (int e = threadIdx.x; e < keys; e += blockDim.x)
+                if (BMMC_WR_OK(offsets + e, 4)) offsets[e] = base[e];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (key[r] >= keys) continue;
@@ -204,11 +216,12 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__
             const int64_t i = at + in_tile;
             const int to = base[key[r]] + in_key;
             const bool routed = key[r] < experts;
-            slot[i] = routed ? to : ~to;
+            if (BMMC_WR_OK(slot + i, 4)) slot[i] = routed ? to : ~to;
             if (counts) {
-                order[start[key[r]] + in_key] = in_tile;
-                order_key[start[key[r]] + in_key] = (unsigned short)key[r];
-            } else {
+                const int j = start[key[r]] + in_key;
+                if (BMMC_SH_OK(order + j, 4)) order[j] = in_tile;
+                if (BMMC_SH_OK(order_key + j, 2)) order_key[j] = (unsigned short)key[r];
+            } else if (BMMC_WR_OK(source + to, 4)) {
                 source[to] = routed ? (int)i : ~(int)i;
             }
         }
@@ -217,7 +230,7 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__
         const int here = (int)min((int64_t)blockDim.x * R, hi - at);
         for (int j = threadIdx.x; j < here; j += blockDim.x) {
             const int k = order_key[j], i = (int)at + order[j], to = base[k] + j - start[k];
-            if ((unsigned)to < (unsigned)n) source[to] = k < experts ? i : ~i;  // also if ids changed meanwhile
+            if ((unsigned)to < (unsigned)n && BMMC_WR_OK(source + to, 4)) source[to] = k < experts ? i : ~i;  // also if ids changed meanwhile
         }
         at += (int64_t)blockDim.x * R;
         if (at >= hi) return;
@@ -260,7 +273,8 @@ SortShape sort_shape(int64_t n, int experts) {
 
 template <class Id, int R>
 bmmc_status launch_sort(const SortShape& s, const void* ids_, int64_t n, int experts, int32_t* slot, int32_t* source,
-                        int32_t* offsets, int* counts, cudaStream_t st) {
+                        int32_t* offsets, int* counts, const chk::Spans& spans, cudaStream_t st) {
+    (void)spans;
     const Id* ids = static_cast<const Id*>(ids_);
     const auto place = sort_place_kernel<Id, R>;
     if (s.smem > 48 * 1024) {
@@ -280,10 +294,12 @@ bmmc_status launch_sort(const SortShape& s, const void* ids_, int64_t n, int exp
     }
     const int* none = nullptr;
     if (s.blocks == 1) {
-        place<<<1, s.warps * 32, s.smem, st>>>(ids, n, experts, s.per_block, s.pitch, s.bits, none, slot, source, offsets);
+        place<<<1, s.warps * 32, s.smem, st>>>(ids, n, experts, s.per_block, s.pitch, s.bits, none, slot, source,
+                                                 offsets BMMC_SPANS_ARG(spans));
         return launched();
     }
-    sort_count_kernel<Id><<<s.blocks, 1024, s.pitch * sizeof(int), st>>>(ids, n, experts, s.per_block, s.pitch, counts);
+    sort_count_kernel<Id><<<s.blocks, 1024, s.pitch * sizeof(int), st>>>(ids, n, experts, s.per_block, s.pitch,
+                                                                                counts BMMC_SPANS_ARG(spans));
     if (launched() != BMMC_OK) return BMMC_ERR_CUDA;
     cudaLaunchAttribute early[1];
     early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -296,7 +312,7 @@ bmmc_status launch_sort(const SortShape& s, const void* ids_, int64_t n, int exp
     cfg.attrs = early;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, place, ids, n, experts, s.per_block, s.pitch, s.bits, (const int*)counts, slot, source,
-                           offsets) != cudaSuccess) {
+                           offsets BMMC_SPANS_ARG(spans)) != cudaSuccess) {
         cudaGetLastError();
         return BMMC_ERR_CUDA;
     }
@@ -333,17 +349,20 @@ template <class Word>
 __global__ void __launch_bounds__(256, 8) dispatch_kernel(const char* __restrict__ x, int64_t x_stride,
                                                           const int* __restrict__ slot, int64_t tokens, int choices,
                                                           int64_t n_rows, int words, char* __restrict__ rows,
-                                                          int64_t row_stride) {
+                                                          int64_t row_stride BMMC_SPANS_PARAM) {
+    BMMC_SPANS_ENTER_GLOBAL();
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const int w = blockIdx.y * blockDim.x + threadIdx.x;
     if (t >= tokens || w >= words) return;
-    const Word v = __ldg(reinterpret_cast<const Word*>(x + t * x_stride) + w);
+    const Word* const from = reinterpret_cast<const Word*>(x + t * x_stride) + w;
+    const Word v = BMMC_RD_OK(from, sizeof(Word)) ? __ldg(from) : Word{};
     slot += t * choices;
 #pragma unroll 4
     for (int k = 0; k < choices; ++k) {
-        const int s = __ldg(slot + k);
+        const int s = BMMC_RD_OK(slot + k, 4) ? __ldg(slot + k) : 0;
         const int64_t row = s < 0 ? ~s : s;
-        if (row < n_rows) reinterpret_cast<Word*>(rows + row * row_stride)[w] = s < 0 ? Word{} : v;
+        Word* const to = reinterpret_cast<Word*>(rows + row * row_stride) + w;
+        if (row < n_rows && BMMC_WR_OK(to, sizeof(Word))) *to = s < 0 ? Word{} : v;
     }
 }
 
@@ -355,7 +374,9 @@ template <class T>
 __global__ void __launch_bounds__(256, 6) dispatch_across_kernel(const char* __restrict__ x, int64_t x_stride,
                                                                  const int* __restrict__ slot, int64_t tokens,
                                                                  int choices, int64_t n_rows, int length,
-                                                                 char* __restrict__ rows, int64_t row_stride) {
+                                                                 char* __restrict__ rows, int64_t row_stride
+                                                                     BMMC_SPANS_PARAM) {
+    BMMC_SPANS_ENTER_GLOBAL();
     constexpr int W = 16 / sizeof(T);
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const int w = blockIdx.y * blockDim.x + threadIdx.x;
@@ -364,12 +385,13 @@ __global__ void __launch_bounds__(256, 6) dispatch_across_kernel(const char* __r
     const int from = (int)((unsigned)reinterpret_cast<uintptr_t>(row_x) & 15u);
     const int bytes = length * (int)sizeof(T);
     uint4 a, b;  // bytes [w * 16 - 16 - from, + 32) of the row
-    load_if(w > 0 && w * 16 - 16 - from < bytes, a, row_x + (int64_t)w * 16 - 16 - from);
-    load_if(w * 16 - from < bytes, b, row_x + (int64_t)w * 16 - from);
+    const char* const word = row_x + (int64_t)w * 16 - from;
+    load_if(w > 0 && w * 16 - 16 - from < bytes && BMMC_RD_WORD_OK(word - 16, 16), a, word - 16);
+    load_if(w * 16 - from < bytes && BMMC_RD_WORD_OK(word, 16), b, word);
     slot += t * choices;
 #pragma unroll 2
     for (int k = 0; k < choices; ++k) {
-        const int s = __ldg(slot + k);
+        const int s = BMMC_RD_OK(slot + k, 4) ? __ldg(slot + k) : 0;
         const int64_t row = s < 0 ? ~s : s;
         if (row >= n_rows) continue;
         char* const out = rows + row * row_stride;
@@ -388,6 +410,7 @@ __global__ void __launch_bounds__(256, 6) dispatch_across_kernel(const char* __r
 // A weight of the rows' type or of 32 bits.
 template <class T>
 __device__ __forceinline__ float weight_at(const void* weights, int in_f32, int64_t i) {
+    if (!BMMC_RD_OK(static_cast<const char*>(weights) + i * (in_f32 ? 4 : (int)sizeof(T)), in_f32 ? 4 : sizeof(T))) return 0.0f;
     return in_f32 ? static_cast<const float*>(weights)[i] : to_f32(static_cast<const T*>(weights)[i]);
 }
 
@@ -398,7 +421,8 @@ template <class T, int W, int KB, bool ACROSS>
 __global__ void __launch_bounds__(256, KB > 2 ? 4 : ACROSS && sizeof(T) == 2 ? 6 : 8) combine_kernel(const char* __restrict__ rows, int64_t row_stride, int64_t n_rows,
                                                       const int* __restrict__ slot, const void* __restrict__ weights,
                                                       int weights_f32, int64_t tokens, int choices, int length,
-                                                      char* __restrict__ out, int64_t out_stride) {
+                                                      char* __restrict__ out, int64_t out_stride BMMC_SPANS_PARAM) {
+    BMMC_SPANS_ENTER_GLOBAL();
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const int w = blockIdx.y * blockDim.x + threadIdx.x;
     if (t >= tokens) return;
@@ -417,7 +441,7 @@ __global__ void __launch_bounds__(256, KB > 2 ? 4 : ACROSS && sizeof(T) == 2 ? 6
         for (int j = 0; j < KB; ++j) {
             const bool there = k0 + j < choices;
             const int64_t at = t * choices + k0 + j;
-            s[j] = there ? slot[at] : -1;
+            s[j] = there && BMMC_RD_OK(slot + at, 4) ? slot[at] : -1;
             f[j] = there && weights ? weight_at<T>(weights, weights_f32, at) : 1.0f;
         }
 #pragma unroll
@@ -455,8 +479,10 @@ template <class T, int W, int KB, bool ACROSS>
 __global__ void __launch_bounds__(256, KB <= 2 ? 6 : 4) combine_backward_kernel(
     const char* __restrict__ grad, int64_t grad_stride, const char* __restrict__ rows, int64_t row_stride,
     int64_t n_rows, const int* __restrict__ slot, const void* __restrict__ weights, int weights_f32, int64_t tokens,
-    int choices, int length, char* __restrict__ grad_rows, int64_t grad_row_stride, void* __restrict__ grad_weights) {
+    int choices, int length, char* __restrict__ grad_rows, int64_t grad_row_stride, void* __restrict__ grad_weights
+        BMMC_SPANS_PARAM) {
     __shared__ float s_part[8][KB];
+    BMMC_SPANS_ENTER(s_part, sizeof(s_part));
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const bool live = t < tokens;
     const int x = blockDim.x, tid = threadIdx.y * x + threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -472,7 +498,7 @@ __global__ void __launch_bounds__(256, KB <= 2 ? 6 : 4) combine_backward_kernel(
             const bool there = live && k0 + j < choices;
             const int64_t at = t * choices + k0 + j;
             dot[j] = 0.0f;
-            s[j] = there ? slot[at] : -1 - (int)n_rows;
+            s[j] = there && BMMC_RD_OK(slot + at, 4) ? slot[at] : -1 - (int)n_rows;
             f[j] = there ? weight_at<T>(weights, weights_f32, at) : 0.0f;
             if (s[j] < 0) f[j] = 0.0f;
         }
@@ -520,7 +546,8 @@ __global__ void __launch_bounds__(256, KB <= 2 ? 6 : 4) combine_backward_kernel(
             if (k0) __syncthreads();
             if (lane == 0)
 #pragma unroll
-                for (int j = 0; j < KB; ++j) s_part[warp][j] = dot[j];
+                for (int j = 0; j < KB; ++j)
+                    if (BMMC_SH_OK(&s_part[warp][j], 4)) s_part[warp][j] = dot[j];
             __syncthreads();
             const int first = threadIdx.y * (x >> 5);
 #pragma unroll
@@ -534,6 +561,9 @@ __global__ void __launch_bounds__(256, KB <= 2 ? 6 : 4) combine_backward_kernel(
             for (int j = 0; j < KB; ++j)
                 if (k0 + j < choices) {
                     const int64_t at = t * choices + k0 + j;
+                    if (!BMMC_WR_OK(static_cast<char*>(grad_weights) + at * (weights_f32 ? 4 : (int)sizeof(T)),
+                                    weights_f32 ? 4 : sizeof(T)))
+                        continue;
                     if (weights_f32) static_cast<float*>(grad_weights)[at] = dot[j];
                     else static_cast<T*>(grad_weights)[at] = from_f32<T>(dot[j]);
                 }
@@ -627,7 +657,8 @@ bmmc_status expert_sort(const void* ids, int id_bytes, int64_t tokens, int choic
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int* counts = static_cast<int*>(need ? workspace : nullptr);
     const SortShape shape = sort_shape(n, experts);
-    const auto go = [&](auto launch) { return launch(shape, ids, n, experts, slot, source, offsets, counts, st); };
+    const chk::Spans spans = spans_of({in, o[3]}, {o[0], o[1], o[2], o[3]});
+    const auto go = [&](auto launch) { return launch(shape, ids, n, experts, slot, source, offsets, counts, spans, st); };
     if (id_bytes == 4) return shape.rounds == 1 ? go(launch_sort<int32_t, 1>) : go(launch_sort<int32_t, kSortRounds>);
     return shape.rounds == 1 ? go(launch_sort<int64_t, 1>) : go(launch_sort<int64_t, kSortRounds>);
 }
@@ -652,15 +683,17 @@ bmmc_status expert_dispatch(const void* x, int64_t x_stride, const int32_t* slot
     const char* from = static_cast<const char*>(x);
     char* to = static_cast<char*>(rows);
     const int most = tokens * words <= kFewWords ? 128 : 256;
+    const chk::Spans spans = spans_of({in, {slot, 1, 0, tokens * choices * 4}}, {out});
+    (void)spans;
     const auto copy = [&](auto word) {
         const Cover c = cover(tokens, words, most);
         dispatch_kernel<decltype(word)><<<c.grid, c.block, 0, st>>>(from, x_stride * es, slot, tokens, choices, n_rows, words,
-                                                                    to, row_stride * es);
+                                                                    to, row_stride * es BMMC_SPANS_ARG(spans));
     };
     const auto across = [&](auto e) {
         const Cover c = cover(tokens, words + 1, most);  // one more: thread 0 holds no word w - 1
         dispatch_across_kernel<decltype(e)><<<c.grid, c.block, 0, st>>>(from, x_stride * es, slot, tokens, choices, n_rows,
-                                                                        (int)hidden, to, row_stride * es);
+                                                                        (int)hidden, to, row_stride * es BMMC_SPANS_ARG(spans));
     };
     if (way.bytes == 16) copy(uint4{});
     else if (way.bytes == 8) copy(uint2{});
@@ -692,6 +725,9 @@ bmmc_status expert_combine(const void* rows, int64_t row_stride, int64_t n_rows,
                                    (uint64_t)(out_stride * es), (uint64_t)(hidden * es)});
     const int words = way.words;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const chk::Spans spans = spans_of({{rows, n_rows, row_stride * es, hidden * es}, {slot, 1, 0, tokens * choices * 4},
+                                       {weights, 1, 0, tokens * choices * ws}}, {to});
+    (void)spans;
     by_type(type, way, [&](auto e, auto width, auto across) {
         using T = decltype(e);
         constexpr int W = decltype(width)::value;
@@ -702,7 +738,7 @@ bmmc_status expert_combine(const void* rows, int64_t row_stride, int64_t n_rows,
             if (choices > 2) kernel = choices <= 4 ? combine_kernel<T, W, 4, A> : combine_kernel<T, W, 8, A>;
         kernel<<<c.grid, c.block, 0, st>>>(static_cast<const char*>(rows), row_stride * es, n_rows, slot, weights,
                                           weight_type == BMMC_F32, tokens, choices, (int)hidden, static_cast<char*>(out),
-                                          out_stride * es);
+                                          out_stride * es BMMC_SPANS_ARG(spans));
     });
     return launched();
 }
@@ -743,6 +779,8 @@ bmmc_status expert_combine_backward(const void* grad, int64_t grad_stride, const
     while (x < words && x < most) x <<= 1;
     const dim3 block(x, 256 / x);
     const unsigned blocks = (unsigned)((tokens + block.y - 1) / block.y);
+    const chk::Spans spans = spans_of({in[0], in[1], in[2], in[3]}, {gr, gw});
+    (void)spans;
     by_type(type, way, [&](auto e, auto width, auto across) {
         using T = decltype(e);
         constexpr int W = decltype(width)::value;
@@ -752,9 +790,16 @@ bmmc_status expert_combine_backward(const void* grad, int64_t grad_stride, const
             if (choices > 2) kernel = combine_backward_kernel<T, W, 4, A>;
         kernel<<<blocks, block, 0, st>>>(static_cast<const char*>(grad), grad_stride * es, static_cast<const char*>(rows),
                                         row_stride * es, n_rows, slot, weights, weight_type == BMMC_F32, tokens, choices,
-                                        (int)hidden, static_cast<char*>(grad_rows), grad_row_stride * es, grad_weights);
+                                        (int)hidden, static_cast<char*>(grad_rows), grad_row_stride * es,
+                                        grad_weights BMMC_SPANS_ARG(spans));
     });
     return launched();
 }
 
 }  // extern "C"
+
+namespace bmmc {
+cudaError_t bounds_record_experts(unsigned long long out[chk::kRecordWords], bool clear) {
+    return chk::read_record(out, clear);
+}
+}  // namespace bmmc

@@ -14,6 +14,8 @@
 #include <type_traits>
 
 #include "../../include/bmmc.h"
+#define BMMC_CHK_FILE 7  // site tag of this file in bounds-checked builds
+#include "bounds.cuh"
 #include "token_moves.hpp"
 #include "token_words.cuh"
 
@@ -67,7 +69,7 @@ __device__ int64_t find_sequence_warp(const int* starts, int64_t sequences, int6
     while (n > 0) {
         const int64_t step = (n + 31) / 32;
         const int64_t i = lo + lane * step;
-        const bool before = lane * step < n && starts[i] <= t;
+        const bool before = lane * step < n && BMMC_RD_OK(starts + i, 4) && starts[i] <= t;
         const int c = __popc(__ballot_sync(~0u, before));
         if (c == 0) return lo - 1;
         const int64_t at = lo + (c - 1) * step;  // starts[at] <= t
@@ -82,7 +84,7 @@ __device__ int64_t find_sequence(const int* starts, int64_t sequences, int64_t t
     int64_t lo = 0, hi = sequences;  // starts[lo - 1] <= t, starts[hi] > t
     while (lo < hi) {
         const int64_t mid = (lo + hi) >> 1;
-        if (starts[mid] <= t) lo = mid + 1;
+        if (BMMC_RD_OK(starts + mid, 4) && starts[mid] <= t) lo = mid + 1;
         else hi = mid;
     }
     return lo - 1;
@@ -98,17 +100,19 @@ __device__ Place place_of(const MoveParams& p, int64_t t, int64_t b) {
     Place r{0, {-1, -1}};
     int64_t first = t;
     if (p.starts) {
-        if (b < 0) return r;
+        if (b < 0 || !BMMC_RD_OK(p.starts + b, 8)) return r;
         first = p.starts[b];
     } else if (t >= p.sequences) {
         return r;
     }
+    if (!BMMC_RD_OK(p.lengths + b, 4)) return r;
     const int length = p.lengths[b], next = p.starts ? p.starts[b + 1] : 0;  // on their way together
     if (p.starts && t >= next) return r;
     r.at = (int64_t)length + (t - first);
     if (r.at < 0 || r.at >= (int64_t)1 << 32) return r;  // (more only by starts below zero)
     const unsigned at = (unsigned)r.at, column = at / p.page_size;
     if (column >= p.table_columns) return r;
+    if (!BMMC_RD_OK(p.table + b * p.table_stride + column, 4)) return r;
     const int page = p.table[b * p.table_stride + column];
     if (page < 0 || page >= p.pages) return r;
     for (int c = 0; c < 2; ++c)
@@ -125,10 +129,12 @@ __device__ __forceinline__ float turned_second(float x, float y, float2 r) { ret
 // memory, once for all heads; then a thread keeps those of its word of a head
 // in registers and walks over the heads, two at a time.
 template <class T, int W, bool ADJACENT>
-__global__ void __launch_bounds__(kMostThreads, 4) move_heads_kernel(const __grid_constant__ MoveParams p) {
+__global__ void __launch_bounds__(kMostThreads, 4) move_heads_kernel(const __grid_constant__ MoveParams p
+                                                                        BMMC_SPANS_PARAM) {
     extern __shared__ float2 s_turn[];  // [tokens of the block][pairs] cos, sin
     __shared__ int64_t s_place[2][kMaxTokensPerBlock];  // byte offsets in the caches, -1 = none
     __shared__ float s_position[kMaxTokensPerBlock];
+    BMMC_SPANS_ENTER(s_turn, chk::dyn_smem_bytes(), s_place, sizeof(s_place), s_position, sizeof(s_position));
     const int tid = threadIdx.x, threads = blockDim.x, per_block = threads >> p.group_log2;
     const int64_t t0 = (int64_t)blockIdx.x * per_block;
     const int nt = (int)min((int64_t)per_block, p.tokens - t0);
@@ -143,13 +149,13 @@ __global__ void __launch_bounds__(kMostThreads, 4) move_heads_kernel(const __gri
     bool by_place[kAhead] = {};
     const auto start_turn = [&](int i, float& f, float& at, bool& from_place) {
         const int k = i / p.pairs, pair = i - k * p.pairs;
-        const int axis = p.pair_axes ? p.pair_axes[pair] : 0;
-        f = p.freq[pair];
+        const int axis = p.pair_axes && BMMC_RD_OK(p.pair_axes + pair, 4) ? p.pair_axes[pair] : 0;
+        f = BMMC_RD_OK(p.freq + pair, 4) ? p.freq[pair] : 0.0f;
         at = 0.0f;  // an axis that is not there does not turn
         from_place = !p.positions && axis == 0;
         if (p.positions && axis >= 0 && axis < p.axes) {
             const int64_t j = axis * p.axis_stride + t0 + k;
-            at = p.position_bytes == 4 ? (float)static_cast<const int32_t*>(p.positions)[j]
+            if (BMMC_RD_OK(static_cast<const char*>(p.positions) + j * p.position_bytes, p.position_bytes)) at = p.position_bytes == 4 ? (float)static_cast<const int32_t*>(p.positions)[j]
                                        : (float)static_cast<const int64_t*>(p.positions)[j];
         }
     };
@@ -168,12 +174,14 @@ __global__ void __launch_bounds__(kMostThreads, 4) move_heads_kernel(const __gri
         if (p.starts && per_block <= 8) {
             for (int i = tid >> 5; i < nt; i += threads >> 5) {
                 const Place r = place_of(p, t0 + i, find_sequence_warp(p.starts, p.sequences, t0 + i, tid & 31));
-                if ((tid & 31) == 0) s_place[0][i] = r.byte[0], s_place[1][i] = r.byte[1], s_position[i] = (float)r.at;
+                if ((tid & 31) == 0 && BMMC_SH_OK(&s_place[1][i], 8) && BMMC_SH_OK(s_position + i, 4))
+                    s_place[0][i] = r.byte[0], s_place[1][i] = r.byte[1], s_position[i] = (float)r.at;
             }
         } else if (tid < nt) {
             const int64_t t = t0 + tid;
             const Place r = place_of(p, t, p.starts ? find_sequence(p.starts, p.sequences, t) : t);
-            s_place[0][tid] = r.byte[0], s_place[1][tid] = r.byte[1], s_position[tid] = (float)r.at;
+            if (BMMC_SH_OK(&s_place[1][tid], 8) && BMMC_SH_OK(s_position + tid, 4))
+                s_place[0][tid] = r.byte[0], s_place[1][tid] = r.byte[1], s_position[tid] = (float)r.at;
         }
         if (!p.positions) __syncthreads();
     }
@@ -182,7 +190,7 @@ __global__ void __launch_bounds__(kMostThreads, 4) move_heads_kernel(const __gri
             if (from_place) at = s_position[i / p.pairs];
             float s, c;
             sincosf(at * f, &s, &c);
-            s_turn[i] = make_float2(c, p.sign * s);
+            if (BMMC_SH_OK(s_turn + i, 8)) s_turn[i] = make_float2(c, p.sign * s);
         };
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
@@ -226,15 +234,16 @@ __global__ void __launch_bounds__(kMostThreads, 4) move_heads_kernel(const __gri
             float2 r[kTurns];
             if (turned)
 #pragma unroll
-                for (int i = 0; i < kTurns; ++i) r[i] = turn[j * kTurns + i];
+                for (int i = 0; i < kTurns; ++i)
+                    r[i] = BMMC_SH_OK(turn + j * kTurns + i, 8) ? turn[j * kTurns + i] : float2{};
             for (int head = down; head < h.heads; head += kHeadsAtOnce * step) {
                 Pack<T, W> a[kHeadsAtOnce], b[kHeadsAtOnce];
 #pragma unroll
                 for (int u = 0; u < kHeadsAtOnce; ++u)
                     if (u == 0 || head + u * step < h.heads) {
                         const char* from = src + (head + u * step) * h.src_head + at;
-                        a[u].load(from);
-                        if (kTwo && turned) b[u].load(from + half);
+                        if (BMMC_RD_OK(from, sizeof(a[u]))) a[u].load(from);
+                        if (kTwo && turned && BMMC_RD_OK(from + half, sizeof(b[u]))) b[u].load(from + half);
                     }
 #pragma unroll
                 for (int u = 0; u < kHeadsAtOnce; ++u)
@@ -249,7 +258,7 @@ __global__ void __launch_bounds__(kMostThreads, 4) move_heads_kernel(const __gri
                                     y[i] = turned_second(a[u].get(i), b[u].get(i), r[i]);
                                 }
                                 b[u].set(y);
-                                b[u].store(out + half);
+                                if (BMMC_WR_OK(out + half, sizeof(b[u]))) b[u].store(out + half);
                             } else {
 #pragma unroll
                                 for (int i = 0; i < W; i += 2) {
@@ -259,7 +268,7 @@ __global__ void __launch_bounds__(kMostThreads, 4) move_heads_kernel(const __gri
                             }
                             a[u].set(x);
                         }
-                        a[u].store(out);
+                        if (BMMC_WR_OK(out, sizeof(a[u]))) a[u].store(out);
                     }
             }
         }
@@ -300,34 +309,35 @@ int deal_out(MoveParams& p, const int (&dims)[3], int W, int es, bool adjacent, 
 }
 
 template <class T, int W>
-bmmc_status launch_width(MoveParams& p, const int (&dims)[3], bool adjacent, cudaStream_t st) {
+bmmc_status launch_width(MoveParams& p, const int (&dims)[3], bool adjacent, const chk::Spans& spans, cudaStream_t st) {
+    (void)spans;
     bool split;
     const int threads = deal_out(p, dims, W, sizeof(T), adjacent, &split);
     const int per_block = threads >> p.group_log2;
     const dim3 grid((unsigned)((p.tokens + per_block - 1) / per_block), split ? p.parts : 1);
     const size_t smem = (size_t)per_block * p.pairs * sizeof(float2);
-    if (adjacent) move_heads_kernel<T, W, true><<<grid, threads, smem, st>>>(p);
-    else move_heads_kernel<T, W, false><<<grid, threads, smem, st>>>(p);
+    if (adjacent) move_heads_kernel<T, W, true><<<grid, threads, smem, st>>>(p BMMC_SPANS_ARG(spans));
+    else move_heads_kernel<T, W, false><<<grid, threads, smem, st>>>(p BMMC_SPANS_ARG(spans));
     return launched();
 }
 
 template <class T>
-bmmc_status launch_type(MoveParams& p, const int (&dims)[3], bool adjacent, int bytes, cudaStream_t st) {
+bmmc_status launch_type(MoveParams& p, const int (&dims)[3], bool adjacent, int bytes, const chk::Spans& spans, cudaStream_t st) {
     constexpr int es = sizeof(T);
     switch (bytes) {
-        case 16: return launch_width<T, 16 / es>(p, dims, adjacent, st);
-        case 8: return launch_width<T, 8 / es>(p, dims, adjacent, st);
-        case 4: return launch_width<T, 4 / es>(p, dims, adjacent, st);
+        case 16: return launch_width<T, 16 / es>(p, dims, adjacent, spans, st);
+        case 8: return launch_width<T, 8 / es>(p, dims, adjacent, spans, st);
+        case 4: return launch_width<T, 4 / es>(p, dims, adjacent, spans, st);
     }
-    return launch_width<T, 1>(p, dims, adjacent, st);
+    return launch_width<T, 1>(p, dims, adjacent, spans, st);
 }
 
-bmmc_status launch(MoveParams& p, const int (&dims)[3], int type, bool adjacent, int bytes, cudaStream_t st) {
+bmmc_status launch(MoveParams& p, const int (&dims)[3], int type, bool adjacent, int bytes, const chk::Spans& spans, cudaStream_t st) {
     switch (type) {
-        case BMMC_F32: return launch_type<float>(p, dims, adjacent, bytes, st);
-        case BMMC_F16: return launch_type<__half>(p, dims, adjacent, bytes, st);
+        case BMMC_F32: return launch_type<float>(p, dims, adjacent, bytes, spans, st);
+        case BMMC_F16: return launch_type<__half>(p, dims, adjacent, bytes, spans, st);
     }
-    return launch_type<__nv_bfloat16>(p, dims, adjacent, bytes, st);
+    return launch_type<__nv_bfloat16>(p, dims, adjacent, bytes, spans, st);
 }
 
 bool bad_stride(int64_t s) { return s < 0 || s > kMaxStride; }
@@ -385,6 +395,13 @@ bmmc_status set_turns(MoveParams& p, const rotary_turns_t& r, bool device, bool 
     return all_reachable(device, {r.inv_freq, r.pair_axes, r.positions});
 }
 
+// What the turns read.
+Rows turn_rows(const rotary_turns_t& r, int64_t tokens, int what) {
+    if (what == 0) return Rows{r.inv_freq, 1, 0, r.pairs * 4};
+    if (what == 1) return Rows{r.pair_axes, 1, 0, r.pairs * 4};
+    return Rows{r.positions, r.axes, r.axis_stride * r.position_bytes, tokens * r.position_bytes};
+}
+
 // The bits that a word's size has to divide on account of the pairs.
 uint64_t pair_bits(const rotary_turns_t& r, int es) {
     return (uint64_t)(r.flags & ROTARY_ADJACENT ? 2 * r.pairs : r.pairs) * es;
@@ -430,8 +447,11 @@ bmmc_status rotary(const rotary_args_t* a, void* stream) {
     p.part[0].dst_head = a->out.head_stride * es;
     p.tokens = a->tokens;
     const int dims[3] = {(int)a->x.dim};
+    const chk::Spans spans = spans_of({rows_of(a->x, a->tokens, es), turn_rows(a->turns, a->tokens, 0),
+                                       turn_rows(a->turns, a->tokens, 1), turn_rows(a->turns, a->tokens, 2)},
+                                      {rows_of(a->out, a->tokens, es)});
     const int wb = word_bytes(es, {address_bits(a->x, es), address_bits(a->out, es), pair_bits(a->turns, es)});
-    return launch(p, dims, type, a->turns.flags & ROTARY_ADJACENT, wb, static_cast<cudaStream_t>(stream));
+    return launch(p, dims, type, a->turns.flags & ROTARY_ADJACENT, wb, spans, static_cast<cudaStream_t>(stream));
 }
 
 bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
@@ -519,8 +539,21 @@ bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
     p.pages = a->pages;
     p.page_size = (int)a->page_size;
     const int dims[3] = {(int)a->k.dim, (int)a->v.dim, (int)a->q.dim};
+    const Rows none{nullptr, 0, 0, 0};
+    const chk::Spans spans =
+        spans_of({k, v, with_q ? rows_of(a->q, a->tokens, es) : none, turn_rows(a->turns, a->tokens, 0),
+                  turn_rows(a->turns, a->tokens, 1), turn_rows(a->turns, a->tokens, 2),
+                  Rows{a->starts, 1, 0, (a->sequences + 1) * 4}, Rows{a->lengths, 1, 0, a->sequences * 4},
+                  Rows{a->table, a->sequences, a->table_stride * 4, a->table_columns * 4}},
+                 {cache_rows[0], cache_rows[1], with_q ? rows_of(a->q_out, a->tokens, es) : none});
     const int wb = word_bytes(es, {bits, pair_bits(a->turns, es)});
-    return launch(p, dims, type, a->turns.flags & ROTARY_ADJACENT, wb, static_cast<cudaStream_t>(stream));
+    return launch(p, dims, type, a->turns.flags & ROTARY_ADJACENT, wb, spans, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
+
+namespace bmmc {
+cudaError_t bounds_record_rotary(unsigned long long out[chk::kRecordWords], bool clear) {
+    return chk::read_record(out, clear);
+}
+}  // namespace bmmc

@@ -1,5 +1,6 @@
 // Host-side checks shared by the entry points that move tokens by maps held
-// on the device (experts.cu, rotary.cu).
+// on the device (experts.cu, rotary.cu).  Each includes bounds.cuh before this
+// header.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -32,6 +33,17 @@ struct Rows {
     uintptr_t lo() const { return (uintptr_t)base; }
     uintptr_t hi() const { return rows < 1 ? lo() : lo() + (uintptr_t)((rows - 1) * stride + span); }
 };
+
+// The ranges a checked build's launch may read and write (others drop them).
+inline chk::Spans spans_of(std::initializer_list<Rows> rd, std::initializer_list<Rows> wr) {
+    chk::Spans s{};
+    if (!chk::kEnabled) return s;
+    for (const Rows& r : rd)
+        if (r.base && r.rows > 0) s.rd[s.n_rd++] = chk::Span{r.lo(), r.hi()};
+    for (const Rows& r : wr)
+        if (r.base && r.rows > 0) s.wr[s.n_wr++] = chk::Span{r.lo(), r.hi()};
+    return s;
+}
 
 // Whether two arrays may share bytes.  Rows with one common stride that do
 // not run into each other are told apart (slices of one fused projection);

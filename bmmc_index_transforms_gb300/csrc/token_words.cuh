@@ -1,4 +1,6 @@
 // Vectors of tensor elements as the token-moving kernels load and store them.
+// Each source includes bounds.cuh, with its own BMMC_CHK_FILE tag, before this
+// header.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -114,10 +116,10 @@ struct Walk {
             const char* const end = row + (int64_t)length * sizeof(T);
             f.shift = (unsigned)reinterpret_cast<uintptr_t>(p) & 15u;
             p -= f.shift;
-            load_if(want && p + 16 > row, f.a, p);
-            load_if(want && f.shift && p + 16 < end, f.b, p + 16);
+            load_if(want && p + 16 > row && BMMC_RD_WORD_OK(p, 16), f.a, p);
+            load_if(want && f.shift && p + 16 < end && BMMC_RD_WORD_OK(p + 16, 16), f.b, p + 16);
         } else {
-            load_if(want, f.a, p);
+            load_if(want && BMMC_RD_OK(p, sizeof(f.a)), f.a, p);
         }
     }
     __device__ __forceinline__ Pack<T, W> get(const Fetch& f) const {
@@ -129,11 +131,11 @@ struct Walk {
     __device__ __forceinline__ void store(const Pack<T, W>& y, char* row, int w) const {
         const int a = at(w);
         if (!ACROSS || (a >= 0 && a + W <= length)) {
-            y.store(row + (int64_t)a * sizeof(T));
+            if (BMMC_WR_OK(row + (int64_t)a * sizeof(T), sizeof(y))) y.store(row + (int64_t)a * sizeof(T));
         } else {
 #pragma unroll
             for (int i = 0; i < W; ++i)
-                if (a + i >= 0 && a + i < length) reinterpret_cast<T*>(row)[a + i] = y.e[i];
+                if (a + i >= 0 && a + i < length && BMMC_WR_OK(reinterpret_cast<T*>(row) + a + i, sizeof(T))) reinterpret_cast<T*>(row)[a + i] = y.e[i];
         }
     }
     // zero in the elements of pack w that lie outside the row

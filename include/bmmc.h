@@ -689,14 +689,16 @@ bmmc_status paged_append(const paged_append_args_t *args, void *stream);
  * shared arrays.  A failing access is skipped, never trapped (a load gives
  * zero), and counted.  The source and destination buffers are the pass's
  * 2^n * elem_size bytes for the permutes and the caller's in_elems and
- * out_elems for lmad_copy.  This stands in for a memory checker; it is
+ * out_elems for lmad_copy; for the token moves, the arrays that the arguments
+ * describe (a cache: from its first element to its last).  This stands in for a memory checker; it is
  * slower and not meant for production. */
 typedef struct {
     int enabled;        /* 1 in a bounds-checked build, else 0 (and the rest zero) */
     uint64_t failures;  /* accesses that failed their test since the last reset */
     int site;           /* first failure: source file tag * 100000 + line
                            (tag 1: kernels.cu, 2: lmad.cu, 3: lmad_transpose_1_2.cu,
-                           4: lmad_transpose_4_8_16.cu, 5: lmad_block.cu) */
+                           4: lmad_transpose_4_8_16.cu, 5: lmad_block.cu,
+                           6: experts.cu, 7: rotary.cu) */
     int bytes;          /* its access size */
     uint64_t address;   /* its address (a shared-memory offset for shared accesses) */
     uint64_t lo, hi;    /* the range [lo, hi) it was tested against */
