@@ -121,8 +121,8 @@ __device__ __forceinline__ void sum_counts(const int* counts, int pitch, int* ba
 }
 
 // The lanes with the same key, from one ballot for each bit of the keys
-// (`bits` of them); faster here than the match instruction, whose rate is one
-// in about 30 cycles.
+// (`bits` of them).  With the match instruction in its place, and source
+// written where it goes instead of in runs, 524168 ids took 11.9 us, not 11.0.
 __device__ __forceinline__ unsigned same_key(int key, int bits) {
     unsigned same = ~0u;
     for (int b = 0; b < bits; ++b) {
@@ -133,6 +133,13 @@ __device__ __forceinline__ unsigned same_key(int key, int bits) {
     return same;
 }
 
+// What bounds it: not bytes (65521 x 8 ids of 32 bits, 256 experts, take 11.0 us
+// on the device and could be moved in 0.9) but latency: two launches, the
+// ids' first load and the barriers between a tile's steps leave 6.8 us of it
+// when all other work is skipped.  One block per SM of 32 warps was taken for
+// that reason; 64 blocks of twice the ids, which summed the blocks' counts one
+// key a load, took 18 us.  384 ids are one block and one launch: 2.6 us.
+//
 // Each block numbers its part, a tile of blockDim.x * R choices at a time.
 // Inside a warp a choice's rank among equal keys comes from the lanes of a
 // round with its key plus the warp's running count of that key; a column sum
@@ -344,7 +351,9 @@ Cover cover(int64_t tokens, int words, int most) {
 }
 
 // Pure movement: a token's row is read once and written to the rows of its
-// choices.
+// choices, one word a thread.  Bound by HBM: 16384 tokens of 4096 bf16 to 8
+// rows each, 1.21 GB, 180.8 us = 6685 GB/s, a plain copy's rate; to 2 rows
+// each 59.9 us (6720 GB/s).  32 tokens of 2048 to 4 rows: 1.7 us, a launch.
 template <class Word>
 __global__ void __launch_bounds__(256, 8) dispatch_kernel(const char* __restrict__ x, int64_t x_stride,
                                                           const int* __restrict__ slot, int64_t tokens, int choices,
@@ -370,6 +379,9 @@ __global__ void __launch_bounds__(256, 8) dispatch_kernel(const char* __restrict
 // aligned words w - 1 and w, whatever row they go to: of a row that lies
 // `to` bytes behind its granule (the source `from` bytes behind its own), the
 // words w - 1 and w cover granule w - 1 where from >= to, else granule w.
+// The loads do not wait for slot.  16384 x 2 rows of 4095 bf16: 81.7 us, 74 % of
+// the copy rate (rows of 4092 in words of 8 bytes: 84.1); a form that read each
+// choice's words once slot was known took 136-181.
 template <class T>
 __global__ void __launch_bounds__(256, 6) dispatch_across_kernel(const char* __restrict__ x, int64_t x_stride,
                                                                  const int* __restrict__ slot, int64_t tokens,
@@ -417,6 +429,15 @@ __device__ __forceinline__ float weight_at(const void* weights, int in_f32, int6
 // Each thread holds the sums of a word in 32 bits, adds the choices in order,
 // KB of them loaded at a time, and rounds once.  A choice that is not there
 // adds zero times zero.
+//
+// Bound by HBM once enough loads are in flight, and by how soon slot is there
+// before.  Measured on bf16 rows of 4096, blocks of 128: 16384 x 2 choices
+// (floor 60.3 us) KB = 2 with 8 x 256 threads on an SM 63.5, with the registers
+// it would like 75, KB = 1 70.6; 4096 x 8 (45.2) KB = 8 with 4 x 256 46.1,
+// without a bound on its registers and blocks of 256 55.9.  Rows that lie across
+// words: two loads for one, and the cut; 4096 x 8 rows of
+// 4095 60.7 us (74 %), 40961 x 2 rows of 1031 f32 93.3 (floor 75.9).  32 tokens x
+// 8 rows of 4096: 2.3 us.
 template <class T, int W, int KB, bool ACROSS>
 __global__ void __launch_bounds__(256, KB > 2 ? 4 : ACROSS && sizeof(T) == 2 ? 6 : 8) combine_kernel(const char* __restrict__ rows, int64_t row_stride, int64_t n_rows,
                                                       const int* __restrict__ slot, const void* __restrict__ weights,
@@ -475,6 +496,13 @@ __device__ __forceinline__ void sum_lanes(float (&v)[N], int lanes) {
 // at a time; the products are summed in 32 bits, by lanes and then across
 // them in a fixed order.  x threads (a power of two, or whole warps) walk a
 // token's row.
+//
+// Bound by HBM: grad_rows is written and rows are read once, grad once for KB
+// choices.  16384 x 8 rows of 4096 bf16, 2.28 GB: KB = 4 with 4 x 256 threads on
+// an SM 336.9 us = 6780 GB/s; KB = 8 (106 registers) 405, a choice after the
+// other with a barrier each 357.  16384 x 2: KB = 2, 6 x 128 98.8 us (floor 100.5),
+// blocks of 256 with the registers they would like 131.6.  Rows that lie across
+// words are bound by their instructions: 4096 x 8 rows of 4095 142.6 us (85.4).
 template <class T, int W, int KB, bool ACROSS>
 __global__ void __launch_bounds__(256, KB <= 2 ? 6 : 4) combine_backward_kernel(
     const char* __restrict__ grad, int64_t grad_stride, const char* __restrict__ rows, int64_t row_stride,

@@ -128,6 +128,17 @@ __device__ __forceinline__ float turned_second(float x, float y, float2 r) { ret
 // tokens' places and put the cosines and sines of their pairs into shared
 // memory, once for all heads; then a thread keeps those of its word of a head
 // in registers and walks over the heads, two at a time.
+//
+// Bound by HBM where there are tokens enough: 32768 tokens x 32 heads x 128 bf16
+// 79.7 us = 6740 GB/s; 16001 tokens' queries, keys and values (32 + 8 + 8 heads)
+// into pages 64.2 us (floor 58.9; 64001 tokens 228.5, at the copy rate): what is left
+// is the start of a block, whose loads of starts, lengths and table follow one
+// another, which is why positions, frequencies and, to L2, the heads are sent
+// for first (without that 76 us).  12 heads of 96 f32 with adjacent pairs, 10007
+// tokens: 17.1 us (13.8).  Shapes tried there: one head at a time 71.5 us, four
+// 71-95; 6 blocks of 256 threads on an SM instead of 4, whose registers then spill,
+// 88; blocks of 256 threads 70.8, of 128 68.1.  256 single tokens: 4.3 us, the
+// chain lengths - table - sine - store and a launch.
 template <class T, int W, bool ADJACENT>
 __global__ void __launch_bounds__(kMostThreads, 4) move_heads_kernel(const __grid_constant__ MoveParams p
                                                                         BMMC_SPANS_PARAM) {
@@ -276,8 +287,9 @@ __global__ void __launch_bounds__(kMostThreads, 4) move_heads_kernel(const __gri
 }
 
 // Threads of a token: as many as the words of its largest part in a small
-// call, a quarter of them in one that fills the machine, so that each thread
-// uses its cosines and sines for several heads.  *split: the parts go to
+// call (so that all its loads are in flight at once), a quarter of them in one
+// that fills the machine (each thread uses its cosines and sines for several
+// heads: append of 16001 tokens 70.8 us, with half 94, with an eighth 73.9).  *split: the parts go to
 // blocks of their own, where all of these still run at once.  Returns the
 // block's threads.
 int deal_out(MoveParams& p, const int (&dims)[3], int W, int es, bool adjacent, bool* split) {

@@ -16,6 +16,10 @@ row-major array of that shape), lmad_transpose (the shape's axes
 reversed, made contiguous) and lmad_permute (the shape's axes in the order
 --perm, out dimension k = in dimension perm[k], made contiguous; --blocked
 auto / force / never chooses for the blocked copy).
+Moves of tokens (--tokens, --type; --choices, --experts, --hidden or --heads,
+--kv-heads, --dim): token_sort, token_dispatch, token_combine,
+token_combine_backward, token_rotary (positions on three axes), token_append
+(8 sequences, pages of 64 entries, queries turned with the keys).
 Prints the plan and the CUDA-event time of each repetition.
 """
 
@@ -47,7 +51,8 @@ def main(argv=None):
     ap.add_argument("--kind", default="random",
                     choices=["random", "worst", "bitrev", "transpose", "dims5", "copy", "two_factor",
                              "complement", "window", "lmad_slice_2d", "lmad_slice_3d", "lmad_reversed_rows",
-                             "lmad_transpose", "lmad_permute"])
+                             "lmad_transpose", "lmad_permute", "token_sort", "token_dispatch", "token_combine",
+                             "token_combine_backward", "token_rotary", "token_append"])
     ap.add_argument("--n", type=int, default=26)
     ap.add_argument("--elem", type=int, default=4)
     ap.add_argument("--seed", type=int, default=0)
@@ -59,7 +64,13 @@ def main(argv=None):
     ap.add_argument("--window", type=int, default=22, help="window: log2 elements of a window")
     ap.add_argument("--perm", default="", help="lmad_permute: axis order of the destination")
     ap.add_argument("--blocked", default="auto", choices=["auto", "force", "never"])
+    ap.add_argument("--type", default="bf16", choices=["f32", "f16", "bf16"])
+    for name, value in (("tokens", 4096), ("choices", 8), ("experts", 64), ("hidden", 4096), ("heads", 32),
+                        ("kv-heads", 8), ("dim", 128)):
+        ap.add_argument(f"--{name}", type=int, default=value)
     a = ap.parse_args(argv)
+    if a.kind.startswith("token_"):
+        return token_case(a)
     if a.kind.startswith("lmad_"):
         return lmad_case(a)
     n, elem = a.n, a.elem
@@ -137,6 +148,57 @@ def lmad_view(a) -> dict:
         return dict(sizes=shape, in_offset=0, in_strides=synth.row_major_strides(shape), in_elems=total,
                     out_offset=0, out_strides=out_strides, out_elems=total)
     return synth.page_lmad_workload(a.kind[len("lmad_"):], shape)
+
+
+def token_call(a):
+    """The call of a token_* kind, and the bytes that it cannot do without."""
+    g = torch.Generator("cuda").manual_seed(a.seed)
+    dtype = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[a.type]
+    T, K, H, es = a.tokens, a.choices, a.hidden, 4 if a.type == "f32" else 2
+    new = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=dtype)  # noqa: E731
+    if a.kind in ("token_rotary", "token_append"):
+        pairs = a.dim // 2
+        freq = 10000.0 ** (-torch.arange(pairs, device="cuda") / pairs)
+        axes = (torch.arange(pairs, device="cuda") * 3 // pairs).int()
+        positions = torch.randint(0, 4096, (3, T), generator=g, device="cuda").int()
+        if a.kind == "token_rotary":
+            x = new(T, a.heads, a.dim)
+            return lambda: bm.rotary(x, positions, freq, axes), 2 * x.numel() * es
+        qkv = new(T, a.heads + 2 * a.kv_heads, a.dim)
+        q, k, v = qkv.split([a.heads, a.kv_heads, a.kv_heads], dim=1)
+        starts = (torch.arange(9, device="cuda") * T // 8).int()
+        columns = (T // 8 + 1000) // 64 + 2
+        table = torch.randperm(8 * columns, generator=g, device="cuda").int().view(8, columns)
+        lengths = torch.randint(0, 1000, (8,), generator=g, device="cuda").int()
+        caches = [new(8 * columns, 64, a.kv_heads, a.dim) for _ in range(2)]
+        return lambda: bm.paged_append(k, v, *caches, table, lengths, starts=starts, q=q, positions=positions,
+                                       inv_freq=freq, pair_axes=axes), 2 * qkv.numel() * es
+    ids = torch.rand(T, a.experts, generator=g, device="cuda").topk(K, dim=1)[1]
+    slot = bm.expert_sort(ids, a.experts)[0]
+    if a.kind == "token_sort":
+        return lambda: bm.expert_sort(ids, a.experts), T * K * 16
+    if a.kind == "token_dispatch":
+        x = new(T, H)
+        return lambda: bm.expert_dispatch(x, slot), (T + T * K) * H * es
+    rows, w = new(T * K, H), torch.rand(T, K, generator=g, device="cuda")
+    if a.kind == "token_combine":
+        return lambda: bm.expert_combine(rows, slot, w), (T + T * K) * H * es
+    x = new(T, H)
+    return lambda: bm.expert_combine_backward(x, rows, slot, w), (T + 2 * T * K) * H * es
+
+
+def token_case(a):
+    call, nbytes = token_call(a)
+    stream = torch.cuda.current_stream()
+    for r in range(a.reps):
+        s, t = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        s.record(stream)
+        call()
+        t.record(stream)
+        torch.cuda.synchronize()
+        ms = s.elapsed_time(t)
+        print(f"rep {r}: {ms:.4f} ms, {nbytes / ms / 1e6:.1f} GB/s effective")
+    return 0
 
 
 def lmad_case(a):

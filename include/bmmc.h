@@ -543,6 +543,9 @@ bmmc_status bmmc_copy(const void *in, void *out, size_t bytes, void *stream);
  *     their element (MISALIGNED); 16-byte aligned rows are the fast case.
  *   - What a map says is checked where it is used: an index outside its array
  *     moves nothing and reads nothing out of range.
+ *   - Rows that are not multiples of 8 bytes apart, long or aligned are read in
+ *     whole aligned 16-byte words that hold at least one byte of the row (as
+ *     lmad_copy reads); only the outputs' own elements are written.
  *   - Calls enqueue work on `stream`, allocate nothing, can be captured in a
  *     CUDA graph, and give the same bits every time.
  * Errors of all of them: INVALID_ARG (a null pointer, a size or stride out of
@@ -625,7 +628,8 @@ typedef struct {
 
 /* How heads are turned: pair i of the first 2 * pairs elements of a head by
  * the angle position * inv_freq[i] (a product in 32 bits), position =
- * positions[a * axis_stride + t] on the pair's axis a = pair_axes[i]:
+ * positions[a * axis_stride + t] (converted to 32 bits) on the pair's axis a =
+ * pair_axes[i]:
  *   (x, y) -> (x cos - y sin, y cos + x sin).
  * The rest of a head is copied. */
 typedef struct {
