@@ -63,12 +63,13 @@ constexpr bool kEnabled = true;
 // One record per translation unit (each .cu file is compiled on its own).
 static __device__ unsigned long long g_record[kRecordWords];
 
-// The launch's buffers and up to three shared arrays, written by every
+// The launch's buffers and up to four shared arrays, written by every
 // thread on entry (all with the same values, each thread reading back its
 // own write, so no barrier is needed).
+constexpr int kMaxShared = 4;
 struct Entry {
     Bounds b;
-    uint32_t sh_lo[3], sh_hi[3];
+    uint32_t sh_lo[kMaxShared], sh_hi[kMaxShared];
 };
 static __shared__ Entry s_entry;
 
@@ -87,12 +88,12 @@ __device__ __forceinline__ uint32_t sh_off(const void* p) { return (uint32_t)__c
 
 __device__ __forceinline__ void enter(const Bounds& b, const void* s0 = nullptr, uint32_t n0 = 0,
                                       const void* s1 = nullptr, uint32_t n1 = 0, const void* s2 = nullptr,
-                                      uint32_t n2 = 0) {
+                                      uint32_t n2 = 0, const void* s3 = nullptr, uint32_t n3 = 0) {
     s_entry.b = b;
-    const void* s[3] = {s0, s1, s2};
-    const uint32_t n[3] = {n0, n1, n2};
+    const void* s[kMaxShared] = {s0, s1, s2, s3};
+    const uint32_t n[kMaxShared] = {n0, n1, n2, n3};
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < kMaxShared; ++i) {
         s_entry.sh_lo[i] = s[i] ? sh_off(s[i]) : 0u;
         s_entry.sh_hi[i] = s[i] ? sh_off(s[i]) + n[i] : 0u;
     }
@@ -123,7 +124,7 @@ __device__ __forceinline__ bool in_word_ok(const void* p, unsigned bytes, int si
 __device__ __forceinline__ bool sh_ok(const void* p, unsigned bytes, int site) {
     const uint32_t a = sh_off(p);
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
+    for (int i = 0; i < kMaxShared; ++i)
         if (a >= s_entry.sh_lo[i] && a + bytes <= s_entry.sh_hi[i] && a + bytes >= a) return true;
     fail(site, a, s_entry.sh_lo[0], s_entry.sh_hi[0], bytes);
     return false;
@@ -134,9 +135,9 @@ static __shared__ Spans s_spans;
 
 __device__ __forceinline__ void enter_spans(const Spans& b, const void* s0 = nullptr, uint32_t n0 = 0,
                                             const void* s1 = nullptr, uint32_t n1 = 0, const void* s2 = nullptr,
-                                            uint32_t n2 = 0) {
+                                            uint32_t n2 = 0, const void* s3 = nullptr, uint32_t n3 = 0) {
     s_spans = b;
-    enter(Bounds{}, s0, n0, s1, n1, s2, n2);
+    enter(Bounds{}, s0, n0, s1, n1, s2, n2, s3, n3);
 }
 
 __device__ __forceinline__ bool inside_one(const void* p, unsigned bytes, const Span* s, int n, int site) {

@@ -422,7 +422,9 @@ __global__ void __launch_bounds__(256, 6) dispatch_across_kernel(const char* __r
 // A weight of the rows' type or of 32 bits.
 template <class T>
 __device__ __forceinline__ float weight_at(const void* weights, int in_f32, int64_t i) {
-    if (!BMMC_RD_OK(static_cast<const char*>(weights) + i * (in_f32 ? 4 : (int)sizeof(T)), in_f32 ? 4 : sizeof(T))) return 0.0f;
+    const int bytes = in_f32 ? 4 : (int)sizeof(T);
+    (void)bytes;
+    if (!BMMC_RD_OK(static_cast<const char*>(weights) + i * bytes, bytes)) return 0.0f;
     return in_f32 ? static_cast<const float*>(weights)[i] : to_f32(static_cast<const T*>(weights)[i]);
 }
 
@@ -435,14 +437,14 @@ __device__ __forceinline__ float weight_at(const void* weights, int in_f32, int6
 // (floor 60.3 us) KB = 2 with 8 x 256 threads on an SM 63.5, with the registers
 // it would like 75, KB = 1 70.6; 4096 x 8 (45.2) KB = 8 with 4 x 256 46.1,
 // without a bound on its registers and blocks of 256 55.9.  Rows that lie across
-// words: two loads for one, and the cut; 4096 x 8 rows of
-// 4095 60.7 us (74 %), 40961 x 2 rows of 1031 f32 93.3 (floor 75.9).  32 tokens x
-// 8 rows of 4096: 2.3 us.
+// words: two loads for one, and the cut; 4096 x 8 rows of 4095 60.7 us (74 %),
+// 40961 x 2 rows of 1031 f32 93.3 (floor 75.9).  32 tokens x 8 rows of 4096:
+// 2.3 us.
 template <class T, int W, int KB, bool ACROSS>
-__global__ void __launch_bounds__(256, KB > 2 ? 4 : ACROSS && sizeof(T) == 2 ? 6 : 8) combine_kernel(const char* __restrict__ rows, int64_t row_stride, int64_t n_rows,
-                                                      const int* __restrict__ slot, const void* __restrict__ weights,
-                                                      int weights_f32, int64_t tokens, int choices, int length,
-                                                      char* __restrict__ out, int64_t out_stride BMMC_SPANS_PARAM) {
+__global__ void __launch_bounds__(256, KB > 2 ? 4 : ACROSS && sizeof(T) == 2 ? 6 : 8)
+    combine_kernel(const char* __restrict__ rows, int64_t row_stride, int64_t n_rows, const int* __restrict__ slot,
+                   const void* __restrict__ weights, int weights_f32, int64_t tokens, int choices, int length,
+                   char* __restrict__ out, int64_t out_stride BMMC_SPANS_PARAM) {
     BMMC_SPANS_ENTER_GLOBAL();
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const int w = blockIdx.y * blockDim.x + threadIdx.x;
@@ -589,9 +591,9 @@ __global__ void __launch_bounds__(256, KB <= 2 ? 6 : 4) combine_backward_kernel(
             for (int j = 0; j < KB; ++j)
                 if (k0 + j < choices) {
                     const int64_t at = t * choices + k0 + j;
-                    if (!BMMC_WR_OK(static_cast<char*>(grad_weights) + at * (weights_f32 ? 4 : (int)sizeof(T)),
-                                    weights_f32 ? 4 : sizeof(T)))
-                        continue;
+                    const int bytes = weights_f32 ? 4 : (int)sizeof(T);
+                    (void)bytes;
+                    if (!BMMC_WR_OK(static_cast<char*>(grad_weights) + at * bytes, bytes)) continue;
                     if (weights_f32) static_cast<float*>(grad_weights)[at] = dot[j];
                     else static_cast<T*>(grad_weights)[at] = from_f32<T>(dot[j]);
                 }
@@ -639,8 +641,9 @@ bmmc_status check_moves(int64_t tokens, int choices, int64_t hidden, int64_t n_r
     return BMMC_OK;
 }
 
-bool bad_stride(int64_t stride, int64_t hidden, int64_t rows) {
-    return stride > kMaxStride || (rows > 1 && stride < hidden) || stride < 0;
+// Rows that are written lie apart.
+bool bad_output_stride(int64_t stride, int64_t hidden, int64_t rows) {
+    return bad_stride(stride, rows) || (rows > 1 && stride < hidden);
 }
 
 bool misaligned(const void* p, size_t bytes) { return (uintptr_t)p & (bytes - 1); }
@@ -697,7 +700,7 @@ bmmc_status expert_dispatch(const void* x, int64_t x_stride, const int32_t* slot
     const bool device = device_pointers(type);
     bmmc_status s = check_moves(tokens, choices, hidden, n_rows, type, &es);
     if (s != BMMC_OK) return s;
-    if (bad_stride(x_stride, 0, tokens) || bad_stride(row_stride, hidden, n_rows)) return BMMC_ERR_INVALID_ARG;
+    if (bad_stride(x_stride, tokens) || bad_output_stride(row_stride, hidden, n_rows)) return BMMC_ERR_INVALID_ARG;
     if (!n_rows) return BMMC_OK;
     if (!x || !slot || !rows) return BMMC_ERR_INVALID_ARG;
     if (misaligned(x, es) || misaligned(rows, es) || misaligned(slot, 4)) return BMMC_ERR_MISALIGNED;
@@ -738,7 +741,7 @@ bmmc_status expert_combine(const void* rows, int64_t row_stride, int64_t n_rows,
     bmmc_status s = check_moves(tokens, choices, hidden, n_rows, type, &es);
     if (s != BMMC_OK) return s;
     if (weights && weight_type != BMMC_F32 && weight_type != type) return BMMC_ERR_UNSUPPORTED_ELEM;
-    if (bad_stride(row_stride, 0, n_rows) || bad_stride(out_stride, hidden, tokens)) return BMMC_ERR_INVALID_ARG;
+    if (bad_stride(row_stride, n_rows) || bad_output_stride(out_stride, hidden, tokens)) return BMMC_ERR_INVALID_ARG;
     if (!tokens) return BMMC_OK;
     if ((!rows && n_rows) || !slot || !out) return BMMC_ERR_INVALID_ARG;
     const int ws = weights ? dtype_bytes(weight_type) : 4;
@@ -780,8 +783,8 @@ bmmc_status expert_combine_backward(const void* grad, int64_t grad_stride, const
     bmmc_status s = check_moves(tokens, choices, hidden, n_rows, type, &es);
     if (s != BMMC_OK) return s;
     if (weight_type != BMMC_F32 && weight_type != type) return BMMC_ERR_UNSUPPORTED_ELEM;
-    if (bad_stride(grad_stride, 0, tokens) || bad_stride(row_stride, 0, n_rows) ||
-        bad_stride(grad_row_stride, hidden, n_rows))
+    if (bad_stride(grad_stride, tokens) || bad_stride(row_stride, n_rows) ||
+        bad_output_stride(grad_row_stride, hidden, n_rows))
         return BMMC_ERR_INVALID_ARG;
     if (!tokens) return BMMC_OK;
     if (!grad || !slot || !weights || !grad_weights || (n_rows && (!rows || !grad_rows))) return BMMC_ERR_INVALID_ARG;

@@ -38,6 +38,8 @@ struct Heads {
     int heads, turned, place;
     int turning, items;  // words of a head that are turned (pairs of words in halves), and all
     int across, magic;   // threads side by side on a head's words, and 65536 / across rounded up
+    int words, batch;    // staged rows: words of a head, heads of a warp at a time
+    unsigned words_magic;  // 2^32 / words rounded up (words > 1)
     unsigned ahead;      // bytes of a token's heads to fetch ahead; 0: they do not lie in one run of 16-byte words
 };
 
@@ -46,6 +48,8 @@ struct MoveParams {
     int parts;
     int64_t tokens;
     int group_log2;  // threads of a token
+    unsigned pairs_magic;  // staged rows: 2^32 / pairs rounded up (pairs > 1)
+    bool adjacent;         // staged rows: pairs side by side
     bool device;     // the heads are the device's own memory and may be fetched ahead
     // rotation
     const void* positions;  // NULL: the token's place in its sequence
@@ -124,33 +128,13 @@ __device__ Place place_of(const MoveParams& p, int64_t t, int64_t b) {
 __device__ __forceinline__ float turned_first(float x, float y, float2 r) { return fmaf(x, r.x, -__fmul_rn(y, r.y)); }
 __device__ __forceinline__ float turned_second(float x, float y, float2 r) { return fmaf(y, r.x, __fmul_rn(x, r.y)); }
 
-// A block takes some tokens, a group of threads each.  Its threads find the
-// tokens' places and put the cosines and sines of their pairs into shared
-// memory, once for all heads; then a thread keeps those of its word of a head
-// in registers and walks over the heads, two at a time.
-//
-// Bound by HBM where there are tokens enough: 32768 tokens x 32 heads x 128 bf16
-// 79.7 us = 6740 GB/s; 16001 tokens' queries, keys and values (32 + 8 + 8 heads)
-// into pages 64.2 us (floor 58.9; 64001 tokens 228.5, at the copy rate): what is left
-// is the start of a block, whose loads of starts, lengths and table follow one
-// another, which is why positions, frequencies and, to L2, the heads are sent
-// for first (without that 76 us).  12 heads of 96 f32 with adjacent pairs, 10007
-// tokens: 17.1 us (13.8).  Shapes tried there: one head at a time 71.5 us, four
-// 71-95; 6 blocks of 256 threads on an SM instead of 4, whose registers then spill,
-// 88; blocks of 256 threads 70.8, of 128 68.1.  256 single tokens: 4.3 us, the
-// chain lengths - table - sine - store and a launch.
-template <class T, int W, bool ADJACENT>
-__global__ void __launch_bounds__(kMostThreads, 4) move_heads_kernel(const __grid_constant__ MoveParams p
-                                                                        BMMC_SPANS_PARAM) {
-    extern __shared__ float2 s_turn[];  // [tokens of the block][pairs] cos, sin
-    __shared__ int64_t s_place[2][kMaxTokensPerBlock];  // byte offsets in the caches, -1 = none
-    __shared__ float s_position[kMaxTokensPerBlock];
-    BMMC_SPANS_ENTER(s_turn, chk::dyn_smem_bytes(), s_place, sizeof(s_place), s_position, sizeof(s_position));
-    const int tid = threadIdx.x, threads = blockDim.x, per_block = threads >> p.group_log2;
-    const int64_t t0 = (int64_t)blockIdx.x * per_block;
-    const int nt = (int)min((int64_t)per_block, p.tokens - t0);
-    // a block of a small call takes one part only
-    const int first_part = gridDim.y > 1 ? blockIdx.y : 0, last_part = gridDim.y > 1 ? first_part + 1 : p.parts;
+// The start of a block that takes tokens t0 .. t0 + nt - 1 and some of the
+// parts: the tokens' places in the caches and positions, and the cosines and
+// sines of their pairs, into shared memory; the whole block takes part.
+__device__ __forceinline__ void begin_block(const MoveParams& p, int64_t t0, int nt, int first_part, int last_part,
+                                            float2* s_turn, int64_t (&s_place)[2][kMaxTokensPerBlock],
+                                            float (&s_position)[kMaxTokensPerBlock]) {
+    const int tid = threadIdx.x, threads = blockDim.x;
     const bool turning = p.pairs && p.part[first_part].turned;
     // A thread's first turns (what they need but for a position that follows
     // from the place), and all the heads (to L2), are on their way while the
@@ -166,8 +150,9 @@ __global__ void __launch_bounds__(kMostThreads, 4) move_heads_kernel(const __gri
         from_place = !p.positions && axis == 0;
         if (p.positions && axis >= 0 && axis < p.axes) {
             const int64_t j = axis * p.axis_stride + t0 + k;
-            if (BMMC_RD_OK(static_cast<const char*>(p.positions) + j * p.position_bytes, p.position_bytes)) at = p.position_bytes == 4 ? (float)static_cast<const int32_t*>(p.positions)[j]
-                                       : (float)static_cast<const int64_t*>(p.positions)[j];
+            if (BMMC_RD_OK(static_cast<const char*>(p.positions) + j * p.position_bytes, p.position_bytes))
+                at = p.position_bytes == 4 ? (float)static_cast<const int32_t*>(p.positions)[j]
+                                           : (float)static_cast<const int64_t*>(p.positions)[j];
         }
     };
 #pragma unroll
@@ -182,7 +167,7 @@ __global__ void __launch_bounds__(kMostThreads, 4) move_heads_kernel(const __gri
                          : "memory");
     }
     if (p.page_size) {
-        if (p.starts && per_block <= 8) {
+        if (p.starts && nt <= 8) {
             for (int i = tid >> 5; i < nt; i += threads >> 5) {
                 const Place r = place_of(p, t0 + i, find_sequence_warp(p.starts, p.sequences, t0 + i, tid & 31));
                 if ((tid & 31) == 0 && BMMC_SH_OK(&s_place[1][i], 8) && BMMC_SH_OK(s_position + i, 4))
@@ -214,6 +199,36 @@ __global__ void __launch_bounds__(kMostThreads, 4) move_heads_kernel(const __gri
         }
     }
     __syncthreads();
+}
+
+// A block takes some tokens, a group of threads each.  Its threads find the
+// tokens' places and put the cosines and sines of their pairs into shared
+// memory, once for all heads; then a thread keeps those of its word of a head
+// in registers and walks over the heads, two at a time.
+//
+// Bound by HBM where there are tokens enough: 32768 tokens x 32 heads x 128 bf16
+// 79.7 us = 6740 GB/s; 16001 tokens' queries, keys and values (32 + 8 + 8 heads)
+// into pages 64.2 us (floor 58.9; 64001 tokens 228.5, at the copy rate): what is left
+// is the start of a block, whose loads of starts, lengths and table follow one
+// another, which is why positions, frequencies and, to L2, the heads are sent
+// for first (without that 76 us).  12 heads of 96 f32 with adjacent pairs, 10007
+// tokens: 17.1 us (13.8).  Shapes tried there: one head at a time 71.5 us, four
+// 71-95; 6 blocks of 256 threads on an SM instead of 4, whose registers then spill,
+// 88; blocks of 256 threads 70.8, of 128 68.1.  256 single tokens: 4.3 us, the
+// chain lengths - table - sine - store and a launch.
+template <class T, int W, bool ADJACENT>
+__global__ void __launch_bounds__(kMostThreads, 4)
+    move_heads_kernel(const __grid_constant__ MoveParams p BMMC_SPANS_PARAM) {
+    extern __shared__ float2 s_turn[];  // [tokens of the block][pairs] cos, sin
+    __shared__ int64_t s_place[2][kMaxTokensPerBlock];  // byte offsets in the caches, -1 = none
+    __shared__ float s_position[kMaxTokensPerBlock];
+    BMMC_SPANS_ENTER(s_turn, chk::dyn_smem_bytes(), s_place, sizeof(s_place), s_position, sizeof(s_position));
+    const int tid = threadIdx.x, per_block = blockDim.x >> p.group_log2;
+    const int64_t t0 = (int64_t)blockIdx.x * per_block;
+    const int nt = (int)min((int64_t)per_block, p.tokens - t0);
+    // a block of a small call takes one part only
+    const int first_part = gridDim.y > 1 ? blockIdx.y : 0, last_part = gridDim.y > 1 ? first_part + 1 : p.parts;
+    begin_block(p, t0, nt, first_part, last_part, s_turn, s_place, s_position);
     const int k = tid >> p.group_log2, in = tid & ((1 << p.group_log2) - 1);
     if (k >= nt) return;
     for (int q = first_part; q < last_part; ++q) {
@@ -286,12 +301,100 @@ __global__ void __launch_bounds__(kMostThreads, 4) move_heads_kernel(const __gri
     }
 }
 
+constexpr int kRowThreads = 128;
+constexpr int kRowBytes = 2048;  // of a warp's rows in shared memory
+constexpr int kRowBatch = 32;    // most rows of a warp at a time
+
+// x / d for x, d < 2^16, with magic = 2^32 / d rounded up.
+__device__ __forceinline__ int quotient(int x, int d, unsigned magic) { return d == 1 ? x : (int)__umulhi(x, magic); }
+
+// The same for heads whose pairs do not lie in the words that their rows allow
+// (an odd number of pairs in halves of a 16-bit type): a warp brings some rows
+// (heads of tokens) into shared memory in words, turns their pairs there by
+// element, and writes them back in words.
+//
+// 16384 tokens x 16 heads of 128 bf16 (floor 20.1 us): 37 pairs in halves 33.5 us,
+// by element from memory 108; 36 pairs 30.6, in words of 8 bytes 40.5; 16001
+// tokens appended with 37 pairs 92 us, by element 290.  Rows of 4-byte words (heads
+// of 66) are no faster this way (49 and 47 us) and keep the other.  2 KB of rows a
+// warp in flight; with 1 KB the append takes 98, with 8 tokens a block instead of 4
+// 108.
+template <class T, class Word>
+__global__ void __launch_bounds__(kRowThreads)
+    move_rows_kernel(const __grid_constant__ MoveParams p BMMC_SPANS_PARAM) {
+    constexpr int kWarps = kRowThreads / 32;
+    extern __shared__ float2 s_turn[];  // [tokens of the block][pairs] cos, sin
+    __shared__ int64_t s_place[2][kMaxTokensPerBlock];
+    __shared__ float s_position[kMaxTokensPerBlock];
+    __shared__ struct {
+        __align__(16) char data[kRowBytes];
+        const char* src[kRowBatch];
+        char* dst[kRowBatch];  // NULL: not written
+        int turns[kRowBatch];  // where its token's turns start
+    } s_rows[kWarps];
+    BMMC_SPANS_ENTER(s_turn, chk::dyn_smem_bytes(), s_place, sizeof(s_place), s_position, sizeof(s_position), s_rows,
+                     sizeof(s_rows));
+    const int tid = threadIdx.x, lane = tid & 31, per_block = blockDim.x >> p.group_log2;
+    const int64_t t0 = (int64_t)blockIdx.x * per_block;
+    const int nt = (int)min((int64_t)per_block, p.tokens - t0);
+    const int first_part = gridDim.y > 1 ? blockIdx.y : 0, last_part = gridDim.y > 1 ? first_part + 1 : p.parts;
+    begin_block(p, t0, nt, first_part, last_part, s_turn, s_place, s_position);
+    auto& mine = s_rows[tid >> 5];
+    Word* const words = reinterpret_cast<Word*>(mine.data);
+    T* const elements = reinterpret_cast<T*>(mine.data);
+    for (int q = first_part; q < last_part; ++q) {
+        const Heads& h = p.part[q];
+        const int row_elements = h.words * (int)(sizeof(Word) / sizeof(T));
+        for (int r0 = (tid >> 5) * h.batch; r0 < nt * h.heads; r0 += kWarps * h.batch) {
+            const int rows = min(h.batch, nt * h.heads - r0);
+            if (lane < rows) {
+                const int k = (r0 + lane) / h.heads, head = r0 + lane - k * h.heads;
+                const int64_t to = h.place ? s_place[h.place - 1][k] : (t0 + k) * h.dst_token;
+                mine.src[lane] = h.src + (t0 + k) * h.src_token + head * h.src_head;
+                mine.dst[lane] = to < 0 ? nullptr : h.dst + to + head * h.dst_head;
+                mine.turns[lane] = k * p.pairs;
+            }
+            __syncwarp();
+#pragma unroll 4
+            for (int x = lane; x < rows * h.words; x += 32) {
+                const int row = quotient(x, h.words, h.words_magic);
+                const char* const from = mine.src[row] + (x - row * h.words) * sizeof(Word);
+                if (BMMC_RD_OK(from, sizeof(Word)) && BMMC_SH_OK(words + x, sizeof(Word)))
+                    words[x] = *reinterpret_cast<const Word*>(from);
+            }
+            __syncwarp();
+            if (h.turned) {
+#pragma unroll 2
+                for (int x = lane; x < rows * p.pairs; x += 32) {
+                    const int row = quotient(x, p.pairs, p.pairs_magic), i = x - row * p.pairs;
+                    T* const a = elements + row * row_elements + (p.adjacent ? 2 * i : i);
+                    T* const b = a + (p.adjacent ? 1 : p.pairs);
+                    const float2* const turn = s_turn + mine.turns[row] + i;
+                    if (!BMMC_SH_OK(a, sizeof(T)) || !BMMC_SH_OK(b, sizeof(T)) || !BMMC_SH_OK(turn, 8)) continue;
+                    const float2 r = *turn;
+                    const float u = to_f32(*a), v = to_f32(*b);
+                    *a = from_f32<T>(turned_first(u, v, r));
+                    *b = from_f32<T>(turned_second(u, v, r));
+                }
+                __syncwarp();
+            }
+#pragma unroll 4
+            for (int x = lane; x < rows * h.words; x += 32) {
+                const int row = quotient(x, h.words, h.words_magic);
+                char* const to = mine.dst[row] + (x - row * h.words) * sizeof(Word);
+                if (mine.dst[row] && BMMC_WR_OK(to, sizeof(Word))) *reinterpret_cast<Word*>(to) = words[x];
+            }
+            __syncwarp();
+        }
+    }
+}
+
 // Threads of a token: as many as the words of its largest part in a small
 // call (so that all its loads are in flight at once), a quarter of them in one
 // that fills the machine (each thread uses its cosines and sines for several
-// heads: append of 16001 tokens 70.8 us, with half 94, with an eighth 73.9).  *split: the parts go to
-// blocks of their own, where all of these still run at once.  Returns the
-// block's threads.
+// heads: append of 16001 tokens 70.8 us, with half 94, with an eighth 73.9).
+// *split: the parts go to blocks of their own, where all of these still run
+// at once.  Returns the block's threads.
 int deal_out(MoveParams& p, const int (&dims)[3], int W, int es, bool adjacent, bool* split) {
     int64_t most = 1;
     for (int q = 0; q < p.parts; ++q) {
@@ -320,6 +423,32 @@ int deal_out(MoveParams& p, const int (&dims)[3], int W, int es, bool adjacent, 
     return threads;
 }
 
+// Staged rows: words of `bytes`; tokens of a block by the size of the call.
+template <class T, class Word>
+bmmc_status launch_rows(MoveParams& p, const int (&dims)[3], bool adjacent, const chk::Spans& spans, cudaStream_t st) {
+    (void)spans;
+    p.adjacent = adjacent;
+    p.pairs_magic = p.pairs > 1 ? (unsigned)((((uint64_t)1 << 32) + p.pairs - 1) / p.pairs) : 0;
+    int per_block = p.tokens >= 152 * 32 ? 4 : 1;
+    while (per_block > 1 && per_block * p.pairs * sizeof(float2) > 32 * 1024) per_block >>= 1;
+    p.group_log2 = per_block == 4 ? 5 : per_block == 2 ? 6 : 7;
+    for (int q = 0; q < p.parts; ++q) {
+        Heads& h = p.part[q];
+        const int row_bytes = dims[q] * (int)sizeof(T);
+        h.words = row_bytes / (int)sizeof(Word);
+        h.words_magic = h.words > 1 ? (unsigned)((((uint64_t)1 << 32) + h.words - 1) / h.words) : 0;
+        // no more rows a warp than its share
+        h.batch = std::min({kRowBytes / row_bytes, kRowBatch, (per_block * h.heads + 3) / 4});
+        const bool dense = p.device && sizeof(Word) == 16 && (h.heads < 2 || h.src_head == (int64_t)row_bytes);
+        h.ahead = dense ? std::min((unsigned)(h.heads * row_bytes), 65536u) : 0u;
+    }
+    const bool split = p.parts > 1 && p.tokens * p.parts <= 152 * 8;
+    const dim3 grid((unsigned)((p.tokens + per_block - 1) / per_block), split ? p.parts : 1);
+    move_rows_kernel<T, Word><<<grid, kRowThreads, (size_t)per_block * p.pairs * sizeof(float2), st>>>(
+        p BMMC_SPANS_ARG(spans));
+    return launched();
+}
+
 template <class T, int W>
 bmmc_status launch_width(MoveParams& p, const int (&dims)[3], bool adjacent, const chk::Spans& spans, cudaStream_t st) {
     (void)spans;
@@ -334,8 +463,14 @@ bmmc_status launch_width(MoveParams& p, const int (&dims)[3], bool adjacent, con
 }
 
 template <class T>
-bmmc_status launch_type(MoveParams& p, const int (&dims)[3], bool adjacent, int bytes, const chk::Spans& spans, cudaStream_t st) {
+bmmc_status launch_type(MoveParams& p, const int (&dims)[3], bool adjacent, int bytes, int row_word,
+                        const chk::Spans& spans, cudaStream_t st) {
     constexpr int es = sizeof(T);
+    bool staged = row_word >= 8 && row_word > bytes;
+    for (int q = 0; q < p.parts; ++q) staged = staged && dims[q] * es <= kRowBytes;
+    if (staged)
+        return row_word == 16 ? launch_rows<T, uint4>(p, dims, adjacent, spans, st)
+                              : launch_rows<T, uint2>(p, dims, adjacent, spans, st);
     switch (bytes) {
         case 16: return launch_width<T, 16 / es>(p, dims, adjacent, spans, st);
         case 8: return launch_width<T, 8 / es>(p, dims, adjacent, spans, st);
@@ -344,19 +479,18 @@ bmmc_status launch_type(MoveParams& p, const int (&dims)[3], bool adjacent, int 
     return launch_width<T, 1>(p, dims, adjacent, spans, st);
 }
 
-bmmc_status launch(MoveParams& p, const int (&dims)[3], int type, bool adjacent, int bytes, const chk::Spans& spans, cudaStream_t st) {
+bmmc_status launch(MoveParams& p, const int (&dims)[3], int type, bool adjacent, int bytes, int row_word,
+                   const chk::Spans& spans, cudaStream_t st) {
     switch (type) {
-        case BMMC_F32: return launch_type<float>(p, dims, adjacent, bytes, spans, st);
-        case BMMC_F16: return launch_type<__half>(p, dims, adjacent, bytes, spans, st);
+        case BMMC_F32: return launch_type<float>(p, dims, adjacent, bytes, row_word, spans, st);
+        case BMMC_F16: return launch_type<__half>(p, dims, adjacent, bytes, row_word, spans, st);
     }
-    return launch_type<__nv_bfloat16>(p, dims, adjacent, bytes, spans, st);
+    return launch_type<__nv_bfloat16>(p, dims, adjacent, bytes, row_word, spans, st);
 }
 
-bool bad_stride(int64_t s) { return s < 0 || s > kMaxStride; }
-
-bmmc_status check_heads(const token_heads_t& x, int es) {
+bmmc_status check_heads(const token_heads_t& x, int64_t tokens, int es) {
     if (!x.data || x.heads < 1 || x.dim < 1 || x.dim > ROTARY_MAX_DIM || x.heads > (1 << 24) / x.dim ||
-        bad_stride(x.token_stride) || bad_stride(x.head_stride))
+        bad_stride(x.token_stride, tokens) || bad_stride(x.head_stride, x.heads))
         return BMMC_ERR_INVALID_ARG;
     return (uintptr_t)x.data % es ? BMMC_ERR_MISALIGNED : BMMC_OK;
 }
@@ -393,7 +527,7 @@ bmmc_status set_turns(MoveParams& p, const rotary_turns_t& r, bool device, bool 
     if ((uintptr_t)r.inv_freq % 4 || (uintptr_t)r.pair_axes % 4) return BMMC_ERR_MISALIGNED;
     if (r.positions) {
         if (r.position_bytes != 4 && r.position_bytes != 8) return BMMC_ERR_UNSUPPORTED_ELEM;
-        if (r.axes < 1 || r.axes > r.pairs || bad_stride(r.axis_stride)) return BMMC_ERR_INVALID_ARG;
+        if (r.axes < 1 || r.axes > ROTARY_MAX_AXES || bad_stride(r.axis_stride, r.axes)) return BMMC_ERR_INVALID_ARG;
         if ((uintptr_t)r.positions % r.position_bytes) return BMMC_ERR_MISALIGNED;
         p.position_bytes = (int)r.position_bytes;
         p.axes = (int)r.axes;
@@ -440,8 +574,8 @@ bmmc_status rotary(const rotary_args_t* a, void* stream) {
     const int es = dtype_bytes(type);
     if (!es) return BMMC_ERR_UNSUPPORTED_ELEM;
     if (!a->tokens) return BMMC_OK;
-    bmmc_status s = check_heads(a->x, es);
-    if (s == BMMC_OK) s = check_heads(a->out, es);
+    bmmc_status s = check_heads(a->x, a->tokens, es);
+    if (s == BMMC_OK) s = check_heads(a->out, a->tokens, es);
     if (s != BMMC_OK) return s;
     if (a->x.heads != a->out.heads || a->x.dim != a->out.dim || !a->turns.inv_freq || 2 * a->turns.pairs > a->x.dim ||
         !writable(a->out, a->tokens))
@@ -462,8 +596,10 @@ bmmc_status rotary(const rotary_args_t* a, void* stream) {
     const chk::Spans spans = spans_of({rows_of(a->x, a->tokens, es), turn_rows(a->turns, a->tokens, 0),
                                        turn_rows(a->turns, a->tokens, 1), turn_rows(a->turns, a->tokens, 2)},
                                       {rows_of(a->out, a->tokens, es)});
-    const int wb = word_bytes(es, {address_bits(a->x, es), address_bits(a->out, es), pair_bits(a->turns, es)});
-    return launch(p, dims, type, a->turns.flags & ROTARY_ADJACENT, wb, spans, static_cast<cudaStream_t>(stream));
+    const uint64_t bits = address_bits(a->x, es) | address_bits(a->out, es);
+    const int wb = word_bytes(es, {bits, pair_bits(a->turns, es)});
+    return launch(p, dims, type, a->turns.flags & ROTARY_ADJACENT, wb, word_bytes(es, {bits}), spans,
+                  static_cast<cudaStream_t>(stream));
 }
 
 bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
@@ -474,10 +610,10 @@ bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
     if (!es) return BMMC_ERR_UNSUPPORTED_ELEM;
     if (!a->tokens) return BMMC_OK;
     const bool with_q = a->q.data || a->q_out.data;
-    bmmc_status s = check_heads(a->k, es);
-    if (s == BMMC_OK) s = check_heads(a->v, es);
-    if (s == BMMC_OK && with_q) s = check_heads(a->q, es);
-    if (s == BMMC_OK && with_q) s = check_heads(a->q_out, es);
+    bmmc_status s = check_heads(a->k, a->tokens, es);
+    if (s == BMMC_OK) s = check_heads(a->v, a->tokens, es);
+    if (s == BMMC_OK && with_q) s = check_heads(a->q, a->tokens, es);
+    if (s == BMMC_OK && with_q) s = check_heads(a->q_out, a->tokens, es);
     if (s != BMMC_OK) return s;
     const int64_t turned = 2 * a->turns.pairs;
     if (a->k.heads != a->v.heads || turned > a->k.dim || (a->turns.flags & ROTARY_INVERSE)) return BMMC_ERR_INVALID_ARG;
@@ -485,7 +621,8 @@ bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
                    !writable(a->q_out, a->tokens)))
         return BMMC_ERR_INVALID_ARG;
     if (a->sequences < 0 || a->sequences > kMaxTokens || (a->sequences && !a->lengths) ||
-        (a->sequences && a->table_columns && !a->table) || a->table_columns < 0 || a->table_columns > kMaxTokens || bad_stride(a->table_stride) || a->pages < 0 || a->pages > kMaxTokens ||
+        (a->sequences && a->table_columns && !a->table) || a->table_columns < 0 || a->table_columns > kMaxTokens ||
+        bad_stride(a->table_stride, a->sequences) || a->pages < 0 || a->pages > kMaxTokens ||
         a->page_size < 1 || a->page_size > kMaxTokens || (!a->starts && a->sequences != a->tokens))
         return BMMC_ERR_INVALID_ARG;
     if ((uintptr_t)a->starts % 4 || (uintptr_t)a->lengths % 4 || (uintptr_t)a->table % 4) return BMMC_ERR_MISALIGNED;
@@ -497,7 +634,8 @@ bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
     uint64_t bits = 0;
     for (int c = 0; c < 2; ++c) {
         const paged_cache_t& m = *cache[c];
-        if ((!m.data && a->pages) || bad_stride(m.page_stride) || bad_stride(m.slot_stride) || bad_stride(m.head_stride))
+        if ((!m.data && a->pages) || bad_stride(m.page_stride, a->pages) || bad_stride(m.slot_stride, a->page_size) ||
+            bad_stride(m.head_stride, from[c]->heads))
             return BMMC_ERR_INVALID_ARG;
         if ((uintptr_t)m.data % es) return BMMC_ERR_MISALIGNED;
         const int64_t sizes[3] = {a->pages, a->page_size, from[c]->heads};
@@ -559,7 +697,8 @@ bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
                   Rows{a->table, a->sequences, a->table_stride * 4, a->table_columns * 4}},
                  {cache_rows[0], cache_rows[1], with_q ? rows_of(a->q_out, a->tokens, es) : none});
     const int wb = word_bytes(es, {bits, pair_bits(a->turns, es)});
-    return launch(p, dims, type, a->turns.flags & ROTARY_ADJACENT, wb, spans, static_cast<cudaStream_t>(stream));
+    return launch(p, dims, type, a->turns.flags & ROTARY_ADJACENT, wb, word_bytes(es, {bits}), spans,
+                  static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -14,8 +14,14 @@
 
 namespace bmmc {
 
-constexpr int64_t kMaxStride = (int64_t)1 << 40;  // elements; with the token limit, byte offsets stay below 2^63
+constexpr int64_t kMaxStride = (int64_t)1 << 40;  // elements
 constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 1;
+
+// Whether a stride is out of range, or `n` steps of it lead further than any
+// memory (so that byte offsets stay far below 2^63).
+inline bool bad_stride(int64_t stride, int64_t n) {
+    return stride < 0 || stride > kMaxStride || (n > 1 && stride > ((int64_t)1 << 50) / (n - 1));
+}
 
 // Bytes of one element; 0 for an unknown type.
 inline int dtype_bytes(int type) {
@@ -37,11 +43,12 @@ struct Rows {
 // The ranges a checked build's launch may read and write (others drop them).
 inline chk::Spans spans_of(std::initializer_list<Rows> rd, std::initializer_list<Rows> wr) {
     chk::Spans s{};
-    if (!chk::kEnabled) return s;
-    for (const Rows& r : rd)
-        if (r.base && r.rows > 0) s.rd[s.n_rd++] = chk::Span{r.lo(), r.hi()};
-    for (const Rows& r : wr)
-        if (r.base && r.rows > 0) s.wr[s.n_wr++] = chk::Span{r.lo(), r.hi()};
+    if constexpr (chk::kEnabled) {
+        for (const Rows& r : rd)
+            if (r.base && r.rows > 0) s.rd[s.n_rd++] = chk::Span{r.lo(), r.hi()};
+        for (const Rows& r : wr)
+            if (r.base && r.rows > 0) s.wr[s.n_wr++] = chk::Span{r.lo(), r.hi()};
+    }
     return s;
 }
 

@@ -536,8 +536,9 @@ bmmc_status bmmc_copy(const void *in, void *out, size_t bytes, void *stream);
  * conventions:
  *   - `type` is a bmmc_dtype; sums are held in 32 bits and every result is
  *     rounded once, to nearest even.
- *   - Strides are in elements of the array's type, >= 0 and at most 2^40; a
- *     row's elements lie next to each other.  Rows of an input may share
+ *   - Strides are in elements of the array's type, >= 0 and at most 2^40, and
+ *     an array reaches over 2^50 elements at most; a row's elements lie next to
+ *     each other.  Rows of an input may share
  *     memory (stride 0), elements of an output have addresses of their own.
  *   - Pointers are reachable by the GPU as for bmmc_permute and aligned to
  *     their element (MISALIGNED); 16-byte aligned rows are the fast case.
@@ -623,6 +624,7 @@ typedef struct {
 } token_heads_t;
 
 #define ROTARY_MAX_DIM 8192
+#define ROTARY_MAX_AXES 32
 #define ROTARY_ADJACENT 0x1  /* pair i is elements 2i, 2i+1 (else i, i + pairs) */
 #define ROTARY_INVERSE  0x2  /* turn by the opposite angles: the gradient */
 

@@ -353,6 +353,32 @@ def test_rotary(tokens, heads, dim, pairs, axes, interleaved, dtype):
             assert torch.equal(got[0], x[0])  # position 0
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("tokens,heads,dim,pairs", [
+    (1, 1, 16, 1), (3, 5, 128, 37), (6000, 3, 128, 37), (5000, 1, 24, 11), (70, 40, 64, 3), (33, 2, 512, 255), (9, 3, 520, 131),
+    (4, 2, 1024, 509), (5, 2, 1032, 3), (777, 9, 96, 25), (20000, 2, 8, 3),
+])
+def test_rotary_pairs_across_words(tokens, heads, dim, pairs, interleaved, dtype):
+    """Rows that allow wide words and pairs that do not lie in them; dense and
+    as slices, out of place, head-major and in place."""
+    g = _gen(dim + pairs)
+    fused = _randn(g, tokens, heads + 1, dim, dtype=dtype)
+    x = fused[:, 1:]
+    freq = 1000.0 ** (-torch.arange(pairs, device="cuda") / pairs)
+    at = torch.randint(-9, 4096, (2, tokens), generator=g, device="cuda")
+    axes = (torch.arange(pairs, device="cuda") % 3).int()  # one axis that is not there
+    want, size = _turn64(x, at, freq, axes, interleaved)
+    got = bm.rotary(x, at, freq, axes, interleaved=interleaved)
+    _within(got, want, TURN * size, dtype)
+    assert torch.equal(got[..., 2 * pairs:], x[..., 2 * pairs:])
+    out = torch.empty(heads, tokens, dim, dtype=dtype, device="cuda").transpose(0, 1)
+    assert torch.equal(bm.rotary(x.contiguous(), at, freq, axes, interleaved=interleaved, out=out), got)
+    keep = fused[:, 0].clone()
+    bm.rotary(x, at, freq, axes, interleaved=interleaved, out=x)
+    assert torch.equal(x, got) and torch.equal(fused[:, 0], keep)
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("dim,offset", [(64, 0), (64, 1), (36, 0), (35, 3)])
@@ -501,6 +527,23 @@ def test_append_ragged(counts, page, cached, interleaved, dtype):
     axes = (torch.arange(16, device="cuda") % 3).int()
     _check_append(c, _freq(16), positions, axes, interleaved)
     _check_append(c, _freq(16), positions.int(), axes, interleaved)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("head_major", [False, True])
+@pytest.mark.parametrize("counts,Dk,Dv,pairs", [
+    ([1], 64, 64, 5), ([1] * 130, 128, 128, 37), ([30, 0, 7], 96, 32, 25), ([4000, 0, 2100], 64, 72, 31), ([2, 1], 512, 1024, 13),
+])
+def test_append_pairs_across_words(counts, Dk, Dv, pairs, head_major, interleaved, dtype):
+    g = _gen(Dk + pairs)
+    c = _append_case(g, len(counts), counts, 16, 6, 2, Dk, Dv, dtype, head_major, 40)
+    freq = 100.0 ** (-torch.arange(pairs, device="cuda") / pairs)
+    _check_append(c, freq, interleaved=interleaved, starts=max(counts) > 1)
+    c["table"][0, 0] = -1
+    T = c["k"].shape[0]
+    positions = torch.randint(0, 4096, (2, T), generator=g, device="cuda")
+    _check_append(c, freq, positions, (torch.arange(pairs, device="cuda") % 2).int(), interleaved)
 
 
 def test_append_skips_tokens_without_a_page():

@@ -153,6 +153,22 @@ def test_append_refusals(lib, change, status):
     assert lib.paged_append(None, None) == INVALID
 
 
+def test_arrays_beyond_any_memory(lib):
+    """Strides that are fine by themselves, with so many rows that byte
+    offsets would leave 64 bits."""
+    n = 2**31 - 1
+    assert lib.expert_dispatch(P, 2**40, S, n, 1, 64, 2, Q, 64, n, None) == INVALID
+    assert lib.expert_dispatch(P, 64, S, n, 1, 64, 2, Q, 2**40, n, None) == INVALID
+    assert lib.expert_combine(P, 2**40, n, S, None, 0, n, 1, 64, 2, Q, 64, None) == INVALID
+    assert lib.expert_combine_backward(P, 2**40, P, 64, n, S, S, 0, n, 1, 64, 2, Q, 64, S, None) == INVALID
+    a = list(ROTARY)
+    a[0], a[5], a[10] = n, 2**40, 2**40
+    assert lib.rotary(_capi.ROTARY_ARGS.pack(*a), None) == INVALID
+    a = list(APPEND)
+    a[36], a[39] = n, 2**40
+    assert lib.paged_append(_capi.PAGED_APPEND_ARGS.pack(*a), None) == INVALID
+
+
 def test_nothing_to_do_is_fine(lib):
     a = list(APPEND)
     a[0] = 0
