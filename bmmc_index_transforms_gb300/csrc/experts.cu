@@ -7,6 +7,7 @@
 // inverse.  Choices that are not routed (an id outside [0, E)) are sorted
 // behind all others and marked by the complement of the number, so that the
 // map stays a permutation and every row of the sorted array has one writer.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -27,6 +28,7 @@ namespace {
 
 constexpr int kMaxExperts = 4096;
 constexpr int kSortRounds = 4;       // ids per lane and tile
+constexpr int kSortCluster = 8;      // blocks that are launched as one cluster
 constexpr int kMaxSortBlocks = 152;  // blocks of a sort that one block does not cover: one for each SM
 
 #ifdef BMMC_BOUNDS_CHECK
@@ -138,17 +140,20 @@ __device__ __forceinline__ unsigned same_key(int key, int bits) {
 // ids' first load and the barriers between a tile's steps leave 6.8 us of it
 // when all other work is skipped.  One block per SM of 32 warps was taken for
 // that reason; 64 blocks of twice the ids, which summed the blocks' counts one
-// key a load, took 18 us.  384 ids are one block and one launch: 2.6 us.
+// key a load, took 18 us.  384 ids are one block and one launch: 2.5 us; 4096 ids
+// 6.8 us (7.4 with source written where it goes), 32768 as one cluster, without a
+// second launch or a workspace, 8.8; 32800 in two launches 9.6.
 //
 // Each block numbers its part, a tile of blockDim.x * R choices at a time.
 // Inside a warp a choice's rank among equal keys comes from the lanes of a
 // round with its key plus the warp's running count of that key; a column sum
 // over the warps and the block's start for the key complete its place.  The
-// starts come from the counts of all blocks, or (counts == NULL: one block
-// and one tile) from the tile itself.  Integer sums: the result does not
+// starts come from the counts of all blocks; or (counts == NULL: one tile a
+// block) from the tile itself where there is one block, and from the tiles of
+// the blocks of one cluster, which read each other's shared memory.  Integer sums: the result does not
 // depend on timing.  The first tile is ranked before the counts are waited
-// for, so that this work runs beside the count kernel; a tile of many blocks
-// is put in order in shared memory, so that source is written in runs.
+// for, so that this work runs beside the count kernel; a tile of several
+// rounds is put in order in shared memory, so that source is written in runs.
 template <class Id, int R>
 __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__ ids, int64_t n, int experts,
                                                           int64_t per_block, int pitch, int bits, const int* counts,
@@ -157,13 +162,16 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__
     extern __shared__ int s_mem[];
     BMMC_SPANS_ENTER(s_mem, chk_dynamic_bytes());
     const int keys = experts + 1, warps = blockDim.x >> 5, none = (1 << bits) - 1;
+    const bool many = gridDim.x > 1;
+    constexpr bool kOrder = R > 1;  // a tile large enough to put source in order before it is written
     int* base = s_mem;           // [pitch] where the block's next choice of each key goes
     int* total = base + pitch;   // [pitch] choices of the tile
-    int* start = total + pitch;  // [pitch] the tile's first choice of each key, in order (counts only)
-    int* tmp = start + pitch;    // [32]
+    int* start = total + pitch;  // [pitch] the tile's first choice of each key, in order (several blocks)
+    int* ahead = start + pitch;  // [pitch] choices of the blocks before this one (a cluster)
+    int* tmp = ahead + pitch;    // [32]
     int* hist = tmp + 32;        // [warps][keys] counts of the tile, then starts inside the key
     int* order = hist + warps * keys;                                        // [blockDim.x * R] the tile in order,
-    unsigned short* order_key = reinterpret_cast<unsigned short*>(order + blockDim.x * R);  // and its keys (counts only)
+    unsigned short* order_key = reinterpret_cast<unsigned short*>(order + blockDim.x * R);  // and its keys (R > 1)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int* mine = hist + warp * keys;
     const int64_t lo = (int64_t)blockIdx.x * per_block, hi = min(n, lo + per_block);
@@ -209,11 +217,31 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__
                 run += c;
             }
             total[e] = run;
-            (counts ? start : base)[e] = run;
+            (many ? start : base)[e] = run;
+        }
+        if (many && !counts) {  // the tiles' counts, from the blocks of the cluster
+            const auto cluster = cooperative_groups::this_cluster();
+            cluster.sync();
+            for (int e = threadIdx.x; e < keys; e += blockDim.x) {
+                int all = 0, before = 0;
+                for (int b = 0; b < (int)gridDim.x; ++b) {
+                    const int c = *cluster.map_shared_rank(total + e, b);
+                    all += c;
+                    if (b < (int)blockIdx.x) before += c;
+                }
+                base[e] = all;
+                ahead[e] = before;
+            }
+            cluster.sync();  // no block leaves while its counts are read
+            block_exclusive_scan(base, keys, tmp);
+            for (int e = threadIdx.x; e < keys; e += blockDim.x) {
+                if (blockIdx.x == 0 && BMMC_WR_OK(offsets + e, 4)) offsets[e] = base[e];
+                base[e] += ahead[e];
+            }
         }
         __syncthreads();
-        block_exclusive_scan(counts ? start : base, keys, tmp);
-        if (!counts)
+        block_exclusive_scan(many ? start : base, keys, tmp);
+        if (!many)
             for (int e = threadIdx.x; e < keys; e += blockDim.x)
                 if (BMMC_WR_OK(offsets + e, 4)) offsets[e] = base[e];
 #pragma unroll
@@ -224,19 +252,19 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__
             const int to = base[key[r]] + in_key;
             const bool routed = key[r] < experts;
             if (BMMC_WR_OK(slot + i, 4)) slot[i] = routed ? to : ~to;
-            if (counts) {
-                const int j = start[key[r]] + in_key;
+            if (kOrder) {
+                const int j = (many ? start : base)[key[r]] + in_key;
                 if (BMMC_SH_OK(order + j, 4)) order[j] = in_tile;
                 if (BMMC_SH_OK(order_key + j, 2)) order_key[j] = (unsigned short)key[r];
             } else if (BMMC_WR_OK(source + to, 4)) {
                 source[to] = routed ? (int)i : ~(int)i;
             }
         }
-        if (!counts) return;
+        if (!kOrder) return;
         __syncthreads();
         const int here = (int)min((int64_t)blockDim.x * R, hi - at);
         for (int j = threadIdx.x; j < here; j += blockDim.x) {
-            const int k = order_key[j], i = (int)at + order[j], to = base[k] + j - start[k];
+            const int k = order_key[j], i = (int)at + order[j], to = many ? base[k] + j - start[k] : j;
             if ((unsigned)to < (unsigned)n && BMMC_WR_OK(source + to, 4)) source[to] = k < experts ? i : ~i;  // also if ids changed meanwhile
         }
         at += (int64_t)blockDim.x * R;
@@ -255,7 +283,8 @@ struct SortShape {
 constexpr size_t kSortSmem = 200 * 1024;
 
 // One block where one tile covers all choices (of one round a warp where that
-// is enough), else at most kMaxSortBlocks blocks of whole tiles.  A block has
+// is enough), a cluster of blocks of one tile each, else at most
+// kMaxSortBlocks blocks of whole tiles.  A block has
 // as many warps as their counts of every key leave room for.
 SortShape sort_shape(int64_t n, int experts) {
     SortShape s;
@@ -263,7 +292,7 @@ SortShape sort_shape(int64_t n, int experts) {
     s.bits = 1;  // of the keys 0 .. experts and one past them
     while ((1 << s.bits) < experts + 2) ++s.bits;
     const auto smem = [&](int warps) {
-        return ((size_t)warps * (experts + 1) + 3 * s.pitch + 32) * sizeof(int) + (size_t)warps * 32 * kSortRounds * 6;
+        return ((size_t)warps * (experts + 1) + 4 * s.pitch + 32) * sizeof(int) + (size_t)warps * 32 * kSortRounds * 6;
     };
     s.warps = 32;
     while (smem(s.warps) > kSortSmem) s.warps >>= 1;
@@ -300,30 +329,22 @@ bmmc_status launch_sort(const SortShape& s, const void* ids_, int64_t n, int exp
         }
     }
     const int* none = nullptr;
-    if (s.blocks == 1) {
-        place<<<1, s.warps * 32, s.smem, st>>>(ids, n, experts, s.per_block, s.pitch, s.bits, none, slot, source,
-                                                 offsets BMMC_SPANS_ARG(spans));
-        return launched();
+    if (s.blocks <= kSortCluster) {
+        cudaLaunchAttribute together{};
+        together.id = cudaLaunchAttributeClusterDimension;
+        together.val.clusterDim.x = s.blocks;
+        together.val.clusterDim.y = together.val.clusterDim.z = 1;
+        return launch(place, dim3(s.blocks), dim3(s.warps * 32), s.smem, st, s.blocks > 1 ? &together : nullptr, ids, n,
+                      experts, s.per_block, s.pitch, s.bits, none, slot, source, offsets BMMC_SPANS_ARG(spans));
     }
-    sort_count_kernel<Id><<<s.blocks, 1024, s.pitch * sizeof(int), st>>>(ids, n, experts, s.per_block, s.pitch,
-                                                                                counts BMMC_SPANS_ARG(spans));
-    if (launched() != BMMC_OK) return BMMC_ERR_CUDA;
-    cudaLaunchAttribute early[1];
-    early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(s.blocks);
-    cfg.blockDim = dim3(s.warps * 32);
-    cfg.dynamicSmemBytes = s.smem;
-    cfg.stream = st;
-    cfg.attrs = early;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, place, ids, n, experts, s.per_block, s.pitch, s.bits, (const int*)counts, slot, source,
-                           offsets BMMC_SPANS_ARG(spans)) != cudaSuccess) {
-        cudaGetLastError();
-        return BMMC_ERR_CUDA;
-    }
-    return BMMC_OK;
+    const bmmc_status counted = launch(sort_count_kernel<Id>, dim3(s.blocks), dim3(1024), s.pitch * sizeof(int), st, nullptr,
+                                       ids, n, experts, s.per_block, s.pitch, counts BMMC_SPANS_ARG(spans));
+    if (counted != BMMC_OK) return counted;
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    return launch(place, dim3(s.blocks), dim3(s.warps * 32), s.smem, st, &early, ids, n, experts, s.per_block, s.pitch,
+                  s.bits, (const int*)counts, slot, source, offsets BMMC_SPANS_ARG(spans));
 }
 
 // ---- dispatch ----------------------------------------------------------------
@@ -659,7 +680,7 @@ bmmc_status expert_sort_workspace(int64_t tokens, int choices, int experts, size
         experts > kMaxExperts)
         return BMMC_ERR_INVALID_ARG;
     const SortShape s = sort_shape(tokens * choices, experts);
-    *bytes = s.blocks > 1 ? (size_t)s.blocks * s.pitch * sizeof(int) : 0;
+    *bytes = s.blocks > kSortCluster ? (size_t)s.blocks * s.pitch * sizeof(int) : 0;
     return BMMC_OK;
 }
 
@@ -718,19 +739,17 @@ bmmc_status expert_dispatch(const void* x, int64_t x_stride, const int32_t* slot
     (void)spans;
     const auto copy = [&](auto word) {
         const Cover c = cover(tokens, words, most);
-        dispatch_kernel<decltype(word)><<<c.grid, c.block, 0, st>>>(from, x_stride * es, slot, tokens, choices, n_rows, words,
-                                                                    to, row_stride * es BMMC_SPANS_ARG(spans));
+        return launch(dispatch_kernel<decltype(word)>, c.grid, c.block, 0, st, nullptr, from, x_stride * es, slot, tokens,
+                      choices, n_rows, words, to, row_stride * es BMMC_SPANS_ARG(spans));
     };
     const auto across = [&](auto e) {
         const Cover c = cover(tokens, words + 1, most);  // one more: thread 0 holds no word w - 1
-        dispatch_across_kernel<decltype(e)><<<c.grid, c.block, 0, st>>>(from, x_stride * es, slot, tokens, choices, n_rows,
-                                                                        (int)hidden, to, row_stride * es BMMC_SPANS_ARG(spans));
+        return launch(dispatch_across_kernel<decltype(e)>, c.grid, c.block, 0, st, nullptr, from, x_stride * es, slot,
+                      tokens, choices, n_rows, (int)hidden, to, row_stride * es BMMC_SPANS_ARG(spans));
     };
-    if (way.bytes == 16) copy(uint4{});
-    else if (way.bytes == 8) copy(uint2{});
-    else if (es == 4) across(uint32_t{});
-    else across(uint16_t{});
-    return launched();
+    if (way.bytes == 16) return copy(uint4{});
+    if (way.bytes == 8) return copy(uint2{});
+    return es == 4 ? across(uint32_t{}) : across(uint16_t{});
 }
 
 bmmc_status expert_combine(const void* rows, int64_t row_stride, int64_t n_rows, const int32_t* slot,
@@ -767,11 +786,11 @@ bmmc_status expert_combine(const void* rows, int64_t row_stride, int64_t n_rows,
         auto kernel = combine_kernel<T, W, 2, A>;
         if constexpr (!A)
             if (choices > 2) kernel = choices <= 4 ? combine_kernel<T, W, 4, A> : combine_kernel<T, W, 8, A>;
-        kernel<<<c.grid, c.block, 0, st>>>(static_cast<const char*>(rows), row_stride * es, n_rows, slot, weights,
-                                          weight_type == BMMC_F32, tokens, choices, (int)hidden, static_cast<char*>(out),
-                                          out_stride * es BMMC_SPANS_ARG(spans));
+        s = launch(kernel, c.grid, c.block, 0, st, nullptr, static_cast<const char*>(rows), row_stride * es, n_rows, slot,
+                   weights, int(weight_type == BMMC_F32), tokens, choices, (int)hidden, static_cast<char*>(out),
+                   out_stride * es BMMC_SPANS_ARG(spans));
     });
-    return launched();
+    return s;
 }
 
 bmmc_status expert_combine_backward(const void* grad, int64_t grad_stride, const void* rows, int64_t row_stride,
@@ -819,12 +838,12 @@ bmmc_status expert_combine_backward(const void* grad, int64_t grad_stride, const
         auto kernel = combine_backward_kernel<T, W, 2, A>;
         if constexpr (!A)
             if (choices > 2) kernel = combine_backward_kernel<T, W, 4, A>;
-        kernel<<<blocks, block, 0, st>>>(static_cast<const char*>(grad), grad_stride * es, static_cast<const char*>(rows),
-                                        row_stride * es, n_rows, slot, weights, weight_type == BMMC_F32, tokens, choices,
-                                        (int)hidden, static_cast<char*>(grad_rows), grad_row_stride * es,
-                                        grad_weights BMMC_SPANS_ARG(spans));
+        s = launch(kernel, dim3(blocks), block, 0, st, nullptr, static_cast<const char*>(grad), grad_stride * es,
+                   static_cast<const char*>(rows), row_stride * es, n_rows, slot, weights, int(weight_type == BMMC_F32),
+                   tokens, choices, (int)hidden, static_cast<char*>(grad_rows), grad_row_stride * es,
+                   grad_weights BMMC_SPANS_ARG(spans));
     });
-    return launched();
+    return s;
 }
 
 }  // extern "C"

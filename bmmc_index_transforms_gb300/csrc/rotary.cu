@@ -444,9 +444,8 @@ bmmc_status launch_rows(MoveParams& p, const int (&dims)[3], bool adjacent, cons
     }
     const bool split = p.parts > 1 && p.tokens * p.parts <= 152 * 8;
     const dim3 grid((unsigned)((p.tokens + per_block - 1) / per_block), split ? p.parts : 1);
-    move_rows_kernel<T, Word><<<grid, kRowThreads, (size_t)per_block * p.pairs * sizeof(float2), st>>>(
-        p BMMC_SPANS_ARG(spans));
-    return launched();
+    return launch(move_rows_kernel<T, Word>, grid, dim3(kRowThreads), (size_t)per_block * p.pairs * sizeof(float2), st,
+                  nullptr, p BMMC_SPANS_ARG(spans));
 }
 
 template <class T, int W>
@@ -457,9 +456,8 @@ bmmc_status launch_width(MoveParams& p, const int (&dims)[3], bool adjacent, con
     const int per_block = threads >> p.group_log2;
     const dim3 grid((unsigned)((p.tokens + per_block - 1) / per_block), split ? p.parts : 1);
     const size_t smem = (size_t)per_block * p.pairs * sizeof(float2);
-    if (adjacent) move_heads_kernel<T, W, true><<<grid, threads, smem, st>>>(p BMMC_SPANS_ARG(spans));
-    else move_heads_kernel<T, W, false><<<grid, threads, smem, st>>>(p BMMC_SPANS_ARG(spans));
-    return launched();
+    const auto kernel = adjacent ? move_heads_kernel<T, W, true> : move_heads_kernel<T, W, false>;
+    return launch(kernel, grid, dim3(threads), smem, st, nullptr, p BMMC_SPANS_ARG(spans));
 }
 
 template <class T>
@@ -479,8 +477,8 @@ bmmc_status launch_type(MoveParams& p, const int (&dims)[3], bool adjacent, int 
     return launch_width<T, 1>(p, dims, adjacent, spans, st);
 }
 
-bmmc_status launch(MoveParams& p, const int (&dims)[3], int type, bool adjacent, int bytes, int row_word,
-                   const chk::Spans& spans, cudaStream_t st) {
+bmmc_status launch_moves(MoveParams& p, const int (&dims)[3], int type, bool adjacent, int bytes, int row_word,
+                         const chk::Spans& spans, cudaStream_t st) {
     switch (type) {
         case BMMC_F32: return launch_type<float>(p, dims, adjacent, bytes, row_word, spans, st);
         case BMMC_F16: return launch_type<__half>(p, dims, adjacent, bytes, row_word, spans, st);
@@ -598,8 +596,8 @@ bmmc_status rotary(const rotary_args_t* a, void* stream) {
                                       {rows_of(a->out, a->tokens, es)});
     const uint64_t bits = address_bits(a->x, es) | address_bits(a->out, es);
     const int wb = word_bytes(es, {bits, pair_bits(a->turns, es)});
-    return launch(p, dims, type, a->turns.flags & ROTARY_ADJACENT, wb, word_bytes(es, {bits}), spans,
-                  static_cast<cudaStream_t>(stream));
+    return launch_moves(p, dims, type, a->turns.flags & ROTARY_ADJACENT, wb, word_bytes(es, {bits}), spans,
+                        static_cast<cudaStream_t>(stream));
 }
 
 bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
@@ -697,8 +695,8 @@ bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
                   Rows{a->table, a->sequences, a->table_stride * 4, a->table_columns * 4}},
                  {cache_rows[0], cache_rows[1], with_q ? rows_of(a->q_out, a->tokens, es) : none});
     const int wb = word_bytes(es, {bits, pair_bits(a->turns, es)});
-    return launch(p, dims, type, a->turns.flags & ROTARY_ADJACENT, wb, word_bytes(es, {bits}), spans,
-                  static_cast<cudaStream_t>(stream));
+    return launch_moves(p, dims, type, a->turns.flags & ROTARY_ADJACENT, wb, word_bytes(es, {bits}), spans,
+                        static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -108,6 +108,20 @@ inline bmmc_status all_reachable(bool device, std::initializer_list<const void*>
     return BMMC_OK;
 }
 
-inline bmmc_status launched() { return cudaGetLastError() == cudaSuccess ? BMMC_OK : BMMC_ERR_CUDA; }
+// Launch a kernel, with one attribute or none.
+template <class... P, class... A>
+bmmc_status launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                   cudaLaunchAttribute* attribute, const A&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attribute;
+    cfg.numAttrs = attribute ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess) return BMMC_OK;
+    cudaGetLastError();
+    return BMMC_ERR_CUDA;
+}
 
 }  // namespace bmmc

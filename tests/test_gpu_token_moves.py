@@ -74,6 +74,15 @@ def test_sort(tokens, choices, experts, dtype):
     _check_sort(ids, experts)
 
 
+@pytest.mark.parametrize("tokens", [1024, 1025, 4096, 4097, 8191, 20000, 32768, 32769, 40961])
+@pytest.mark.parametrize("experts", [3, 200, 1024, 4096])
+def test_sort_around_the_sizes_of_tiles(tokens, experts):
+    g = _gen(tokens + experts)
+    ids = torch.randint(0, experts, (tokens, 1), generator=g, device="cuda")
+    ids[torch.rand(tokens, 1, generator=g, device="cuda") < 0.1] = -1
+    _check_sort(ids, experts)
+
+
 @pytest.mark.parametrize("tokens", [5, 2000, 40000])
 def test_sort_one_sided(tokens):
     """Every choice the same expert, none routed, and an expert without any."""
