@@ -694,6 +694,25 @@ def test_stream_argument():
     assert torch.equal(out, want)
 
 
+def test_sort_on_a_given_stream_keeps_its_workspace():
+    """The workspace of a sort on another stream is not handed out again
+    before that stream is done with it."""
+    g = _gen(21)
+    ids = torch.randint(0, 300, (30000, 4), generator=g, device="cuda")
+    want = [x.clone() for x in bm.expert_sort(ids, 300)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        got = bm.expert_sort(ids, 300, stream=stream)
+        for _ in range(50):  # whatever is free on the current stream is written over meanwhile
+            torch.full((40 * 304,), -7, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
 def test_no_tokens():
     """Calls without any token write nothing and give empty results."""
     slot = torch.empty(0, 4, dtype=torch.int32, device="cuda")
