@@ -27,6 +27,7 @@ constexpr int kThreads = 128;           // threads of a block, at most (one toke
 constexpr int kMostThreads = 256;
 constexpr int kMaxTokensPerBlock = 64;
 constexpr int kHeadsAtOnce = 2;         // heads whose words a thread has in flight
+constexpr int kAhead = 2;               // turns whose inputs a thread has in flight
 
 // Heads of one kind (queries, keys, values): where they lie and where they
 // go.  Strides in bytes.  place: 0 = the token's own place (dst_token apart),
@@ -48,12 +49,12 @@ struct MoveParams {
     int parts;
     int64_t tokens;
     int group_log2;  // threads of a token
-    unsigned pairs_magic;  // staged rows: 2^32 / pairs rounded up (pairs > 1)
-    bool adjacent;         // staged rows: pairs side by side
+    bool adjacent;   // staged rows: pairs side by side
     bool device;     // the heads are the device's own memory and may be fetched ahead
     // rotation
     const void* positions;  // NULL: the token's place in its sequence
     int position_bytes, axes, pairs;
+    unsigned pairs_magic;  // 2^32 / pairs rounded up (pairs > 1)
     int64_t axis_stride;
     const float* freq;
     const int* pair_axes;  // NULL: axis 0
@@ -64,6 +65,9 @@ struct MoveParams {
     int page_size;
     int64_t page_stride[2], slot_stride[2];  // of the key and the value cache, bytes
 };
+
+// x / d for x, d < 2^16, with magic = 2^32 / d rounded up.
+__device__ __forceinline__ int quotient(int x, int d, unsigned magic) { return d == 1 ? x : (int)__umulhi(x, magic); }
 
 // The last sequence whose start is <= t, -1 if there is none: by a whole
 // warp, 32 starts at a time, and by one thread.  Any starts, in order or not,
@@ -139,11 +143,10 @@ __device__ __forceinline__ void begin_block(const MoveParams& p, int64_t t0, int
     // A thread's first turns (what they need but for a position that follows
     // from the place), and all the heads (to L2), are on their way while the
     // places are worked out.
-    constexpr int kAhead = 2;
     float freq[kAhead] = {}, position[kAhead] = {};
     bool by_place[kAhead] = {};
     const auto start_turn = [&](int i, float& f, float& at, bool& from_place) {
-        const int k = i / p.pairs, pair = i - k * p.pairs;
+        const int k = quotient(i, p.pairs, p.pairs_magic), pair = i - k * p.pairs;
         const int axis = p.pair_axes && BMMC_RD_OK(p.pair_axes + pair, 4) ? p.pair_axes[pair] : 0;
         f = BMMC_RD_OK(p.freq + pair, 4) ? p.freq[pair] : 0.0f;
         at = 0.0f;  // an axis that is not there does not turn
@@ -183,7 +186,7 @@ __device__ __forceinline__ void begin_block(const MoveParams& p, int64_t t0, int
     }
     if (turning) {
         const auto end_turn = [&](int i, float f, float at, bool from_place) {
-            if (from_place) at = s_position[i / p.pairs];
+            if (from_place) at = s_position[quotient(i, p.pairs, p.pairs_magic)];
             float s, c;
             sincosf(at * f, &s, &c);
             if (BMMC_SH_OK(s_turn + i, 8)) s_turn[i] = make_float2(c, p.sign * s);
@@ -212,7 +215,7 @@ __device__ __forceinline__ void begin_block(const MoveParams& p, int64_t t0, int
 // is the start of a block, whose loads of starts, lengths and table follow one
 // another, which is why positions, frequencies and, to L2, the heads are sent
 // for first (without that 76 us).  12 heads of 96 f32 with adjacent pairs, 10007
-// tokens: 17.1 us (13.8).  Shapes tried there: one head at a time 71.5 us, four
+// tokens: 16.7 us (13.8).  Shapes tried there: one head at a time 71.5 us, four
 // 71-95; 6 blocks of 256 threads on an SM instead of 4, whose registers then spill,
 // 88; blocks of 256 threads 70.8, of 128 68.1.  256 single tokens: 4.3 us, the
 // chain lengths - table - sine - store and a launch.
@@ -305,9 +308,6 @@ constexpr int kRowThreads = 128;
 constexpr int kRowBytes = 2048;  // of a warp's rows in shared memory
 constexpr int kRowBatch = 32;    // most rows of a warp at a time
 
-// x / d for x, d < 2^16, with magic = 2^32 / d rounded up.
-__device__ __forceinline__ int quotient(int x, int d, unsigned magic) { return d == 1 ? x : (int)__umulhi(x, magic); }
-
 // The same for heads whose pairs do not lie in the words that their rows allow
 // (an odd number of pairs in halves of a 16-bit type): a warp brings some rows
 // (heads of tokens) into shared memory in words, turns their pairs there by
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kRowThreads)
 // *split: the parts go to blocks of their own, where all of these still run
 // at once.  Returns the block's threads.
 int deal_out(MoveParams& p, const int (&dims)[3], int W, int es, bool adjacent, bool* split) {
-    int64_t most = 1;
+    int64_t most = std::max(1, p.pairs / kAhead);  // (at least as many as find their turns at once)
     for (int q = 0; q < p.parts; ++q) {
         Heads& h = p.part[q];
         const int pairs = h.turned ? p.pairs : 0;
@@ -428,7 +428,6 @@ template <class T, class Word>
 bmmc_status launch_rows(MoveParams& p, const int (&dims)[3], bool adjacent, const chk::Spans& spans, cudaStream_t st) {
     (void)spans;
     p.adjacent = adjacent;
-    p.pairs_magic = p.pairs > 1 ? (unsigned)((((uint64_t)1 << 32) + p.pairs - 1) / p.pairs) : 0;
     int per_block = p.tokens >= 152 * 32 ? 4 : 1;
     while (per_block > 1 && per_block * p.pairs * sizeof(float2) > 32 * 1024) per_block >>= 1;
     p.group_log2 = per_block == 4 ? 5 : per_block == 2 ? 6 : 7;
@@ -533,6 +532,7 @@ bmmc_status set_turns(MoveParams& p, const rotary_turns_t& r, bool device, bool 
     }
     p.positions = r.positions;
     p.pairs = (int)r.pairs;
+    p.pairs_magic = r.pairs > 1 ? (unsigned)((((uint64_t)1 << 32) + r.pairs - 1) / r.pairs) : 0;
     p.freq = r.inv_freq;
     p.pair_axes = r.pair_axes;
     p.sign = r.flags & ROTARY_INVERSE ? -1.0f : 1.0f;
