@@ -347,6 +347,73 @@ bmmc_status launch_sort(const SortShape& s, const void* ids_, int64_t n, int exp
                   s.bits, (const int*)counts, slot, source, offsets BMMC_SPANS_ARG(spans));
 }
 
+// ---- rows staged in shared memory ------------------------------------------
+
+constexpr int kStagedThreads = 128;
+constexpr int kStagedChoices = 8;
+constexpr int kStagedWords = 1100;  // of a block, 17.6 KB: a dozen blocks on an SM have 200 KB in flight
+
+// Word j of the aligned words that hold a row's bytes from `start` on, copied
+// asynchronously; zero where it holds none of the row's `bytes` (or row NULL).
+__device__ __forceinline__ void stage_word(uint4* to, const char* row, int64_t start, int bytes, int j) {
+    const char* const p =
+        reinterpret_cast<const char*>((reinterpret_cast<uintptr_t>(row) + start) & ~(uintptr_t)15) + (int64_t)j * 16;
+    if (!BMMC_SH_OK(to, 16)) return;
+    if (row && p + 16 > row && p < row + bytes && BMMC_RD_WORD_OK(p, 16))
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(to)), "l"(p)
+                     : "memory");
+    else
+        *to = uint4{};
+}
+
+// The block's words are there.
+__device__ __forceinline__ void staged() {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+}
+
+// 16 bytes of a row, `start` bytes behind its start, from the staged words
+// that hold them.
+template <class T, int W>
+__device__ __forceinline__ Pack<T, W> staged_pack(const uint4* words, const char* row, int64_t start) {
+    Pack<T, W> y;
+    y.word = cut(words[0], words[1], (unsigned)(reinterpret_cast<uintptr_t>(row) + start) & 15u);
+    return y;
+}
+
+// Where a part's staged words start for rows that lie differently: the aligned
+// word 16 bytes before byte `at` of the row; part + 3 words reach over the part
+// of every row.
+__device__ __forceinline__ int64_t stage_from(int64_t at) { return at - 16; }
+
+// 16 bytes from byte `start` of a row on, out of words staged from byte `from`.
+template <class T, int W>
+__device__ __forceinline__ Pack<T, W> staged_pack_at(const uint4* words, const char* row, int64_t from, int64_t start) {
+    const int at = (int)((reinterpret_cast<uintptr_t>(row) + start) -
+                         ((reinterpret_cast<uintptr_t>(row) + from) & ~(uintptr_t)15));
+    Pack<T, W> y;
+    y.word = cut(words[at >> 4], words[(at >> 4) + 1], at & 15);
+    return y;
+}
+
+// How a row's packs are cut into parts of at most `most`, and the threads of a
+// block that walk over one, with few of them idle in the last round.
+struct Parts {
+    int count, words, threads;
+};
+
+template <class T>
+Parts parts_of(int64_t hidden, int most) {
+    constexpr int W = 16 / sizeof(T);
+    const int packs = (int)((hidden + 2 * (W - 1)) / W);
+    Parts p;
+    p.count = (packs + most - 1) / most;
+    p.words = (packs + p.count - 1) / p.count;
+    const int rounds = (p.words + kStagedThreads - 1) / kStagedThreads;
+    p.threads = ((p.words + rounds - 1) / rounds + 31) / 32 * 32;
+    return p;
+}
+
 // ---- dispatch ----------------------------------------------------------------
 
 // How the words of the tokens' rows are dealt out: blocks of x * y threads
@@ -438,6 +505,43 @@ __global__ void __launch_bounds__(256, 6) dispatch_across_kernel(const char* __r
     }
 }
 
+// The same, staged: a block brings a part of a token's row into shared memory,
+// each word once, and cuts every choice's packs there.  16384 x 2 rows of 4095
+// bf16 63.4 us (from registers 83.0, floor 60.3), of 4092 62.0 (85.6 in words of 8
+// bytes), 4096 x 8 52.4 (56.9); short rows lie idle too long: 65536 x 2 of 1025 91
+// (87), of 513 70 (53).
+template <class T>
+__global__ void __launch_bounds__(kStagedThreads)
+    dispatch_staged_kernel(const char* __restrict__ x, int64_t x_stride, const int* __restrict__ slot, int choices,
+                           int64_t n_rows, int length, int part, char* __restrict__ rows,
+                           int64_t row_stride BMMC_SPANS_PARAM) {
+    constexpr int W = 16 / sizeof(T);
+    extern __shared__ uint4 s_words[];  // [part + 3]
+    BMMC_SPANS_ENTER(s_words, chk::dyn_smem_bytes());
+    const int64_t t = blockIdx.x;
+    const char* const row_x = x + t * x_stride;
+    const int first = blockIdx.y * part;
+    const int64_t from = stage_from((int64_t)first * 16);
+    for (int j = threadIdx.x; j < part + 3; j += blockDim.x)
+        stage_word(s_words + j, row_x, from, length * (int)sizeof(T), j);
+    staged();
+    slot += t * choices;
+    for (int k = 0; k < choices; ++k) {
+        const int s = BMMC_RD_OK(slot + k, 4) ? __ldg(slot + k) : 0;
+        const int64_t row = s < 0 ? ~s : s;
+        if (row >= n_rows) continue;
+        char* const to = rows + row * row_stride;
+        const Walk<T, W, true> walk(length, to);
+        const int packs = min(part, walk.packs() - first);
+        for (int j = threadIdx.x; j < packs; j += blockDim.x) {
+            Pack<T, W> o;
+            if (s < 0) o.word = {};
+            else o = staged_pack_at<T, W>(s_words, row_x, from, (int64_t)walk.at(first + j) * (int)sizeof(T));
+            walk.store(o, to, first + j);
+        }
+    }
+}
+
 // ---- combine -----------------------------------------------------------------
 
 // A weight of the rows' type or of 32 bits.
@@ -506,6 +610,65 @@ __global__ void __launch_bounds__(256, KB > 2 ? 4 : ACROSS && sizeof(T) == 2 ? 6
     walk.store(o, to, w);
 }
 
+// The same, staged: a block brings a part of the rows of one token's choices
+// into shared memory and adds the packs there.
+//
+// What the asynchronous copies have in flight takes no registers, which rows
+// across words and few choices need.  40961 x 2 rows of 1031 f32 75.5 us, 100 % of
+// the copy rate (from registers 93.3); 16384 x 2 rows of 4095 bf16 66.8 (89), of
+// 4096 62.1 (64.3), 40960 x 2 of 1024 f32 73.0 (79.2); 8192 x 4 rows of 4095 61.7,
+// 4096 x 8 58.5 (60.7).  But 4096 x 8 rows of 4096 57 (46.1): with many choices that
+// lie in words there is enough in flight without, as there is for short rows:
+// 65536 x 2 rows of 1024 bf16 78.5 (63.4), of 701 70.8 (61.7), of 1025 92.4 (102.4).
+// Parts of 800 words, or of 1100 with two choices: 640 words 67.5 us at 16384 x 2
+// x 4095, 2200 77.4 at 4096 x 8.
+template <class T>
+__global__ void __launch_bounds__(kStagedThreads)
+    combine_staged_kernel(const char* __restrict__ rows, int64_t row_stride, int64_t n_rows,
+                          const int* __restrict__ slot, const void* __restrict__ weights, int weights_f32, int choices,
+                          int length, int part, unsigned part_magic, char* __restrict__ out,
+                          int64_t out_stride BMMC_SPANS_PARAM) {
+    constexpr int W = 16 / sizeof(T);
+    extern __shared__ uint4 s_words[];  // [choices][part + 1]
+    __shared__ const char* s_row[kStagedChoices];  // NULL: not there
+    __shared__ float s_weight[kStagedChoices];
+    BMMC_SPANS_ENTER(s_words, chk::dyn_smem_bytes(), s_row, sizeof(s_row), s_weight, sizeof(s_weight));
+    const int64_t t = blockIdx.x;
+    const int tid = threadIdx.x;
+    char* const to = out + t * out_stride;
+    const Walk<T, W, true> walk(length, to);
+    const int first = blockIdx.y * part, packs = min(part, walk.packs() - first);
+    if (packs <= 0) return;
+    if (tid < choices) {
+        const int64_t at = t * choices + tid;
+        const int s = BMMC_RD_OK(slot + at, 4) ? slot[at] : -1;
+        const float f = weights ? weight_at<T>(weights, weights_f32, at) : 1.0f;
+        const bool there = s >= 0 && s < n_rows;
+        s_row[tid] = there ? rows + s * row_stride : nullptr;
+        s_weight[tid] = there ? f : 0.0f;
+    }
+    __syncthreads();
+    const int64_t start = (int64_t)walk.at(first) * (int)sizeof(T);  // of the part in a row, bytes
+    for (int x = tid; x < choices * (part + 1); x += blockDim.x) {
+        const int k = quotient(x, part + 1, part_magic), j = x - k * (part + 1);
+        if (j <= packs) stage_word(s_words + x, s_row[k], start, length * (int)sizeof(T), j);
+    }
+    staged();
+    for (int j = tid; j < packs; j += blockDim.x) {
+        float sum[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) sum[i] = 0.0f;
+        for (int k = 0; k < choices; ++k) {
+            const Pack<T, W> y = staged_pack<T, W>(s_words + k * (part + 1) + j, s_row[k], start);
+#pragma unroll
+            for (int i = 0; i < W; ++i) sum[i] = fmaf(s_weight[k], y.get(i), sum[i]);
+        }
+        Pack<T, W> o;
+        o.set(sum);
+        walk.store(o, to, first + j);
+    }
+}
+
 // The sums of v[0..N) over groups of `lanes` lanes (a power of two), in a
 // fixed order; every lane gets all of them.
 template <int N>
@@ -525,7 +688,7 @@ __device__ __forceinline__ void sum_lanes(float (&v)[N], int lanes) {
 // an SM 336.9 us = 6780 GB/s; KB = 8 (106 registers) 405, a choice after the
 // other with a barrier each 357.  16384 x 2: KB = 2, 6 x 128 98.8 us (floor 100.5),
 // blocks of 256 with the registers they would like 131.6.  Rows that lie across
-// words are bound by their instructions: 4096 x 8 rows of 4095 142.6 us (85.4).
+// words are bound by their instructions.
 template <class T, int W, int KB, bool ACROSS>
 __global__ void __launch_bounds__(256, KB <= 2 ? 6 : 4) combine_backward_kernel(
     const char* __restrict__ grad, int64_t grad_stride, const char* __restrict__ rows, int64_t row_stride,
@@ -618,6 +781,97 @@ __global__ void __launch_bounds__(256, KB <= 2 ? 6 : 4) combine_backward_kernel(
                     if (weights_f32) static_cast<float*>(grad_weights)[at] = dot[j];
                     else static_cast<T*>(grad_weights)[at] = from_f32<T>(dot[j]);
                 }
+    }
+}
+
+// The same for rows that lie across words, staged: a block takes a token, brings
+// part after part of grad and of its choices' rows into shared memory, each word
+// once, and cuts the packs there.  40961 x 2 rows of 1031 f32 142.8 us (from
+// registers 180.3, floor 126.6), 16384 x 2 of 4095 bf16 123.8 (132.9), 65536 x 2 of
+// 1025 183 (206), 16384 x 8 of 513 108 (150), 4096 x 8 of 4095 146 (144), but
+// 65536 x 2 of 257 106 (93).  Rows in words of 8 bytes are faster from registers
+// (4096 x 8 of 4092 113, staged 142).
+template <class T>
+__global__ void __launch_bounds__(kStagedThreads)
+    combine_backward_staged_kernel(const char* __restrict__ grad, int64_t grad_stride, const char* __restrict__ rows,
+                                   int64_t row_stride, int64_t n_rows, const int* __restrict__ slot,
+                                   const void* __restrict__ weights, int weights_f32, int choices, int length, int part,
+                                   unsigned part_magic, char* __restrict__ grad_rows, int64_t grad_row_stride,
+                                   void* __restrict__ grad_weights BMMC_SPANS_PARAM) {
+    constexpr int W = 16 / sizeof(T);
+    extern __shared__ uint4 s_words[];  // [choices + 1][part + 3]: grad, then the choices' rows
+    __shared__ const char* s_row[kStagedChoices + 1];  // NULL: not there
+    __shared__ char* s_to[kStagedChoices];             // NULL: not written
+    __shared__ float s_weight[kStagedChoices];
+    __shared__ float s_dot[kStagedThreads / 32][kStagedChoices];
+    BMMC_SPANS_ENTER(s_words, chk::dyn_smem_bytes(), s_row, sizeof(s_row), s_to, sizeof(s_to), s_dot, sizeof(s_dot));
+    const int64_t t = blockIdx.x;
+    const int tid = threadIdx.x, pitch = part + 3;
+    if (tid < choices) {
+        const int64_t at = t * choices + tid;
+        const int s = BMMC_RD_OK(slot + at, 4) ? slot[at] : 0;
+        const int64_t row = s < 0 ? ~s : s;
+        const float f = weight_at<T>(weights, weights_f32, at);
+        const bool there = s >= 0 && row < n_rows;
+        s_row[tid + 1] = there ? rows + row * row_stride : nullptr;
+        s_to[tid] = row < n_rows ? grad_rows + row * grad_row_stride : nullptr;
+        s_weight[tid] = there ? f : 0.0f;
+    }
+    if (tid == 0) s_row[0] = grad + t * grad_stride;
+    float dot[kStagedChoices];
+#pragma unroll
+    for (int k = 0; k < kStagedChoices; ++k) dot[k] = 0.0f;
+    for (int first = 0; first * W < length + W - 1; first += part) {
+        __syncthreads();  // the rows are known; the last part's words are used
+        const int64_t from = stage_from((int64_t)first * 16);
+        for (int x = tid; x < (choices + 1) * pitch; x += blockDim.x) {
+            const int k = quotient(x, pitch, part_magic);
+            stage_word(s_words + x, s_row[k], from, length * (int)sizeof(T), x - k * pitch);
+        }
+        staged();
+#pragma unroll
+        for (int k = 0; k < kStagedChoices; ++k) {
+            if (k >= choices || !s_to[k]) continue;
+            char* const to = s_to[k];
+            const char* const row = s_row[k + 1];
+            const Walk<T, W, true> walk(length, to);
+            const int packs = min(part, walk.packs() - first);
+            const float f = s_weight[k];
+            for (int j = tid; j < packs; j += blockDim.x) {
+                Pack<T, W> o;
+                o.word = {};
+                if (row) {
+                    const int64_t start = (int64_t)walk.at(first + j) * (int)sizeof(T);
+                    Pack<T, W> g = staged_pack_at<T, W>(s_words, s_row[0], from, start);
+                    Pack<T, W> y = staged_pack_at<T, W>(s_words + (k + 1) * pitch, row, from, start);
+                    walk.trim(g, first + j);
+                    walk.trim(y, first + j);
+                    float v[W];
+#pragma unroll
+                    for (int i = 0; i < W; ++i) {
+                        dot[k] = fmaf(g.get(i), y.get(i), dot[k]);
+                        v[i] = f * g.get(i);
+                    }
+                    o.set(v);
+                }
+                walk.store(o, to, first + j);
+            }
+        }
+    }
+    sum_lanes(dot, 32);
+    if ((tid & 31) == 0)
+#pragma unroll
+        for (int k = 0; k < kStagedChoices; ++k) s_dot[tid >> 5][k] = dot[k];
+    __syncthreads();
+    if (tid < choices) {
+        float sum = 0.0f;
+        for (int i = 0; i < (int)blockDim.x >> 5; ++i) sum += s_dot[i][tid];
+        const int64_t at = t * choices + tid;
+        const int bytes = weights_f32 ? 4 : (int)sizeof(T);
+        (void)bytes;
+        if (!BMMC_WR_OK(static_cast<char*>(grad_weights) + at * bytes, bytes)) return;
+        if (weights_f32) static_cast<float*>(grad_weights)[at] = sum;
+        else static_cast<T*>(grad_weights)[at] = from_f32<T>(sum);
     }
 }
 
@@ -737,18 +991,26 @@ bmmc_status expert_dispatch(const void* x, int64_t x_stride, const int32_t* slot
     const int most = tokens * words <= kFewWords ? 128 : 256;
     const chk::Spans spans = spans_of({in, {slot, 1, 0, tokens * choices * 4}}, {out});
     (void)spans;
+    const bool staged = way.bytes < 16 && tokens * words > kFewWords && hidden * es >= 4096;
     const auto copy = [&](auto word) {
         const Cover c = cover(tokens, words, most);
         return launch(dispatch_kernel<decltype(word)>, c.grid, c.block, 0, st, nullptr, from, x_stride * es, slot, tokens,
                       choices, n_rows, words, to, row_stride * es BMMC_SPANS_ARG(spans));
     };
     const auto across = [&](auto e) {
+        using T = decltype(e);
+        if (staged) {
+            const Parts p = parts_of<T>(hidden, kStagedWords);
+            return launch(dispatch_staged_kernel<T>, dim3((unsigned)tokens, p.count), dim3(p.threads),
+                          (size_t)(p.words + 3) * 16, st, nullptr, from, x_stride * es, slot, choices, n_rows, (int)hidden,
+                          p.words, to, row_stride * es BMMC_SPANS_ARG(spans));
+        }
         const Cover c = cover(tokens, words + 1, most);  // one more: thread 0 holds no word w - 1
-        return launch(dispatch_across_kernel<decltype(e)>, c.grid, c.block, 0, st, nullptr, from, x_stride * es, slot,
+        return launch(dispatch_across_kernel<T>, c.grid, c.block, 0, st, nullptr, from, x_stride * es, slot,
                       tokens, choices, n_rows, (int)hidden, to, row_stride * es BMMC_SPANS_ARG(spans));
     };
     if (way.bytes == 16) return copy(uint4{});
-    if (way.bytes == 8) return copy(uint2{});
+    if (way.bytes == 8 && !staged) return copy(uint2{});
     return es == 4 ? across(uint32_t{}) : across(uint16_t{});
 }
 
@@ -783,6 +1045,16 @@ bmmc_status expert_combine(const void* rows, int64_t row_stride, int64_t n_rows,
         constexpr int W = decltype(width)::value;
         constexpr bool A = decltype(across)::value;
         const Cover c = cover(tokens, words, 128);
+        const int64_t bytes = choices * hidden * es;  // of a token's rows
+        if (choices <= kStagedChoices && tokens * words > kFewWords &&
+            (way.bytes == 16 ? choices <= 2 && bytes >= 8192 : bytes >= 4096 && (A || choices <= 4))) {
+            const Parts p = parts_of<T>(hidden, (choices <= 2 ? kStagedWords : 800) / choices);
+            s = launch(combine_staged_kernel<T>, dim3((unsigned)tokens, p.count), dim3(p.threads),
+                       (size_t)choices * (p.words + 1) * 16, st, nullptr, static_cast<const char*>(rows), row_stride * es,
+                       n_rows, slot, weights, int(weight_type == BMMC_F32), choices, (int)hidden, p.words,
+                       magic_of(p.words + 1), static_cast<char*>(out), out_stride * es BMMC_SPANS_ARG(spans));
+            return;
+        }
         auto kernel = combine_kernel<T, W, 2, A>;
         if constexpr (!A)
             if (choices > 2) kernel = choices <= 4 ? combine_kernel<T, W, 4, A> : combine_kernel<T, W, 8, A>;
@@ -835,6 +1107,15 @@ bmmc_status expert_combine_backward(const void* grad, int64_t grad_stride, const
         using T = decltype(e);
         constexpr int W = decltype(width)::value;
         constexpr bool A = decltype(across)::value;
+        if (A && choices <= kStagedChoices && tokens * words > kFewWords && hidden * es >= 1024) {
+            const Parts p = parts_of<T>(hidden, kStagedWords / (choices + 1));
+            s = launch(combine_backward_staged_kernel<T>, dim3((unsigned)tokens), dim3(p.threads),
+                       (size_t)(choices + 1) * (p.words + 3) * 16, st, nullptr, static_cast<const char*>(grad),
+                       grad_stride * es, static_cast<const char*>(rows), row_stride * es, n_rows, slot, weights,
+                       int(weight_type == BMMC_F32), choices, (int)hidden, p.words, magic_of(p.words + 3),
+                       static_cast<char*>(grad_rows), grad_row_stride * es, grad_weights BMMC_SPANS_ARG(spans));
+            return;
+        }
         auto kernel = combine_backward_kernel<T, W, 2, A>;
         if constexpr (!A)
             if (choices > 2) kernel = combine_backward_kernel<T, W, 4, A>;

@@ -66,9 +66,6 @@ struct MoveParams {
     int64_t page_stride[2], slot_stride[2];  // of the key and the value cache, bytes
 };
 
-// x / d for x, d < 2^16, with magic = 2^32 / d rounded up.
-__device__ __forceinline__ int quotient(int x, int d, unsigned magic) { return d == 1 ? x : (int)__umulhi(x, magic); }
-
 // The last sequence whose start is <= t, -1 if there is none: by a whole
 // warp, 32 starts at a time, and by one thread.  Any starts, in order or not,
 // give an index in range.
@@ -435,7 +432,7 @@ bmmc_status launch_rows(MoveParams& p, const int (&dims)[3], bool adjacent, cons
         Heads& h = p.part[q];
         const int row_bytes = dims[q] * (int)sizeof(T);
         h.words = row_bytes / (int)sizeof(Word);
-        h.words_magic = h.words > 1 ? (unsigned)((((uint64_t)1 << 32) + h.words - 1) / h.words) : 0;
+        h.words_magic = magic_of(h.words);
         // no more rows a warp than its share
         h.batch = std::min({kRowBytes / row_bytes, kRowBatch, (per_block * h.heads + 3) / 4});
         const bool dense = p.device && sizeof(Word) == 16 && (h.heads < 2 || h.src_head == (int64_t)row_bytes);
@@ -532,7 +529,7 @@ bmmc_status set_turns(MoveParams& p, const rotary_turns_t& r, bool device, bool 
     }
     p.positions = r.positions;
     p.pairs = (int)r.pairs;
-    p.pairs_magic = r.pairs > 1 ? (unsigned)((((uint64_t)1 << 32) + r.pairs - 1) / r.pairs) : 0;
+    p.pairs_magic = magic_of((int)r.pairs);
     p.freq = r.inv_freq;
     p.pair_axes = r.pair_axes;
     p.sign = r.flags & ROTARY_INVERSE ? -1.0f : 1.0f;

@@ -11,6 +11,10 @@
 
 namespace bmmc {
 
+// x / d for x, d < 2^16, with magic_of(d) = 2^32 / d rounded up.
+inline unsigned magic_of(int d) { return d > 1 ? (unsigned)((((uint64_t)1 << 32) + d - 1) / d) : 0; }
+__device__ __forceinline__ int quotient(int x, int d, unsigned magic) { return d == 1 ? x : (int)__umulhi(x, magic); }
+
 template <int BYTES> struct WordOf;
 template <> struct WordOf<16> { using type = uint4; };
 template <> struct WordOf<8> { using type = uint2; };
@@ -103,6 +107,7 @@ struct Walk {
     }
     __device__ __forceinline__ int at(int w) const { return w * W - lead; }  // first element of pack w
     __device__ __forceinline__ bool in(int w) const { return at(w) < length; }
+    __device__ __forceinline__ int packs() const { return (length + lead + W - 1) / W; }
 
     // A pack on its way: fetch starts the loads (of nothing where !want), get
     // takes the pack.

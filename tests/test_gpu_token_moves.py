@@ -181,6 +181,53 @@ def test_combine_backward(tokens, choices, hidden, weight, dtype):
         assert not grad_w[~keep].any()
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("tokens,choices,hidden,pad,shift", [
+    (700, 2, 4095, 0, 0), (700, 2, 4096, 0, 0), (700, 1, 4092, 8, 0), (1300, 3, 2050, 1, 1), (300, 8, 4093, 0, 3), (5000, 2, 1031, 2, 0),
+    (5000, 4, 516, 0, 0), (200, 2, 12345, 0, 1), (6000, 9, 515, 0, 0), (2500, 7, 1025, 3, 2),
+])
+def test_large_calls_of_rows_that_lie_anyhow(tokens, choices, hidden, pad, shift, dtype):
+    """Rows of any width, alignment and gap in calls that fill the machine,
+    some choices not routed or dropped: dispatch, combine and its gradient."""
+    g = _gen(hidden + pad)
+    slot = _routing(g, tokens, choices, 11)
+    n = tokens * choices
+
+    def spread(k, values=None):
+        base = torch.full((k * (hidden + pad) + shift + 8,), 5.0, dtype=dtype, device="cuda")
+        view = base[shift:shift + k * (hidden + pad)].view(k, hidden + pad)[:, :hidden]
+        if values is not None:
+            view.copy_(values)
+        return base, view
+
+    x, rows = _randn(g, tokens, hidden, dtype=dtype), _randn(g, n, hidden, dtype=dtype)
+    w = torch.rand(tokens, choices, generator=g, device="cuda")
+    xs, rs = spread(tokens, x)[1], spread(n, rows)[1]
+    for num_rows in (n, n - n // 3):
+        keep, row = _picked(slot, num_rows)
+        base, out = spread(num_rows)
+        bm.expert_dispatch(xs, slot, num_rows, out=out)
+        want = torch.zeros(num_rows, hidden, dtype=dtype, device="cuda")
+        want[row[keep]] = x[:, None].expand(-1, choices, -1)[keep]
+        assert torch.equal(out, want)
+        out.fill_(5.0)
+        assert bool((base == 5.0).all())
+        base, out = spread(tokens)
+        bm.expert_combine(rs[:num_rows], slot, w, out=out)
+        want, size = _combine64(rows, slot, w, num_rows)
+        _within(out, want, (choices + 1) * U32 * size, dtype)
+        out.fill_(5.0)
+        assert bool((base == 5.0).all())
+        grad_rows, grad_w = bm.expert_combine_backward(xs, rs[:num_rows], slot, w)
+        want = torch.zeros(num_rows, hidden, dtype=torch.float64, device="cuda")
+        want[row[keep]] = (w.double()[..., None] * x.double()[:, None])[keep]
+        _within(grad_rows, want, U32 * want.abs(), dtype)
+        products = torch.zeros(tokens, choices, hidden, dtype=torch.float64, device="cuda")
+        products[keep] = rows[row[keep]].double() * x.double()[:, None].expand(-1, choices, -1)[keep]
+        _within(grad_w, products.sum(2), (hidden + 1) * U32 * products.abs().sum(2), F32)
+        assert not grad_w[~keep].any()
+
+
 def test_gradients_against_differences():
     """combine is linear in the rows and in the weights, so a difference of
     two results over a step is the gradient up to rounding."""
