@@ -467,9 +467,9 @@ __global__ void __launch_bounds__(256, 8) dispatch_kernel(const char* __restrict
 // aligned words w - 1 and w, whatever row they go to: of a row that lies
 // `to` bytes behind its granule (the source `from` bytes behind its own), the
 // words w - 1 and w cover granule w - 1 where from >= to, else granule w.
-// The loads do not wait for slot.  16384 x 2 rows of 4095 bf16: 81.7 us, 74 % of
-// the copy rate (rows of 4092 in words of 8 bytes: 84.1); a form that read each
-// choice's words once slot was known took 136-181.
+// The loads do not wait for slot.  16384 x 2 rows of 4095 bf16: 81.7 us (long rows
+// are faster staged, below); a form that read each choice's words once slot was
+// known took 136-181.
 template <class T>
 __global__ void __launch_bounds__(256, 6) dispatch_across_kernel(const char* __restrict__ x, int64_t x_stride,
                                                                  const int* __restrict__ slot, int64_t tokens,
@@ -562,8 +562,8 @@ __device__ __forceinline__ float weight_at(const void* weights, int in_f32, int6
 // (floor 60.3 us) KB = 2 with 8 x 256 threads on an SM 63.5, with the registers
 // it would like 75, KB = 1 70.6; 4096 x 8 (45.2) KB = 8 with 4 x 256 46.1,
 // without a bound on its registers and blocks of 256 55.9.  Rows that lie across
-// words: two loads for one, and the cut; 4096 x 8 rows of 4095 60.7 us (74 %),
-// 40961 x 2 rows of 1031 f32 93.3 (floor 75.9).  32 tokens x 8 rows of 4096:
+// words: two loads for one, and the cut; 4096 x 8 rows of 4095 60.7 us,
+// 40961 x 2 rows of 1031 f32 93.3 (both faster staged, below).  32 tokens x 8 rows of 4096:
 // 2.3 us.
 template <class T, int W, int KB, bool ACROSS>
 __global__ void __launch_bounds__(256, KB > 2 ? 4 : ACROSS && sizeof(T) == 2 ? 6 : 8)
