@@ -7,6 +7,12 @@ that are not given are allocated.  Every element is moved by the library's
 CUDA kernels, on the current stream or the one given; nothing waits for the
 device, so the calls can be captured in a CUDA graph.
 
+``stream`` is a torch stream or a raw handle.  The tensors a call makes, its
+outputs and workspaces, are that stream's: they come from its memory and go
+back to it, so another stream that uses them waits for it first (and, as with
+any tensor of torch's, is recorded where they may be dropped meanwhile).  The
+inputs have to be ready on it and to last until its work is done.
+
 The calls of a decoding step take a few microseconds on the device, less than
 a careless binding takes on the host: a check costs no more than its
 comparison here, and what a refusal says is put together when it is raised.
@@ -17,6 +23,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _capi
+from ._streams import empty_on
 
 __all__ = ["expert_sort", "expert_dispatch", "expert_combine", "expert_combine_backward", "rotary", "paged_append"]
 
@@ -60,6 +67,11 @@ def _stream(device: int, stream, where: str, *tensors) -> int:
     if stream is None:
         return _raw_stream(device)
     return stream if isinstance(stream, int) else int(stream.cuda_stream)
+
+
+def _empty_there(stream, st: int):
+    """torch.empty for a call that was given a stream, whose handle is st."""
+    return _empty if st == _raw_stream(_current_device()) else empty_on(stream)
 
 
 def _check(status: int, where: str) -> None:
@@ -123,15 +135,14 @@ def expert_sort(experts, num_experts: int, stream=None):
             _workspaces.clear()
         need = _workspaces[T, K, num_experts] = size.value
     device = experts.device
-    slot = _empty((T, K), dtype=_int32, device=device)
-    source = _empty(T * K, dtype=_int32, device=device)
-    offsets = _empty(num_experts + 1, dtype=_int32, device=device)
+    empty = _empty if stream is None else _empty_there(stream, st)
+    slot = empty((T, K), dtype=_int32, device=device)
+    source = empty(T * K, dtype=_int32, device=device)
+    offsets = empty(num_experts + 1, dtype=_int32, device=device)
     work_ptr = None
     if need:
-        work = _empty(need // 4, dtype=_int32, device=device)
+        work = empty(need // 4, dtype=_int32, device=device)
         work_ptr = work.data_ptr()
-        if stream is not None:  # it is given back when this call returns, and stays that stream's until the work is done
-            work.record_stream(_torch.cuda.ExternalStream(st) if isinstance(stream, int) else stream)
     status = _library.expert_sort(experts.data_ptr(), width | _DEVICE, T, K, num_experts, slot.data_ptr(),
                                   source.data_ptr(), offsets.data_ptr(), work_ptr, need, st)
     if status:
@@ -158,7 +169,8 @@ def expert_dispatch(x, slot, num_rows=None, out=None, stream=None):
         _no_type(x, where, "x")
     if out is None:
         st = _stream(x.get_device(), stream, where, slot)
-        out, stride = _empty((R, H), dtype=x.dtype, device=x.device), H
+        empty = _empty if stream is None else _empty_there(stream, st)
+        out, stride = empty((R, H), dtype=x.dtype, device=x.device), H
     else:
         st = _stream(x.get_device(), stream, where, slot, out)
         stride = _output(out, R, H, x, where)
@@ -195,7 +207,8 @@ def expert_combine(rows, slot, weights=None, out=None, stream=None):
         wt, wp = _weights(weights, slot, rows, where), weights.data_ptr()
     st = _stream(rows.get_device(), stream, where, slot, weights, out)
     if out is None:
-        out, stride = _empty((T, H), dtype=rows.dtype, device=rows.device), H
+        empty = _empty if stream is None else _empty_there(stream, st)
+        out, stride = empty((T, H), dtype=rows.dtype, device=rows.device), H
     else:
         stride = _output(out, T, H, rows, where)
     status = _library.expert_combine(rows.data_ptr(), row_stride, R, slot.data_ptr(), wp, wt, T, K, H, t, out.data_ptr(),
@@ -224,8 +237,9 @@ def expert_combine_backward(grad, rows, slot, weights, stream=None):
     wt = _weights(weights, slot, rows, where)
     st = _stream(rows.get_device(), stream, where, grad, slot, weights)
     device = rows.device
-    grad_rows = _empty((R, H), dtype=rows.dtype, device=device)
-    grad_weights = _empty((T, K), dtype=weights.dtype, device=device)
+    empty = _empty if stream is None else _empty_there(stream, st)
+    grad_rows = empty((R, H), dtype=rows.dtype, device=device)
+    grad_weights = empty((T, K), dtype=weights.dtype, device=device)
     status = _library.expert_combine_backward(grad.data_ptr(), grad_stride, rows.data_ptr(), row_stride, R,
                                               slot.data_ptr(), weights.data_ptr(), wt, T, K, H, t, grad_rows.data_ptr(), H,
                                               grad_weights.data_ptr(), st)
@@ -255,11 +269,12 @@ def _alike(x, tokens: int, dtype, where: str, name: str):
     return h
 
 
-def _turned_output(x, X, out, tokens: int, where: str, name: str):
+def _turned_output(x, X, out, tokens: int, stream, st: int, where: str, name: str):
     """`out`, checked, or a new tensor; and its heads."""
     heads, dim = X[1], X[2]
     if out is None:
-        out = _empty((tokens, heads, dim), dtype=x.dtype, device=x.device)
+        empty = _empty if stream is None else _empty_there(stream, st)
+        out = empty((tokens, heads, dim), dtype=x.dtype, device=x.device)
         return out, (out.data_ptr(), heads, dim, heads * dim, dim)
     O = _alike(out, tokens, x.dtype, where, name)
     if O[1:3] != X[1:3]:
@@ -312,7 +327,7 @@ def rotary(x, positions, inv_freq, pair_axes=None, *, interleaved: bool = False,
     flags = (_capi.ROTARY_ADJACENT if interleaved else 0) | (_capi.ROTARY_INVERSE if inverse else 0)
     turns = _turns(T, positions, inv_freq, pair_axes, flags, where)
     st = _stream(x.get_device(), stream, where, positions, inv_freq, pair_axes, out)
-    out, O = _turned_output(x, X, out, T, where, "out")
+    out, O = _turned_output(x, X, out, T, stream, st, where, "out")
     status = _library.rotary(_capi.ROTARY_ARGS.pack(T, t, *X, *O, *turns), st)
     if status:
         _check(status, where)
@@ -381,7 +396,7 @@ def paged_append(k, v, k_cache, v_cache, page_table, lengths, *, starts=None, q=
     Q = O = _NO_HEADS
     if q is not None:
         Q = _alike(q, T, dtype, where, "q")
-        q_out, O = _turned_output(q, Q, q_out, T, where, "q_out")
+        q_out, O = _turned_output(q, Q, q_out, T, stream, st, where, "q_out")
     elif q_out is not None:
         _no(where, "q_out without q")
     status = _library.paged_append(_capi.PAGED_APPEND_ARGS.pack(
