@@ -19,6 +19,7 @@ from typing import Sequence
 
 from . import _capi
 from ._capi import PlanInfo, PlanOpts
+from ._streams import empty_on
 from .token_moves import (expert_combine, expert_combine_backward, expert_dispatch, expert_sort, paged_append,
                           rotary)
 
@@ -386,10 +387,13 @@ def lmad_copy_tensor(src, dst, stream=None) -> None:
 
 def contiguous(x, stream=None):
     """A new row-major tensor with the contents of the view x (the copy
-    torch's .contiguous() makes), moved by lmad_copy."""
+    torch's .contiguous() makes), moved by lmad_copy.  With a stream, the new
+    tensor is that stream's memory, and x has to be ready on it and to last
+    until its work is done."""
     import torch
 
-    out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    empty = torch.empty if stream is None or not x.is_cuda else empty_on(stream)
+    out = empty(x.shape, dtype=x.dtype, device=x.device)
     if out.numel():
         lmad_copy_tensor(x, out, stream)
     return out

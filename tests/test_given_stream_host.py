@@ -90,3 +90,13 @@ MADE = 4 + 1 + 1 + 2 + 1 + 1
 def test_new_tensors_are_the_given_streams(made, stream, owner):
     _calls(stream)
     assert made == [owner] * MADE
+
+
+@pytest.mark.parametrize("stream,owner", [(None, CURRENT), (GIVEN, GIVEN), (Handle(), GIVEN), (0, 0)])
+def test_the_copy_of_a_view_is_the_given_streams(made, monkeypatch, stream, owner):
+    given = []
+    monkeypatch.setattr(bm, "lmad_copy_tensor", lambda src, dst, st: given.append(st))
+    x = OnDevice(torch.zeros(4, 6).t())
+    x.is_cuda = True
+    assert bm.contiguous(x, stream).shape == (6, 4)
+    assert made == [owner] and given == [stream]

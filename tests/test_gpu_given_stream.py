@@ -33,6 +33,7 @@ CALLS = {
     "rotary": lambda s, st: [bm.rotary(s["heads"], s["at"], s["freq"], stream=st)],
     "append": lambda s, st: [bm.paged_append(s["heads"], s["heads"], *s["caches"], s["table"], s["zero"], q=s["heads"],
                                              inv_freq=s["freq"], stream=st)],
+    "contiguous": lambda s, st: [bm.contiguous(s["x"].t(), st)],
 }
 
 
