@@ -513,7 +513,7 @@ uint64_t address_bits(const token_heads_t& x, int es) {
 }
 
 // The rotation's arguments, checked and put into p.
-bmmc_status set_turns(MoveParams& p, const rotary_turns_t& r, bool device, bool need_positions) {
+bmmc_status set_turns(MoveParams& p, const rotary_turns_t& r, bool need_positions) {
     p.pairs = 0;
     if (r.flags & ~(int64_t)(ROTARY_ADJACENT | ROTARY_INVERSE)) return BMMC_ERR_INVALID_ARG;
     if (!r.inv_freq) return r.pairs || r.positions || r.pair_axes ? BMMC_ERR_INVALID_ARG : BMMC_OK;
@@ -533,7 +533,7 @@ bmmc_status set_turns(MoveParams& p, const rotary_turns_t& r, bool device, bool 
     p.freq = r.inv_freq;
     p.pair_axes = r.pair_axes;
     p.sign = r.flags & ROTARY_INVERSE ? -1.0f : 1.0f;
-    return all_reachable(device, {r.inv_freq, r.pair_axes, r.positions});
+    return BMMC_OK;
 }
 
 // What the turns read.
@@ -541,6 +541,13 @@ Rows turn_rows(const rotary_turns_t& r, int64_t tokens, int what) {
     if (what == 0) return Rows{r.inv_freq, 1, 0, r.pairs * 4};
     if (what == 1) return Rows{r.pair_axes, 1, 0, r.pairs * 4};
     return Rows{r.positions, r.axes, r.axis_stride * r.position_bytes, tokens * r.position_bytes};
+}
+
+// Whether an output may share bytes with what the turns read.
+bool meets_turns(const Rows& out, const rotary_turns_t& r, int64_t tokens) {
+    for (int what = 0; what < 3; ++what)
+        if (may_overlap(turn_rows(r, tokens, what), out)) return true;
+    return false;
 }
 
 // The bits that a word's size has to divide on account of the pairs.
@@ -578,8 +585,11 @@ bmmc_status rotary(const rotary_args_t* a, void* stream) {
     if (!same_place(a->x, a->out, a->tokens) && may_overlap(rows_of(a->x, a->tokens, es), rows_of(a->out, a->tokens, es)))
         return BMMC_ERR_ALIAS;
     MoveParams p{};
-    if ((s = set_turns(p, a->turns, device, true)) != BMMC_OK) return s;
-    if ((s = all_reachable(device, {a->x.data, a->out.data})) != BMMC_OK) return s;
+    if ((s = set_turns(p, a->turns, true)) != BMMC_OK) return s;
+    if (meets_turns(rows_of(a->out, a->tokens, es), a->turns, a->tokens)) return BMMC_ERR_ALIAS;
+    if ((s = all_reachable(device, {a->x.data, a->out.data, a->turns.inv_freq, a->turns.pair_axes, a->turns.positions})) !=
+        BMMC_OK)
+        return s;
     p.device = device;
     p.parts = 1;
     p.part[0] = heads_of(a->x, es, 1);
@@ -654,9 +664,18 @@ bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
             (!same_place(a->q, a->q_out, a->tokens) && may_overlap(q, to)))
             return BMMC_ERR_ALIAS;
     }
-    if ((s = set_turns(p, a->turns, device, false)) != BMMC_OK) return s;
+    if ((s = set_turns(p, a->turns, false)) != BMMC_OK) return s;
+    const Rows none{nullptr, 0, 0, 0};
+    const Rows written[3] = {cache_rows[0], cache_rows[1], with_q ? rows_of(a->q_out, a->tokens, es) : none};
+    const Rows maps[3] = {Rows{a->starts, 1, 0, (a->sequences + 1) * 4}, Rows{a->lengths, 1, 0, a->sequences * 4},
+                          Rows{a->table, a->sequences, a->table_stride * 4, a->table_columns * 4}};
+    for (const Rows& w : written) {
+        if (meets_turns(w, a->turns, a->tokens)) return BMMC_ERR_ALIAS;
+        for (const Rows& m : maps)
+            if (may_overlap(m, w)) return BMMC_ERR_ALIAS;
+    }
     if ((s = all_reachable(device, {a->k.data, a->v.data, a->q.data, a->q_out.data, a->k_cache.data, a->v_cache.data, a->starts,
-                            a->lengths, a->table})) != BMMC_OK)
+                            a->lengths, a->table, a->turns.inv_freq, a->turns.pair_axes, a->turns.positions})) != BMMC_OK)
         return s;
     for (int c = 0; c < 2; ++c) {
         Heads& h = p.part[p.parts++];
@@ -684,13 +703,10 @@ bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
     p.pages = a->pages;
     p.page_size = (int)a->page_size;
     const int dims[3] = {(int)a->k.dim, (int)a->v.dim, (int)a->q.dim};
-    const Rows none{nullptr, 0, 0, 0};
     const chk::Spans spans =
         spans_of({k, v, with_q ? rows_of(a->q, a->tokens, es) : none, turn_rows(a->turns, a->tokens, 0),
-                  turn_rows(a->turns, a->tokens, 1), turn_rows(a->turns, a->tokens, 2),
-                  Rows{a->starts, 1, 0, (a->sequences + 1) * 4}, Rows{a->lengths, 1, 0, a->sequences * 4},
-                  Rows{a->table, a->sequences, a->table_stride * 4, a->table_columns * 4}},
-                 {cache_rows[0], cache_rows[1], with_q ? rows_of(a->q_out, a->tokens, es) : none});
+                  turn_rows(a->turns, a->tokens, 1), turn_rows(a->turns, a->tokens, 2), maps[0], maps[1], maps[2]},
+                 {written[0], written[1], written[2]});
     const int wb = word_bytes(es, {bits, pair_bits(a->turns, es)});
     return launch_moves(p, dims, type, a->turns.flags & ROTARY_ADJACENT, wb, word_bytes(es, {bits}), spans,
                         static_cast<cudaStream_t>(stream));
