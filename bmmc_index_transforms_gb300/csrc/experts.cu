@@ -422,11 +422,15 @@ struct Cover {
     dim3 grid, block;
 };
 
+constexpr int kMostParts = 65535;
+
 // Up to this many words (one for every thread of the machine) the blocks are
 // smaller, so that more of the machine takes part.
 constexpr int64_t kFewWords = 152 * 2048;
 
 Cover cover(int64_t tokens, int words, int most) {
+    // a grid has 65535 parts at most: rows of 2^24 elements are up to 2^23 words
+    while ((words + most - 1) / most > kMostParts) most <<= 1;
     const int parts = (words + most - 1) / most, need = (words + parts - 1) / parts;
     int x = 4;
     while (x < 32 && x < need) x <<= 1;

@@ -540,6 +540,7 @@ bmmc_status bmmc_copy(const void *in, void *out, size_t bytes, void *stream);
  *     an array reaches over 2^50 elements at most; a row's elements lie next to
  *     each other.  Rows of an input may share
  *     memory (stride 0), elements of an output have addresses of their own.
+ *   - A row has 2^24 elements at most (hidden; heads * dim for heads).
  *   - Pointers are reachable by the GPU as for bmmc_permute and aligned to
  *     their element (MISALIGNED); 16-byte aligned rows are the fast case.
  *   - What a map says is checked where it is used: an index outside its array
@@ -649,7 +650,7 @@ typedef struct {
     rotary_turns_t turns;
 } rotary_args_t;
 
-/* out = x turned by its tokens' positions.  heads * dim <= 2^24. */
+/* out = x turned by its tokens' positions. */
 bmmc_status rotary(const rotary_args_t *args, void *stream);
 
 /* A cache of keys or values in pages: element d of head h of the entry `slot`

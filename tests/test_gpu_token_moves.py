@@ -828,3 +828,35 @@ def test_tensors_elsewhere_are_refused():
     cache, table = torch.zeros(5, 4, 2, 8, device="cuda"), torch.zeros(3, 2, dtype=torch.int32, device="cuda")
     with pytest.raises(ValueError, match="without q"):
         bm.paged_append(h, h, cache, cache.clone(), table, at, q_out=h.clone())
+
+
+@pytest.mark.parametrize("choices", [2, 5, 8, 9])
+@pytest.mark.parametrize("shift", [0, 1, 2])
+def test_widest_rows(shift, choices):
+    """The largest hidden of 32 bits, in words of 16 and 8 bytes and across
+    words: every form's grid holds it."""
+    g = _gen(shift)
+    T, H = 2, 1 << 24
+    n = T * choices
+    slot = torch.randperm(n, generator=g, device="cuda").int().view(T, choices)
+    base = torch.randint(-8, 9, (n * H + 4,), generator=g, device="cuda", dtype=torch.int8).float()
+    rows = base[shift:shift + n * H].view(n, H)
+    w = torch.randint(1, 4, (T, choices), generator=g, device="cuda").float()
+    want = torch.zeros(T, H, device="cuda")  # whole numbers: exact in 32 bits in any order
+    for k in range(choices):
+        want += w[:, k, None] * rows[slot[:, k].long()]
+    assert torch.equal(bm.expert_combine(rows, slot, w), want)
+    got = bm.expert_dispatch(rows[:T], slot)
+    for k in range(choices):
+        assert torch.equal(got[slot[:, k].long()], rows[:T])
+    del got
+    grad = base[shift:shift + T * H].view(T, H).sign()
+    grad_rows, grad_w = bm.expert_combine_backward(grad, rows, slot, w)
+    for k in range(choices):
+        row = slot[:, k].long()
+        assert torch.equal(grad_rows[row], w[:, k, None] * grad)
+        # sums of whole numbers below 2**24 * 8, some of them rounded on the way
+        exact = (rows[row].double() * grad.double()).sum(1)
+        size = (rows[row].double() * grad.double()).abs().sum(1)
+        # a thread adds its 2**24 / 128 products, 32 lanes and 4 warps follow
+        _within(grad_w[:, k], exact, (2 ** 17 + 40) * U32 * size, F32)
