@@ -507,6 +507,17 @@ bool writable(const token_heads_t& x, int64_t tokens) {
     return one_to_one(x.dim, sizes, strides);
 }
 
+// Whether key and value cache lie between each other: by page, entry or head.
+bool caches_between(const paged_append_args_t& a, int es) {
+    const paged_cache_t &k = a.k_cache, &v = a.v_cache;
+    const int64_t sizes[3] = {a.pages, a.page_size, a.k.heads};
+    const int64_t strides[3] = {k.page_stride * es, k.slot_stride * es, k.head_stride * es};
+    const int64_t others[3] = {v.page_stride * es, v.slot_stride * es, v.head_stride * es};
+    for (int i = 0; i < 3; ++i)
+        if (sizes[i] > 1 && strides[i] != others[i]) return false;
+    return lie_between(a.k.dim * es, a.v.dim * es, sizes, strides, (int64_t)((uintptr_t)v.data - (uintptr_t)k.data));
+}
+
 uint64_t address_bits(const token_heads_t& x, int es) {
     return (uint64_t)(uintptr_t)x.data | (uint64_t)(x.token_stride * es) | (uint64_t)(x.head_stride * es) |
            (uint64_t)(x.dim * es);
@@ -654,7 +665,7 @@ bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
                 (uint64_t)(m.head_stride * es);
     }
     const Rows k = rows_of(a->k, a->tokens, es), v = rows_of(a->v, a->tokens, es);
-    if (may_overlap(cache_rows[0], cache_rows[1])) return BMMC_ERR_ALIAS;
+    if (may_overlap(cache_rows[0], cache_rows[1]) && !caches_between(*a, es)) return BMMC_ERR_ALIAS;
     for (const Rows& c : cache_rows)
         if (may_overlap(c, k) || may_overlap(c, v)) return BMMC_ERR_ALIAS;
     if (with_q) {

@@ -65,6 +65,43 @@ inline bool may_overlap(const Rows& a, const Rows& b) {
     return !(d >= a.span && d + b.span <= s);
 }
 
+// Whether two arrays of the same sizes and strides, b `distance` behind a, share
+// no address though their ranges meet.  The elements of each have addresses of
+// their own, so its dimensions nest.  From the slowest one inwards: rows that
+// lie in each other's gaps do not meet; where both rows of one number lie
+// within the stride, only those can meet, and their insides decide.  In bytes;
+// runs are the innermost, dense dimension.
+template <int N>
+bool lie_between(int64_t run_a, int64_t run_b, const int64_t (&sizes)[N], const int64_t (&strides)[N], int64_t distance) {
+    int order[N];
+    for (int i = 0; i < N; ++i) order[i] = i;
+    std::sort(order, order + N, [&](int x, int y) { return strides[x] > strides[y]; });
+    for (int k = 0; k < N; ++k) {
+        const int64_t s = strides[k], d = s ? (distance % s + s) % s : 0;
+        if (sizes[k] < 2) continue;
+        __int128 rest = 0;
+        for (int j = 0; j < N; ++j)
+            if (sizes[j] > 1 && strides[j] % s) rest += (__int128)(sizes[j] - 1) * strides[j];
+        if (d >= run_a + rest && d + run_b + rest <= s) return true;
+    }
+    for (int k = 0; k < N; ++k) {
+        const int64_t s = strides[order[k]];
+        if (sizes[order[k]] < 2) continue;
+        __int128 rest = 0;
+        for (int j = k + 1; j < N; ++j)
+            if (sizes[order[j]] > 1) rest += (__int128)(sizes[order[j]] - 1) * strides[order[j]];
+        const int64_t d = (distance % s + s) % s;  // from a row of a to the row of b that starts behind it
+        if (d >= run_a + rest) {
+            if (d + run_b + rest <= s) return true;
+            distance = d - s;
+        } else {
+            if (d + run_b + rest > s) return false;
+            distance = d;
+        }
+    }
+    return distance >= run_a || distance + run_b <= 0;
+}
+
 // Whether the elements of an array with these sizes and strides (elements;
 // the innermost dimension has unit stride) have addresses of their own.
 template <int N>

@@ -553,7 +553,9 @@ bmmc_status bmmc_copy(const void *in, void *out, size_t bytes, void *stream);
  * Errors of all of them: INVALID_ARG (a null pointer, a size or stride out of
  * range, an unknown flag), UNSUPPORTED_ELEM (an unknown type), MISALIGNED,
  * ALIAS (an output may share bytes with an input or another output; slices
- * of one array with a common row stride are told apart), CUDA. */
+ * of one array with a common row stride are told apart, and two caches with
+ * the same strides also where they lie between each other by entry or head),
+ * CUDA. */
 typedef enum {
     BMMC_F32 = 0,
     BMMC_F16 = 1,

@@ -860,3 +860,29 @@ def test_widest_rows(shift, choices):
         size = (rows[row].double() * grad.double()).abs().sum(1)
         # a thread adds its 2**24 / 128 products, 32 lanes and 4 warps follow
         _within(grad_w[:, k], exact, (2 ** 17 + 40) * U32 * size, F32)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("counts", [[1] * 70, [0, 130, 7, 40]])
+@pytest.mark.parametrize("between", ["pages", "entries", "heads", "elements"])
+@pytest.mark.parametrize("head_major", [False, True])
+def test_append_to_caches_that_lie_between_each_other(head_major, between, counts, dtype):
+    """Keys and values in one allocation, page by page, entry by entry, head
+    by head or side by side in a head's row."""
+    g = _gen(len(counts))
+    for Dk, Dv in ((64, 64), (64, 40), (66, 33)):
+        if Dk != Dv and between != "elements":
+            continue
+        c = _append_case(g, len(counts), counts, 16, 4, 2, Dk, Dv, dtype, head_major, 50)
+        pages, a, b, _ = c["caches"][0].shape  # a, b: entries and heads, or heads and entries
+        if between == "elements":
+            one = torch.full((pages, a, b, Dk + Dv), 3.0, dtype=dtype, device="cuda")
+            c["caches"] = [one[..., :Dk], one[..., Dk:]]
+        else:
+            axis = {"pages": 1, "entries": 3 if head_major else 2, "heads": 2 if head_major else 3}[between]
+            shape = [pages, a, b, Dk]
+            shape.insert(axis, 2)
+            one = torch.full(shape, 3.0, dtype=dtype, device="cuda")
+            c["caches"] = [one.select(axis, 0), one.select(axis, 1)]
+        _check_append(c, _freq(16), starts=max(counts) > 1)
+        _check_append(c, _freq(32), interleaved=True)
