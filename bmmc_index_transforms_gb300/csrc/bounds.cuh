@@ -12,7 +12,9 @@
 //   - a shared-memory access must lie inside one of the shared arrays the
 //     kernel registered on entry;
 //   - kernels with several sources and destinations (the token moves) pass
-//     the byte ranges of each in place of the two.
+//     the byte ranges of each in place of the two, and reach their shared
+//     arrays through views (Slots in token_words.cuh) that test each index
+//     against the array's own length, or its part's, too.
 // An access that fails is skipped (a load yields zero), and the failure is
 // counted in a device record of this translation unit: the number of
 // failures and, for the first one, the site (file tag * 100000 + source
@@ -63,10 +65,10 @@ constexpr bool kEnabled = true;
 // One record per translation unit (each .cu file is compiled on its own).
 static __device__ unsigned long long g_record[kRecordWords];
 
-// The launch's buffers and up to four shared arrays, written by every
+// The launch's buffers and up to six shared arrays, written by every
 // thread on entry (all with the same values, each thread reading back its
 // own write, so no barrier is needed).
-constexpr int kMaxShared = 4;
+constexpr int kMaxShared = 6;
 struct Entry {
     Bounds b;
     uint32_t sh_lo[kMaxShared], sh_hi[kMaxShared];
@@ -88,10 +90,12 @@ __device__ __forceinline__ uint32_t sh_off(const void* p) { return (uint32_t)__c
 
 __device__ __forceinline__ void enter(const Bounds& b, const void* s0 = nullptr, uint32_t n0 = 0,
                                       const void* s1 = nullptr, uint32_t n1 = 0, const void* s2 = nullptr,
-                                      uint32_t n2 = 0, const void* s3 = nullptr, uint32_t n3 = 0) {
+                                      uint32_t n2 = 0, const void* s3 = nullptr, uint32_t n3 = 0,
+                                      const void* s4 = nullptr, uint32_t n4 = 0, const void* s5 = nullptr,
+                                      uint32_t n5 = 0) {
     s_entry.b = b;
-    const void* s[kMaxShared] = {s0, s1, s2, s3};
-    const uint32_t n[kMaxShared] = {n0, n1, n2, n3};
+    const void* s[kMaxShared] = {s0, s1, s2, s3, s4, s5};
+    const uint32_t n[kMaxShared] = {n0, n1, n2, n3, n4, n5};
 #pragma unroll
     for (int i = 0; i < kMaxShared; ++i) {
         s_entry.sh_lo[i] = s[i] ? sh_off(s[i]) : 0u;
@@ -130,14 +134,25 @@ __device__ __forceinline__ bool sh_ok(const void* p, unsigned bytes, int site) {
     return false;
 }
 
+// Elements i .. i + count - 1 of a shared array of n elements.
+static __device__ __noinline__ bool slot_ok(const void* array, int i, int count, int n, unsigned bytes, int site) {
+    if (count == 0) return true;
+    if (i >= 0 && count > 0 && i <= n - count)
+        return sh_ok(static_cast<const char*>(array) + (int64_t)i * bytes, count * bytes, site);
+    fail(site, sh_off(array) + i * bytes, sh_off(array), sh_off(array) + n * bytes, bytes);
+    return false;
+}
+
 // The same for a launch that was given spans.
 static __shared__ Spans s_spans;
 
 __device__ __forceinline__ void enter_spans(const Spans& b, const void* s0 = nullptr, uint32_t n0 = 0,
                                             const void* s1 = nullptr, uint32_t n1 = 0, const void* s2 = nullptr,
-                                            uint32_t n2 = 0, const void* s3 = nullptr, uint32_t n3 = 0) {
+                                            uint32_t n2 = 0, const void* s3 = nullptr, uint32_t n3 = 0,
+                                            const void* s4 = nullptr, uint32_t n4 = 0, const void* s5 = nullptr,
+                                            uint32_t n5 = 0) {
     s_spans = b;
-    enter(Bounds{}, s0, n0, s1, n1, s2, n2, s3, n3);
+    enter(Bounds{}, s0, n0, s1, n1, s2, n2, s3, n3, s4, n4, s5, n5);
 }
 
 __device__ __forceinline__ bool inside_one(const void* p, unsigned bytes, const Span* s, int n, int site) {

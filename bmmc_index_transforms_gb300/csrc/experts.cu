@@ -42,30 +42,30 @@ __device__ __forceinline__ int key_of(Id id, int experts) {
 
 // Exclusive prefix sum of v[0..n) in shared memory, in place, by all threads
 // of the block.  tmp: 32 ints.
-__device__ void block_exclusive_scan(int* v, int n, int* tmp) {
+__device__ void block_exclusive_scan(Slots<int> v, int n, Slots<int> tmp) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     int carry = 0;
     for (int at = 0; at < n; at += blockDim.x) {
         const int i = at + threadIdx.x;
-        const int x = i < n ? v[i] : 0;
+        const int x = i < n ? v.get(i) : 0;
         int s = x;
         for (int d = 1; d < 32; d <<= 1) {
             const int y = __shfl_up_sync(~0u, s, d);
             if (lane >= d) s += y;
         }
-        if (lane == 31) tmp[warp] = s;
+        if (lane == 31) tmp.set(warp, s);
         __syncthreads();
         if (warp == 0) {
-            int w = lane < warps ? tmp[lane] : 0;
+            int w = lane < warps ? tmp.get(lane) : 0;
             for (int d = 1; d < 32; d <<= 1) {
                 const int y = __shfl_up_sync(~0u, w, d);
                 if (lane >= d) w += y;
             }
-            tmp[lane] = w;
+            tmp.set(lane, w);
         }
         __syncthreads();
-        if (i < n) v[i] = carry + (warp ? tmp[warp - 1] : 0) + s - x;
-        carry += tmp[31];
+        if (i < n) v.set(i, carry + (warp ? tmp.get(warp - 1) : 0) + s - x);
+        carry += tmp.get(31);
         __syncthreads();
     }
 }
@@ -78,8 +78,9 @@ __global__ void __launch_bounds__(1024) sort_count_kernel(const Id* __restrict__
                                                               BMMC_SPANS_PARAM) {
     extern __shared__ int s_hist[];
     BMMC_SPANS_ENTER(s_hist, chk_dynamic_bytes());
+    const Slots<int> hist(s_hist, pitch);
     cudaTriggerProgrammaticLaunchCompletion();  // the place kernel may rank its first tile meanwhile
-    for (int e = threadIdx.x; e < pitch; e += blockDim.x) s_hist[e] = 0;
+    for (int e = threadIdx.x; e < pitch; e += blockDim.x) hist.set(e, 0);
     __syncthreads();
     const int64_t lo = (int64_t)blockIdx.x * per_block, hi = min(n, lo + per_block);
     for (int64_t at = lo + threadIdx.x; at < hi; at += (int64_t)blockDim.x * kSortRounds) {
@@ -91,17 +92,17 @@ __global__ void __launch_bounds__(1024) sort_count_kernel(const Id* __restrict__
         }
 #pragma unroll
         for (int r = 0; r < kSortRounds; ++r)
-            if (key[r] >= 0 && BMMC_SH_OK(s_hist + key[r], 4)) atomicAdd(&s_hist[key[r]], 1);
+            if (key[r] >= 0) hist.add(key[r], 1);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < pitch; e += blockDim.x)
-        if (BMMC_WR_OK(counts + (int64_t)blockIdx.x * pitch + e, 4)) counts[(int64_t)blockIdx.x * pitch + e] = s_hist[e];
+        if (BMMC_WR_OK(counts + (int64_t)blockIdx.x * pitch + e, 4)) counts[(int64_t)blockIdx.x * pitch + e] = hist.get(e);
 }
 
 // base[e] += the counts of key e over all blocks, before[e] += those over the
 // blocks ahead of this one (both zero in shared memory at the start): four
 // keys a load, the blocks dealt out to groups of threads.
-__device__ __forceinline__ void sum_counts(const int* counts, int pitch, int* base, int* before) {
+__device__ __forceinline__ void sum_counts(const int* counts, int pitch, Slots<int> base, Slots<int> before) {
     const int quads = pitch >> 2, groups = max(1, (int)blockDim.x / quads);
     for (int item = threadIdx.x; item < groups * quads; item += blockDim.x) {
         const int q = item % quads, group = item / quads;
@@ -116,8 +117,8 @@ __device__ __forceinline__ void sum_counts(const int* counts, int pitch, int* ba
         const int a4[4] = {all.x, all.y, all.z, all.w}, b4[4] = {ahead.x, ahead.y, ahead.z, ahead.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            atomicAdd(&base[4 * q + i], a4[i]);
-            atomicAdd(&before[4 * q + i], b4[i]);
+            base.add(4 * q + i, a4[i]);
+            before.add(4 * q + i, b4[i]);
         }
     }
 }
@@ -164,17 +165,20 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__
     const int keys = experts + 1, warps = blockDim.x >> 5, none = (1 << bits) - 1;
     const bool many = gridDim.x > 1;
     constexpr bool kOrder = R > 1;  // a tile large enough to put source in order before it is written
-    int* base = s_mem;           // [pitch] where the block's next choice of each key goes
-    int* total = base + pitch;   // [pitch] choices of the tile
-    int* start = total + pitch;  // [pitch] the tile's first choice of each key, in order (several blocks)
-    int* ahead = start + pitch;  // [pitch] choices of the blocks before this one (a cluster)
-    int* tmp = ahead + pitch;    // [32]
-    int* hist = tmp + 32;        // [warps][keys] counts of the tile, then starts inside the key
-    int* order = hist + warps * keys;                                        // [blockDim.x * R] the tile in order,
-    unsigned short* order_key = reinterpret_cast<unsigned short*>(order + blockDim.x * R);  // and its keys (R > 1)
+    const int tile = blockDim.x * R;
+    const Slots<int> mem(s_mem, 4 * pitch + 32 + warps * keys + (kOrder ? tile : 0));
+    const Slots<int> base = mem.part(0, pitch);           // where the block's next choice of each key goes
+    const Slots<int> total = mem.part(pitch, pitch);      // choices of the tile
+    const Slots<int> start = mem.part(2 * pitch, pitch);  // the tile's first choice of each key, in order (several blocks)
+    const Slots<int> ahead = mem.part(3 * pitch, pitch);  // choices of the blocks before this one (a cluster)
+    const Slots<int> tmp = mem.part(4 * pitch, 32);
+    const Slots<int> hist = mem.part(4 * pitch + 32, warps * keys);  // [warps][keys] counts of the tile, then starts inside the key
+    const Slots<int> order = mem.part(4 * pitch + 32 + warps * keys, kOrder ? tile : 0);  // the tile in order,
+    const Slots<unsigned short> order_key(reinterpret_cast<unsigned short*>(order.p + tile), kOrder ? tile : 0);  // and its keys
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int* mine = hist + warp * keys;
+    const Slots<int> mine = hist.part(warp * keys, keys);
     const int64_t lo = (int64_t)blockIdx.x * per_block, hi = min(n, lo + per_block);
+    const Slots<int> first = many ? start : base;
     int64_t at = lo;
     do {
         int key[R], rank[R];
@@ -183,28 +187,29 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__
             const int64_t i = at + ((int64_t)warp * R + r) * 32 + lane;
             key[r] = i < hi && BMMC_RD_OK(ids + i, sizeof(Id)) ? key_of(ids[i], experts) : none;  // none: a key past all others
         }
-        for (int e = lane; e < keys; e += 32) mine[e] = 0;
+        for (int e = lane; e < keys; e += 32) mine.set(e, 0);
         __syncwarp();
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const unsigned same = same_key(key[r], bits);
-            const bool there = key[r] < keys && BMMC_SH_OK(mine + key[r], 4);
-            const int before = there ? mine[key[r]] : 0;
+            const bool there = key[r] < keys;
+            const int before = there ? mine.get(key[r]) : 0;
             rank[r] = before + __popc(same & ((1u << lane) - 1));
             __syncwarp();
-            if (there && lane == __ffs(same) - 1) mine[key[r]] = before + __popc(same);
+            if (there && lane == __ffs(same) - 1) mine.set(key[r], before + __popc(same));
             __syncwarp();
         }
         if (counts && at == lo) {
-            for (int e = threadIdx.x; e < pitch; e += blockDim.x) base[e] = total[e] = 0;
+            for (int e = threadIdx.x; e < pitch; e += blockDim.x) base.set(e, 0), total.set(e, 0);
             __syncthreads();
             cudaGridDependencySynchronize();
             sum_counts(counts, pitch, base, total);
             __syncthreads();
             block_exclusive_scan(base, keys, tmp);
             for (int e = threadIdx.x; e < keys; e += blockDim.x) {
-                if (blockIdx.x == 0 && BMMC_WR_OK(offsets + e, 4)) offsets[e] = base[e];
-                base[e] += total[e];
+                const int from = base.get(e);
+                if (blockIdx.x == 0 && BMMC_WR_OK(offsets + e, 4)) offsets[e] = from;
+                base.set(e, from + total.get(e));
             }
         }
         __syncthreads();
@@ -212,12 +217,12 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__
             int run = 0;
 #pragma unroll 4
             for (int w = 0; w < warps; ++w) {
-                const int c = hist[w * keys + e];
-                hist[w * keys + e] = run;
+                const int c = hist.get(w * keys + e);
+                hist.set(w * keys + e, run);
                 run += c;
             }
-            total[e] = run;
-            (many ? start : base)[e] = run;
+            total.set(e, run);
+            first.set(e, run);
         }
         if (many && !counts) {  // the tiles' counts, from the blocks of the cluster
             const auto cluster = cooperative_groups::this_cluster();
@@ -225,37 +230,38 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__
             for (int e = threadIdx.x; e < keys; e += blockDim.x) {
                 int all = 0, before = 0;
                 for (int b = 0; b < (int)gridDim.x; ++b) {
-                    const int c = *cluster.map_shared_rank(total + e, b);
+                    const int c = total.ok(e) ? *cluster.map_shared_rank(total.p + e, b) : 0;
                     all += c;
                     if (b < (int)blockIdx.x) before += c;
                 }
-                base[e] = all;
-                ahead[e] = before;
+                base.set(e, all);
+                ahead.set(e, before);
             }
             cluster.sync();  // no block leaves while its counts are read
             block_exclusive_scan(base, keys, tmp);
             for (int e = threadIdx.x; e < keys; e += blockDim.x) {
-                if (blockIdx.x == 0 && BMMC_WR_OK(offsets + e, 4)) offsets[e] = base[e];
-                base[e] += ahead[e];
+                const int from = base.get(e);
+                if (blockIdx.x == 0 && BMMC_WR_OK(offsets + e, 4)) offsets[e] = from;
+                base.set(e, from + ahead.get(e));
             }
         }
         __syncthreads();
-        block_exclusive_scan(many ? start : base, keys, tmp);
+        block_exclusive_scan(first, keys, tmp);
         if (!many)
             for (int e = threadIdx.x; e < keys; e += blockDim.x)
-                if (BMMC_WR_OK(offsets + e, 4)) offsets[e] = base[e];
+                if (BMMC_WR_OK(offsets + e, 4)) offsets[e] = base.get(e);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (key[r] >= keys) continue;
-            const int in_tile = ((warp * R) + r) * 32 + lane, in_key = mine[key[r]] + rank[r];
+            const int in_tile = ((warp * R) + r) * 32 + lane, in_key = mine.get(key[r]) + rank[r];
             const int64_t i = at + in_tile;
-            const int to = base[key[r]] + in_key;
+            const int to = base.get(key[r]) + in_key;
             const bool routed = key[r] < experts;
             if (BMMC_WR_OK(slot + i, 4)) slot[i] = routed ? to : ~to;
             if (kOrder) {
-                const int j = (many ? start : base)[key[r]] + in_key;
-                if (BMMC_SH_OK(order + j, 4)) order[j] = in_tile;
-                if (BMMC_SH_OK(order_key + j, 2)) order_key[j] = (unsigned short)key[r];
+                const int j = first.get(key[r]) + in_key;
+                order.set(j, in_tile);
+                order_key.set(j, (unsigned short)key[r]);
             } else if (BMMC_WR_OK(source + to, 4)) {
                 source[to] = routed ? (int)i : ~(int)i;
             }
@@ -264,13 +270,13 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const Id* __restrict__
         __syncthreads();
         const int here = (int)min((int64_t)blockDim.x * R, hi - at);
         for (int j = threadIdx.x; j < here; j += blockDim.x) {
-            const int k = order_key[j], i = (int)at + order[j], to = many ? base[k] + j - start[k] : j;
+            const int k = order_key.get(j), i = (int)at + order.get(j), to = many ? base.get(k) + j - start.get(k) : j;
             if ((unsigned)to < (unsigned)n && BMMC_WR_OK(source + to, 4)) source[to] = k < experts ? i : ~i;  // also if ids changed meanwhile
         }
         at += (int64_t)blockDim.x * R;
         if (at >= hi) return;
         __syncthreads();
-        for (int e = threadIdx.x; e < keys; e += blockDim.x) base[e] += total[e];
+        for (int e = threadIdx.x; e < keys; e += blockDim.x) base.set(e, base.get(e) + total.get(e));
     } while (true);
 }
 
@@ -355,15 +361,15 @@ constexpr int kStagedWords = 1100;  // of a block, 17.6 KB: a dozen blocks on an
 
 // Word j of the aligned words that hold a row's bytes from `start` on, copied
 // asynchronously; zero where it holds none of the row's `bytes` (or row NULL).
-__device__ __forceinline__ void stage_word(uint4* to, const char* row, int64_t start, int bytes, int j) {
+__device__ __forceinline__ void stage_word(Slots<uint4> words, int to, const char* row, int64_t start, int bytes, int j) {
     const char* const p =
         reinterpret_cast<const char*>((reinterpret_cast<uintptr_t>(row) + start) & ~(uintptr_t)15) + (int64_t)j * 16;
-    if (!BMMC_SH_OK(to, 16)) return;
+    if (!words.ok(to)) return;
     if (row && p + 16 > row && p < row + bytes && BMMC_RD_WORD_OK(p, 16))
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(to)), "l"(p)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(words.p + to)), "l"(p)
                      : "memory");
     else
-        *to = uint4{};
+        words.set(to, uint4{});
 }
 
 // The block's words are there.
@@ -372,12 +378,12 @@ __device__ __forceinline__ void staged() {
     __syncthreads();
 }
 
-// 16 bytes of a row, `start` bytes behind its start, from the staged words
-// that hold them.
+// 16 bytes of a row, `start` bytes behind its start, from the staged words j
+// and j + 1 that hold them.
 template <class T, int W>
-__device__ __forceinline__ Pack<T, W> staged_pack(const uint4* words, const char* row, int64_t start) {
+__device__ __forceinline__ Pack<T, W> staged_pack(Slots<uint4> words, int j, const char* row, int64_t start) {
     Pack<T, W> y;
-    y.word = cut(words[0], words[1], (unsigned)(reinterpret_cast<uintptr_t>(row) + start) & 15u);
+    y.word = cut(words.get(j), words.get(j + 1), (unsigned)(reinterpret_cast<uintptr_t>(row) + start) & 15u);
     return y;
 }
 
@@ -388,11 +394,11 @@ __device__ __forceinline__ int64_t stage_from(int64_t at) { return at - 16; }
 
 // 16 bytes from byte `start` of a row on, out of words staged from byte `from`.
 template <class T, int W>
-__device__ __forceinline__ Pack<T, W> staged_pack_at(const uint4* words, const char* row, int64_t from, int64_t start) {
+__device__ __forceinline__ Pack<T, W> staged_pack_at(Slots<uint4> words, const char* row, int64_t from, int64_t start) {
     const int at = (int)((reinterpret_cast<uintptr_t>(row) + start) -
                          ((reinterpret_cast<uintptr_t>(row) + from) & ~(uintptr_t)15));
     Pack<T, W> y;
-    y.word = cut(words[at >> 4], words[(at >> 4) + 1], at & 15);
+    y.word = cut(words.get(at >> 4), words.get((at >> 4) + 1), at & 15);
     return y;
 }
 
@@ -522,12 +528,13 @@ __global__ void __launch_bounds__(kStagedThreads)
     constexpr int W = 16 / sizeof(T);
     extern __shared__ uint4 s_words[];  // [part + 3]
     BMMC_SPANS_ENTER(s_words, chk::dyn_smem_bytes());
+    const Slots<uint4> words(s_words, part + 3);
     const int64_t t = blockIdx.x;
     const char* const row_x = x + t * x_stride;
     const int first = blockIdx.y * part;
     const int64_t from = stage_from((int64_t)first * 16);
     for (int j = threadIdx.x; j < part + 3; j += blockDim.x)
-        stage_word(s_words + j, row_x, from, length * (int)sizeof(T), j);
+        stage_word(words, j, row_x, from, length * (int)sizeof(T), j);
     staged();
     slot += t * choices;
     for (int k = 0; k < choices; ++k) {
@@ -540,7 +547,7 @@ __global__ void __launch_bounds__(kStagedThreads)
         for (int j = threadIdx.x; j < packs; j += blockDim.x) {
             Pack<T, W> o;
             if (s < 0) o.word = {};
-            else o = staged_pack_at<T, W>(s_words, row_x, from, (int64_t)walk.at(first + j) * (int)sizeof(T));
+            else o = staged_pack_at<T, W>(words, row_x, from, (int64_t)walk.at(first + j) * (int)sizeof(T));
             walk.store(o, to, first + j);
         }
     }
@@ -637,6 +644,9 @@ __global__ void __launch_bounds__(kStagedThreads)
     __shared__ const char* s_row[kStagedChoices];  // NULL: not there
     __shared__ float s_weight[kStagedChoices];
     BMMC_SPANS_ENTER(s_words, chk::dyn_smem_bytes(), s_row, sizeof(s_row), s_weight, sizeof(s_weight));
+    const Slots<uint4> words(s_words, choices * (part + 1));
+    const Slots<const char*> row(s_row, kStagedChoices);
+    const Slots<float> weight(s_weight, kStagedChoices);
     const int64_t t = blockIdx.x;
     const int tid = threadIdx.x;
     char* const to = out + t * out_stride;
@@ -648,14 +658,14 @@ __global__ void __launch_bounds__(kStagedThreads)
         const int s = BMMC_RD_OK(slot + at, 4) ? slot[at] : -1;
         const float f = weights ? weight_at<T>(weights, weights_f32, at) : 1.0f;
         const bool there = s >= 0 && s < n_rows;
-        s_row[tid] = there ? rows + s * row_stride : nullptr;
-        s_weight[tid] = there ? f : 0.0f;
+        row.set(tid, there ? rows + s * row_stride : nullptr);
+        weight.set(tid, there ? f : 0.0f);
     }
     __syncthreads();
     const int64_t start = (int64_t)walk.at(first) * (int)sizeof(T);  // of the part in a row, bytes
     for (int x = tid; x < choices * (part + 1); x += blockDim.x) {
         const int k = quotient(x, part + 1, part_magic), j = x - k * (part + 1);
-        if (j <= packs) stage_word(s_words + x, s_row[k], start, length * (int)sizeof(T), j);
+        if (j <= packs) stage_word(words, x, row.get(k), start, length * (int)sizeof(T), j);
     }
     staged();
     for (int j = tid; j < packs; j += blockDim.x) {
@@ -663,9 +673,10 @@ __global__ void __launch_bounds__(kStagedThreads)
 #pragma unroll
         for (int i = 0; i < W; ++i) sum[i] = 0.0f;
         for (int k = 0; k < choices; ++k) {
-            const Pack<T, W> y = staged_pack<T, W>(s_words + k * (part + 1) + j, s_row[k], start);
+            const Pack<T, W> y = staged_pack<T, W>(words.part(k * (part + 1), part + 1), j, row.get(k), start);
+            const float f = weight.get(k);
 #pragma unroll
-            for (int i = 0; i < W; ++i) sum[i] = fmaf(s_weight[k], y.get(i), sum[i]);
+            for (int i = 0; i < W; ++i) sum[i] = fmaf(f, y.get(i), sum[i]);
         }
         Pack<T, W> o;
         o.set(sum);
@@ -701,6 +712,7 @@ __global__ void __launch_bounds__(256, KB <= 2 ? 6 : 4) combine_backward_kernel(
         BMMC_SPANS_PARAM) {
     __shared__ float s_part[8][KB];
     BMMC_SPANS_ENTER(s_part, sizeof(s_part));
+    const Slots<float> part(&s_part[0][0], 8 * KB);  // [warps][choices]
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const bool live = t < tokens;
     const int x = blockDim.x, tid = threadIdx.y * x + threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -765,13 +777,13 @@ __global__ void __launch_bounds__(256, KB <= 2 ? 6 : 4) combine_backward_kernel(
             if (lane == 0)
 #pragma unroll
                 for (int j = 0; j < KB; ++j)
-                    if (BMMC_SH_OK(&s_part[warp][j], 4)) s_part[warp][j] = dot[j];
+                    part.set(warp * KB + j, dot[j]);
             __syncthreads();
             const int first = threadIdx.y * (x >> 5);
 #pragma unroll
             for (int j = 0; j < KB; ++j) {
                 dot[j] = 0.0f;
-                for (int i = 0; i < x >> 5; ++i) dot[j] += s_part[first + i][j];
+                for (int i = 0; i < x >> 5; ++i) dot[j] += part.get((first + i) * KB + j);
             }
         }
         if (live && threadIdx.x == 0)
@@ -808,20 +820,26 @@ __global__ void __launch_bounds__(kStagedThreads)
     __shared__ char* s_to[kStagedChoices];             // NULL: not written
     __shared__ float s_weight[kStagedChoices];
     __shared__ float s_dot[kStagedThreads / 32][kStagedChoices];
-    BMMC_SPANS_ENTER(s_words, chk::dyn_smem_bytes(), s_row, sizeof(s_row), s_to, sizeof(s_to), s_dot, sizeof(s_dot));
+    BMMC_SPANS_ENTER(s_words, chk::dyn_smem_bytes(), s_row, sizeof(s_row), s_to, sizeof(s_to), s_weight, sizeof(s_weight),
+                     s_dot, sizeof(s_dot));
     const int64_t t = blockIdx.x;
     const int tid = threadIdx.x, pitch = part + 3;
+    const Slots<uint4> words(s_words, (choices + 1) * pitch);
+    const Slots<const char*> row_of(s_row, kStagedChoices + 1);
+    const Slots<char*> to_of(s_to, kStagedChoices);
+    const Slots<float> weight(s_weight, kStagedChoices);
+    const Slots<float> dots(&s_dot[0][0], kStagedThreads / 32 * kStagedChoices);  // [warps][choices]
     if (tid < choices) {
         const int64_t at = t * choices + tid;
         const int s = BMMC_RD_OK(slot + at, 4) ? slot[at] : 0;
         const int64_t row = s < 0 ? ~s : s;
         const float f = weight_at<T>(weights, weights_f32, at);
         const bool there = s >= 0 && row < n_rows;
-        s_row[tid + 1] = there ? rows + row * row_stride : nullptr;
-        s_to[tid] = row < n_rows ? grad_rows + row * grad_row_stride : nullptr;
-        s_weight[tid] = there ? f : 0.0f;
+        row_of.set(tid + 1, there ? rows + row * row_stride : nullptr);
+        to_of.set(tid, row < n_rows ? grad_rows + row * grad_row_stride : nullptr);
+        weight.set(tid, there ? f : 0.0f);
     }
-    if (tid == 0) s_row[0] = grad + t * grad_stride;
+    if (tid == 0) row_of.set(0, grad + t * grad_stride);
     float dot[kStagedChoices];
 #pragma unroll
     for (int k = 0; k < kStagedChoices; ++k) dot[k] = 0.0f;
@@ -830,24 +848,25 @@ __global__ void __launch_bounds__(kStagedThreads)
         const int64_t from = stage_from((int64_t)first * 16);
         for (int x = tid; x < (choices + 1) * pitch; x += blockDim.x) {
             const int k = quotient(x, pitch, part_magic);
-            stage_word(s_words + x, s_row[k], from, length * (int)sizeof(T), x - k * pitch);
+            stage_word(words, x, row_of.get(k), from, length * (int)sizeof(T), x - k * pitch);
         }
         staged();
 #pragma unroll
         for (int k = 0; k < kStagedChoices; ++k) {
-            if (k >= choices || !s_to[k]) continue;
-            char* const to = s_to[k];
-            const char* const row = s_row[k + 1];
+            if (k >= choices) continue;
+            char* const to = to_of.get(k);
+            if (!to) continue;
+            const char* const row = row_of.get(k + 1);
             const Walk<T, W, true> walk(length, to);
             const int packs = min(part, walk.packs() - first);
-            const float f = s_weight[k];
+            const float f = weight.get(k);
             for (int j = tid; j < packs; j += blockDim.x) {
                 Pack<T, W> o;
                 o.word = {};
                 if (row) {
                     const int64_t start = (int64_t)walk.at(first + j) * (int)sizeof(T);
-                    Pack<T, W> g = staged_pack_at<T, W>(s_words, s_row[0], from, start);
-                    Pack<T, W> y = staged_pack_at<T, W>(s_words + (k + 1) * pitch, row, from, start);
+                    Pack<T, W> g = staged_pack_at<T, W>(words.part(0, pitch), row_of.get(0), from, start);
+                    Pack<T, W> y = staged_pack_at<T, W>(words.part((k + 1) * pitch, pitch), row, from, start);
                     walk.trim(g, first + j);
                     walk.trim(y, first + j);
                     float v[W];
@@ -865,11 +884,11 @@ __global__ void __launch_bounds__(kStagedThreads)
     sum_lanes(dot, 32);
     if ((tid & 31) == 0)
 #pragma unroll
-        for (int k = 0; k < kStagedChoices; ++k) s_dot[tid >> 5][k] = dot[k];
+        for (int k = 0; k < kStagedChoices; ++k) dots.set((tid >> 5) * kStagedChoices + k, dot[k]);
     __syncthreads();
     if (tid < choices) {
         float sum = 0.0f;
-        for (int i = 0; i < (int)blockDim.x >> 5; ++i) sum += s_dot[i][tid];
+        for (int i = 0; i < (int)blockDim.x >> 5; ++i) sum += dots.get(i * kStagedChoices + tid);
         const int64_t at = t * choices + tid;
         const int bytes = weights_f32 ? 4 : (int)sizeof(T);
         (void)bytes;

@@ -133,8 +133,7 @@ __device__ __forceinline__ float turned_second(float x, float y, float2 r) { ret
 // parts: the tokens' places in the caches and positions, and the cosines and
 // sines of their pairs, into shared memory; the whole block takes part.
 __device__ __forceinline__ void begin_block(const MoveParams& p, int64_t t0, int nt, int first_part, int last_part,
-                                            float2* s_turn, int64_t (&s_place)[2][kMaxTokensPerBlock],
-                                            float (&s_position)[kMaxTokensPerBlock]) {
+                                            Slots<float2> turns, Slots<int64_t> places, Slots<float> place_numbers) {
     const int tid = threadIdx.x, threads = blockDim.x;
     const bool turning = p.pairs && p.part[first_part].turned;
     // A thread's first turns (what they need but for a position that follows
@@ -166,27 +165,30 @@ __device__ __forceinline__ void begin_block(const MoveParams& p, int64_t t0, int
                          "r"(h.ahead)
                          : "memory");
     }
+    const auto keep_place = [&](int i, const Place& r) {
+        places.set(i, r.byte[0]);
+        places.set(kMaxTokensPerBlock + i, r.byte[1]);
+        place_numbers.set(i, (float)r.at);
+    };
     if (p.page_size) {
         if (p.starts && nt <= 8) {
             for (int i = tid >> 5; i < nt; i += threads >> 5) {
                 const Place r = place_of(p, t0 + i, find_sequence_warp(p.starts, p.sequences, t0 + i, tid & 31));
-                if ((tid & 31) == 0 && BMMC_SH_OK(&s_place[1][i], 8) && BMMC_SH_OK(s_position + i, 4))
-                    s_place[0][i] = r.byte[0], s_place[1][i] = r.byte[1], s_position[i] = (float)r.at;
+                if ((tid & 31) == 0) keep_place(i, r);
             }
         } else if (tid < nt) {
             const int64_t t = t0 + tid;
             const Place r = place_of(p, t, p.starts ? find_sequence(p.starts, p.sequences, t) : t);
-            if (BMMC_SH_OK(&s_place[1][tid], 8) && BMMC_SH_OK(s_position + tid, 4))
-                s_place[0][tid] = r.byte[0], s_place[1][tid] = r.byte[1], s_position[tid] = (float)r.at;
+            keep_place(tid, r);
         }
         if (!p.positions) __syncthreads();
     }
     if (turning) {
         const auto end_turn = [&](int i, float f, float at, bool from_place) {
-            if (from_place) at = s_position[quotient(i, p.pairs, p.pairs_magic)];
+            if (from_place) at = place_numbers.get(quotient(i, p.pairs, p.pairs_magic));
             float s, c;
             sincosf(at * f, &s, &c);
-            if (BMMC_SH_OK(s_turn + i, 8)) s_turn[i] = make_float2(c, p.sign * s);
+            turns.set(i, make_float2(c, p.sign * s));
         };
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
@@ -224,11 +226,14 @@ __global__ void __launch_bounds__(kMostThreads, 4)
     __shared__ float s_position[kMaxTokensPerBlock];
     BMMC_SPANS_ENTER(s_turn, chk::dyn_smem_bytes(), s_place, sizeof(s_place), s_position, sizeof(s_position));
     const int tid = threadIdx.x, per_block = blockDim.x >> p.group_log2;
+    const Slots<float2> turns(s_turn, per_block * p.pairs);
+    const Slots<int64_t> places(&s_place[0][0], 2 * kMaxTokensPerBlock);
+    const Slots<float> place_numbers(s_position, kMaxTokensPerBlock);
     const int64_t t0 = (int64_t)blockIdx.x * per_block;
     const int nt = (int)min((int64_t)per_block, p.tokens - t0);
     // a block of a small call takes one part only
     const int first_part = gridDim.y > 1 ? blockIdx.y : 0, last_part = gridDim.y > 1 ? first_part + 1 : p.parts;
-    begin_block(p, t0, nt, first_part, last_part, s_turn, s_place, s_position);
+    begin_block(p, t0, nt, first_part, last_part, turns, places, place_numbers);
     const int k = tid >> p.group_log2, in = tid & ((1 << p.group_log2) - 1);
     if (k >= nt) return;
     for (int q = first_part; q < last_part; ++q) {
@@ -237,12 +242,12 @@ __global__ void __launch_bounds__(kMostThreads, 4)
         if (down >= step) continue;
         int64_t to = (t0 + k) * h.dst_token;
         if (h.place) {
-            to = s_place[h.place - 1][k];
+            to = places.get((h.place - 1) * kMaxTokensPerBlock + k);
             if (to < 0) continue;
         }
         const char* const src = h.src + (t0 + k) * h.src_token;
         char* const dst = h.dst + to;
-        const float2* const turn = s_turn + k * p.pairs;
+        const Slots<float2> turn = turns.part(k * p.pairs, p.pairs);
         for (int j = in - down * h.across; j < h.items; j += h.across) {
             const bool turned = j < h.turning;
             // where the word lies, and its other half
@@ -261,7 +266,7 @@ __global__ void __launch_bounds__(kMostThreads, 4)
             if (turned)
 #pragma unroll
                 for (int i = 0; i < kTurns; ++i)
-                    r[i] = BMMC_SH_OK(turn + j * kTurns + i, 8) ? turn[j * kTurns + i] : float2{};
+                    r[i] = turn.get(j * kTurns + i);
             for (int head = down; head < h.heads; head += kHeadsAtOnce * step) {
                 Pack<T, W> a[kHeadsAtOnce], b[kHeadsAtOnce];
 #pragma unroll
@@ -332,13 +337,19 @@ __global__ void __launch_bounds__(kRowThreads)
     BMMC_SPANS_ENTER(s_turn, chk::dyn_smem_bytes(), s_place, sizeof(s_place), s_position, sizeof(s_position), s_rows,
                      sizeof(s_rows));
     const int tid = threadIdx.x, lane = tid & 31, per_block = blockDim.x >> p.group_log2;
+    const Slots<float2> turns(s_turn, per_block * p.pairs);
+    const Slots<int64_t> places(&s_place[0][0], 2 * kMaxTokensPerBlock);
+    const Slots<float> place_numbers(s_position, kMaxTokensPerBlock);
     const int64_t t0 = (int64_t)blockIdx.x * per_block;
     const int nt = (int)min((int64_t)per_block, p.tokens - t0);
     const int first_part = gridDim.y > 1 ? blockIdx.y : 0, last_part = gridDim.y > 1 ? first_part + 1 : p.parts;
-    begin_block(p, t0, nt, first_part, last_part, s_turn, s_place, s_position);
+    begin_block(p, t0, nt, first_part, last_part, turns, places, place_numbers);
     auto& mine = s_rows[tid >> 5];
-    Word* const words = reinterpret_cast<Word*>(mine.data);
-    T* const elements = reinterpret_cast<T*>(mine.data);
+    const Slots<Word> words(reinterpret_cast<Word*>(mine.data), kRowBytes / (int)sizeof(Word));
+    const Slots<T> elements(reinterpret_cast<T*>(mine.data), kRowBytes / (int)sizeof(T));
+    const Slots<const char*> src(mine.src, kRowBatch);
+    const Slots<char*> dst(mine.dst, kRowBatch);
+    const Slots<int> turns_of(mine.turns, kRowBatch);
     for (int q = first_part; q < last_part; ++q) {
         const Heads& h = p.part[q];
         const int row_elements = h.words * (int)(sizeof(Word) / sizeof(T));
@@ -346,40 +357,37 @@ __global__ void __launch_bounds__(kRowThreads)
             const int rows = min(h.batch, nt * h.heads - r0);
             if (lane < rows) {
                 const int k = (r0 + lane) / h.heads, head = r0 + lane - k * h.heads;
-                const int64_t to = h.place ? s_place[h.place - 1][k] : (t0 + k) * h.dst_token;
-                mine.src[lane] = h.src + (t0 + k) * h.src_token + head * h.src_head;
-                mine.dst[lane] = to < 0 ? nullptr : h.dst + to + head * h.dst_head;
-                mine.turns[lane] = k * p.pairs;
+                const int64_t to = h.place ? places.get((h.place - 1) * kMaxTokensPerBlock + k) : (t0 + k) * h.dst_token;
+                src.set(lane, h.src + (t0 + k) * h.src_token + head * h.src_head);
+                dst.set(lane, to < 0 ? nullptr : h.dst + to + head * h.dst_head);
+                turns_of.set(lane, k * p.pairs);
             }
             __syncwarp();
 #pragma unroll 4
             for (int x = lane; x < rows * h.words; x += 32) {
                 const int row = quotient(x, h.words, h.words_magic);
-                const char* const from = mine.src[row] + (x - row * h.words) * sizeof(Word);
-                if (BMMC_RD_OK(from, sizeof(Word)) && BMMC_SH_OK(words + x, sizeof(Word)))
-                    words[x] = *reinterpret_cast<const Word*>(from);
+                const char* const from = src.get(row) + (x - row * h.words) * sizeof(Word);
+                if (BMMC_RD_OK(from, sizeof(Word))) words.set(x, *reinterpret_cast<const Word*>(from));
             }
             __syncwarp();
             if (h.turned) {
 #pragma unroll 2
                 for (int x = lane; x < rows * p.pairs; x += 32) {
                     const int row = quotient(x, p.pairs, p.pairs_magic), i = x - row * p.pairs;
-                    T* const a = elements + row * row_elements + (p.adjacent ? 2 * i : i);
-                    T* const b = a + (p.adjacent ? 1 : p.pairs);
-                    const float2* const turn = s_turn + mine.turns[row] + i;
-                    if (!BMMC_SH_OK(a, sizeof(T)) || !BMMC_SH_OK(b, sizeof(T)) || !BMMC_SH_OK(turn, 8)) continue;
-                    const float2 r = *turn;
-                    const float u = to_f32(*a), v = to_f32(*b);
-                    *a = from_f32<T>(turned_first(u, v, r));
-                    *b = from_f32<T>(turned_second(u, v, r));
+                    const int a = row * row_elements + (p.adjacent ? 2 * i : i), b = a + (p.adjacent ? 1 : p.pairs);
+                    const float2 r = turns.get(turns_of.get(row) + i);
+                    const float u = to_f32(elements.get(a)), v = to_f32(elements.get(b));
+                    elements.set(a, from_f32<T>(turned_first(u, v, r)));
+                    elements.set(b, from_f32<T>(turned_second(u, v, r)));
                 }
                 __syncwarp();
             }
 #pragma unroll 4
             for (int x = lane; x < rows * h.words; x += 32) {
                 const int row = quotient(x, h.words, h.words_magic);
-                char* const to = mine.dst[row] + (x - row * h.words) * sizeof(Word);
-                if (mine.dst[row] && BMMC_WR_OK(to, sizeof(Word))) *reinterpret_cast<Word*>(to) = words[x];
+                char* const row_to = dst.get(row);
+                char* const to = row_to + (x - row * h.words) * sizeof(Word);
+                if (row_to && BMMC_WR_OK(to, sizeof(Word))) *reinterpret_cast<Word*>(to) = words.get(x);
             }
             __syncwarp();
         }

@@ -15,6 +15,40 @@ namespace bmmc {
 inline unsigned magic_of(int d) { return d > 1 ? (unsigned)((((uint64_t)1 << 32) + d - 1) / d) : 0; }
 __device__ __forceinline__ int quotient(int x, int d, unsigned magic) { return d == 1 ? x : (int)__umulhi(x, magic); }
 
+// A shared array, or a part of one, whose elements are reached by number.  In
+// bounds-checked builds each number is tested against the length, and each
+// address against the arrays that the kernel registered; otherwise it is a
+// pointer.
+template <class T>
+struct Slots {
+    T* p;
+#ifdef BMMC_BOUNDS_CHECK
+    int n;
+    __device__ __forceinline__ Slots(T* p_, int n_) : p(p_), n(n_) {}
+    __device__ __forceinline__ bool ok(int i, int line = __builtin_LINE()) const {
+        return chk::slot_ok(p, i, 1, n, sizeof(T), BMMC_CHK_FILE * 100000 + line);
+    }
+    // (a part that does not lie in the array has no elements)
+    __device__ __forceinline__ Slots part(int first, int count, int line = __builtin_LINE()) const {
+        return Slots(p + first, chk::slot_ok(p, first, count, n, sizeof(T), BMMC_CHK_FILE * 100000 + line) ? count : 0);
+    }
+    __device__ __forceinline__ T get(int i, int line = __builtin_LINE()) const { return ok(i, line) ? p[i] : T{}; }
+    __device__ __forceinline__ void set(int i, T v, int line = __builtin_LINE()) const {
+        if (ok(i, line)) p[i] = v;
+    }
+    __device__ __forceinline__ void add(int i, T v, int line = __builtin_LINE()) const {
+        if (ok(i, line)) atomicAdd(p + i, v);
+    }
+#else
+    __device__ __forceinline__ Slots(T* p_, int) : p(p_) {}
+    __device__ __forceinline__ bool ok(int) const { return true; }
+    __device__ __forceinline__ Slots part(int first, int) const { return Slots(p + first, 0); }
+    __device__ __forceinline__ T get(int i) const { return p[i]; }
+    __device__ __forceinline__ void set(int i, T v) const { p[i] = v; }
+    __device__ __forceinline__ void add(int i, T v) const { atomicAdd(p + i, v); }
+#endif
+};
+
 template <int BYTES> struct WordOf;
 template <> struct WordOf<16> { using type = uint4; };
 template <> struct WordOf<8> { using type = uint2; };
