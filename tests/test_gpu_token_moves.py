@@ -886,3 +886,43 @@ def test_append_to_caches_that_lie_between_each_other(head_major, between, count
             c["caches"] = [one.select(axis, 0), one.select(axis, 1)]
         _check_append(c, _freq(16), starts=max(counts) > 1)
         _check_append(c, _freq(32), interleaved=True)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("tokens,choices,hidden,pads,shift", [
+    (700, 2, 4095, (0, 0), 0), (700, 1, 4093, (3, 8), 1), (1300, 3, 2050, (1, 0), 1), (300, 8, 4092, (0, 4), 3),
+    (300, 8, 4093, (2, 5), 2), (5000, 2, 1031, (2, 2), 0), (200, 2, 12345, (0, 7), 1), (40, 4, 16400, (1, 0), 1),
+    (2500, 7, 1025, (3, 0), 2), (6000, 9, 515, (0, 0), 0), (20000, 8, 513, (0, 1), 0), (40000, 2, 260, (0, 0), 0), (700, 2, 4096, (0, 0), 0),
+    (400, 8, 4096, (8, 0), 0), (3, 5, 16400, (0, 1), 1), (1, 1, 1, (0, 0), 0), (33, 6, 2047, (0, 0), 3), (9, 64, 131, (1, 0), 0),
+])
+def test_sums_of_whole_numbers_are_exact(tokens, choices, hidden, pads, shift, dtype):
+    """No element of a row is left out or taken twice at a row's ends, where
+    the parts of a row or the words of a pack meet: all products are small
+    whole numbers other than zero, so that sums in 32 bits are exact in any
+    order (below 2**24) and every element counts."""
+    g = _gen(hidden + choices)
+    slot = _routing(g, tokens, choices, 11)
+    n = tokens * choices
+
+    def whole(k, pad):
+        v = torch.randint(1, 4, (k * (hidden + pad) + shift,), generator=g, device="cuda")
+        v = v * (2 * torch.randint(0, 2, v.shape, generator=g, device="cuda") - 1)
+        return v.to(dtype)[shift:].view(k, hidden + pad)[:, :hidden]
+
+    grad, rows = whole(tokens, pads[0]), whole(n, pads[1])
+    w = torch.randint(1, 5, (tokens, choices), generator=g, device="cuda").float()
+    keep, row = _picked(slot, n)
+    want_w, want_rows = torch.zeros_like(w), torch.zeros(n, hidden, device="cuda")
+    want = torch.zeros(tokens, hidden, device="cuda")
+    for k in range(choices):
+        t = keep[:, k].nonzero().flatten()
+        picked = rows[row[t, k]].float()
+        want_w[t, k] = (picked.double() * grad[t].double()).sum(1).float()
+        want_rows[row[t, k]] = w[t, k, None] * grad[t].float()
+        want[t] += w[t, k, None] * picked
+    assert float(want_w.abs().max()) < 2 ** 24
+    for weights in (w, w.to(dtype)):
+        grad_rows, grad_w = bm.expert_combine_backward(grad, rows, slot, weights)
+        assert torch.equal(grad_w, want_w.to(weights.dtype))
+        assert torch.equal(grad_rows, want_rows.to(dtype))
+        assert torch.equal(bm.expert_combine(rows, slot, weights), want.to(dtype))
