@@ -29,7 +29,7 @@ namespace {
 constexpr int kMaxExperts = 4096;
 constexpr int kSortRounds = 4;       // ids per lane and tile
 constexpr int kSortCluster = 8;      // blocks that are launched as one cluster
-constexpr int kMaxSortBlocks = 152;  // blocks of a sort that one block does not cover: one for each SM
+constexpr int kMaxSortBlocks = kSms;  // blocks of a sort that one block does not cover: one for each SM
 
 #ifdef BMMC_BOUNDS_CHECK
 __device__ __forceinline__ uint32_t chk_dynamic_bytes() { return chk::dyn_smem_bytes(); }
@@ -432,7 +432,7 @@ constexpr int kMostParts = 65535;
 
 // Up to this many words (one for every thread of the machine) the blocks are
 // smaller, so that more of the machine takes part.
-constexpr int64_t kFewWords = 152 * 2048;
+constexpr int64_t kFewWords = kSms * 2048;
 
 Cover cover(int64_t tokens, int words, int most) {
     // a grid has 65535 parts at most: rows of 2^24 elements are up to 2^23 words
@@ -574,8 +574,9 @@ __device__ __forceinline__ float weight_at(const void* weights, int in_f32, int6
 // it would like 75, KB = 1 70.6; 4096 x 8 (45.2) KB = 8 with 4 x 256 46.1,
 // without a bound on its registers and blocks of 256 55.9.  Rows that lie across
 // words: two loads for one, and the cut; 4096 x 8 rows of 4095 60.7 us,
-// 40961 x 2 rows of 1031 f32 93.3 (both faster staged, below).  32 tokens x 8 rows of 4096:
-// 2.3 us.
+// 40961 x 2 rows of 1031 f32 93.3 (both faster staged, below).  The bound on the
+// registers makes the 16-bit types spill one of them there (4 bytes).  32 tokens x
+// 8 rows of 4096: 2.1 us.
 template <class T, int W, int KB, bool ACROSS>
 __global__ void __launch_bounds__(256, KB > 2 ? 4 : ACROSS && sizeof(T) == 2 ? 6 : 8)
     combine_kernel(const char* __restrict__ rows, int64_t row_stride, int64_t n_rows, const int* __restrict__ slot,
@@ -625,12 +626,19 @@ __global__ void __launch_bounds__(256, KB > 2 ? 4 : ACROSS && sizeof(T) == 2 ? 6
 // into shared memory and adds the packs there.
 //
 // What the asynchronous copies have in flight takes no registers, which rows
-// across words and few choices need.  40961 x 2 rows of 1031 f32 75.5 us, 100 % of
-// the copy rate (from registers 93.3); 16384 x 2 rows of 4095 bf16 66.8 (89), of
+// across words and few choices need.  40961 x 2 rows of 1031 f32, one in twenty
+// choices left out, 74.7 us (from registers 93.3; with all of them 78.9, 94 % of
+// the copy rate); 16384 x 2 rows of 4095 bf16 66.8 (89), of
 // 4096 62.1 (64.3), 40960 x 2 of 1024 f32 73.0 (79.2); 8192 x 4 rows of 4095 61.7,
 // 4096 x 8 58.5 (60.7).  But 4096 x 8 rows of 4096 57 (46.1): with many choices that
 // lie in words there is enough in flight without, as there is for short rows:
 // 65536 x 2 rows of 1024 bf16 78.5 (63.4), of 701 70.8 (61.7), of 1025 92.4 (102.4).
+// Where the rule draws its lines, calls of about 450 MB, staged (from registers):
+// in words of 16 bytes three choices of 4096 bf16 89.4 us (93.7), of 1024 93.0
+// (92.7), of 4096 f32 87.9 (81.4); four 86.7 (79.3), f32 84.2 (73.8); eight 82.2
+// (67.0).  In words of 8 bytes four choices of 4092 bf16 88.1 (94.9), of 4094 f32
+// 81.6 (81.1); five 89.3 (100.0), f32 79.7 (92.3); six 88.9 (88.2), f32 79.4 (83.4);
+// eight 83.8 (75.3), f32 74.3 (72.4): five and some of six would gain by it.
 // Parts of 800 words, or of 1100 with two choices: 640 words 67.5 us at 16384 x 2
 // x 4095, 2200 77.4 at 4096 x 8.
 template <class T>
@@ -700,10 +708,11 @@ __device__ __forceinline__ void sum_lanes(float (&v)[N], int lanes) {
 //
 // Bound by HBM: grad_rows is written and rows are read once, grad once for KB
 // choices.  16384 x 8 rows of 4096 bf16, 2.28 GB: KB = 4 with 4 x 256 threads on
-// an SM 336.9 us = 6780 GB/s; KB = 8 (106 registers) 405, a choice after the
-// other with a barrier each 357.  16384 x 2: KB = 2, 6 x 128 98.8 us (floor 100.5),
-// blocks of 256 with the registers they would like 131.6.  Rows that lie across
-// words are bound by their instructions.
+// an SM 337.5 us = 6760 GB/s; KB = 8 (106 registers) 405, a choice after the
+// other with a barrier each 357.  16384 x 2: KB = 2 with 6 x 256 threads, 128 of them
+// on a token's row, 98.7 us = 6800 GB/s; with the registers it would like 131.6.
+// Rows that lie across words take two loads and two cuts a word, and the 16-bit
+// types spill one register (4 bytes) for the six blocks.
 template <class T, int W, int KB, bool ACROSS>
 __global__ void __launch_bounds__(256, KB <= 2 ? 6 : 4) combine_backward_kernel(
     const char* __restrict__ grad, int64_t grad_stride, const char* __restrict__ rows, int64_t row_stride,
@@ -806,7 +815,10 @@ __global__ void __launch_bounds__(256, KB <= 2 ? 6 : 4) combine_backward_kernel(
 // registers 180.3, floor 126.6), 16384 x 2 of 4095 bf16 123.8 (132.9), 65536 x 2 of
 // 1025 183 (206), 16384 x 8 of 513 108 (150), 4096 x 8 of 4095 146 (144), but
 // 65536 x 2 of 257 106 (93).  Rows in words of 8 bytes are faster from registers
-// (4096 x 8 of 4092 113, staged 142).
+// (4096 x 8 of 4092 113, staged 142).  Bound by its instructions: at 16384 x 8 of
+// 513, 107 us for 42 us of bytes, the issue slots are 82 % in use, by 105 M warp
+// instructions, and warps that could issue wait their turn (3.3 of the 13.7 that
+// stand by for each issue) more than they wait for loads (0.6).
 template <class T>
 __global__ void __launch_bounds__(kStagedThreads)
     combine_backward_staged_kernel(const char* __restrict__ grad, int64_t grad_stride, const char* __restrict__ rows,

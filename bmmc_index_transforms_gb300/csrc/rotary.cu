@@ -218,6 +218,13 @@ __device__ __forceinline__ void begin_block(const MoveParams& p, int64_t t0, int
 // 71-95; 6 blocks of 256 threads on an SM instead of 4, whose registers then spill,
 // 88; blocks of 256 threads 70.8, of 128 68.1.  256 single tokens: 4.3 us, the
 // chain lengths - table - sine - store and a launch.
+//
+// One head a token has a sine and a cosine for every pair of elements: 65536 x 1
+// x 64 15.1 us for 2.5 us of bytes, 4 heads 19.3 for 9.9.  Not bound by their
+// instructions: the issue slots are 51 % in use, and for each issue 2.3 warps
+// wait for a load, 2.2 for shared memory or a special function, 2.0 for a result
+// and 1.9 at the barrier.  A thread has two turns on their way at a time (kAhead),
+// the rest of its eight follow one after another.
 template <class T, int W, bool ADJACENT>
 __global__ void __launch_bounds__(kMostThreads, 4)
     move_heads_kernel(const __grid_constant__ MoveParams p BMMC_SPANS_PARAM) {
@@ -411,7 +418,7 @@ int deal_out(MoveParams& p, const int (&dims)[3], int W, int es, bool adjacent, 
     }
     int full = 2, group;
     while (full < 8 && (1 << full) < most) ++full;
-    const bool small = (p.tokens << full) <= 152 * 1024;
+    const bool small = (p.tokens << full) <= kSms * 1024;
     group = small ? std::min(full, 7) : most > 1024 ? full : std::max(2, full - 2);
     int threads = small ? std::max(64, 1 << group) : std::max(kThreads, 1 << group);
     while ((threads >> group) > kMaxTokensPerBlock) ++group;
@@ -424,7 +431,7 @@ int deal_out(MoveParams& p, const int (&dims)[3], int W, int es, bool adjacent, 
         const bool dense = p.device && W * es == 16 && (h.heads < 2 || h.src_head == (int64_t)dims[q] * es);
         h.ahead = dense ? std::min((unsigned)(h.heads * dims[q] * es), 65536u) : 0u;
     }
-    *split = p.parts > 1 && p.tokens / (threads >> group) * p.parts * threads <= 152 * 1024;
+    *split = p.parts > 1 && p.tokens / (threads >> group) * p.parts * threads <= kSms * 1024;
     return threads;
 }
 
@@ -433,7 +440,7 @@ template <class T, class Word>
 bmmc_status launch_rows(MoveParams& p, const int (&dims)[3], bool adjacent, const chk::Spans& spans, cudaStream_t st) {
     (void)spans;
     p.adjacent = adjacent;
-    int per_block = p.tokens >= 152 * 32 ? 4 : 1;
+    int per_block = p.tokens >= kSms * 32 ? 4 : 1;
     while (per_block > 1 && per_block * p.pairs * sizeof(float2) > 32 * 1024) per_block >>= 1;
     p.group_log2 = per_block == 4 ? 5 : per_block == 2 ? 6 : 7;
     for (int q = 0; q < p.parts; ++q) {
@@ -446,7 +453,7 @@ bmmc_status launch_rows(MoveParams& p, const int (&dims)[3], bool adjacent, cons
         const bool dense = p.device && sizeof(Word) == 16 && (h.heads < 2 || h.src_head == (int64_t)row_bytes);
         h.ahead = dense ? std::min((unsigned)(h.heads * row_bytes), 65536u) : 0u;
     }
-    const bool split = p.parts > 1 && p.tokens * p.parts <= 152 * 8;
+    const bool split = p.parts > 1 && p.tokens * p.parts <= kSms * 8;
     const dim3 grid((unsigned)((p.tokens + per_block - 1) / per_block), split ? p.parts : 1);
     return launch(move_rows_kernel<T, Word>, grid, dim3(kRowThreads), (size_t)per_block * p.pairs * sizeof(float2), st,
                   nullptr, p BMMC_SPANS_ARG(spans));

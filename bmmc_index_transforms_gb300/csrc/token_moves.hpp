@@ -17,6 +17,11 @@ namespace bmmc {
 constexpr int64_t kMaxStride = (int64_t)1 << 40;  // elements
 constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 1;
 
+// SMs of a GB300.  Rules that ask whether a call fills the machine count in
+// them; on another number of SMs they choose another form, with the same
+// results.
+constexpr int kSms = 152;
+
 // Whether a stride is out of range, or `n` steps of it lead further than any
 // memory (so that byte offsets stay far below 2^63).
 inline bool bad_stride(int64_t stride, int64_t n) {

@@ -13,6 +13,9 @@ back to it, so another stream that uses them waits for it first (and, as with
 any tensor of torch's, is recorded where they may be dropped meanwhile).  The
 inputs have to be ready on it and to last until its work is done.
 
+Results carry no autograd history: the gradients are calls of their own
+(``examples/expert_decoder.py`` wraps them in autograd functions).
+
 The calls of a decoding step take a few microseconds on the device, less than
 a careless binding takes on the host: a check costs no more than its
 comparison here, and what a refusal says is put together when it is raised.
