@@ -20,8 +20,8 @@ from typing import Sequence
 from . import _capi
 from ._capi import PlanInfo, PlanOpts
 from ._streams import empty_on
-from .token_moves import (expert_combine, expert_combine_backward, expert_dispatch, expert_sort, paged_append,
-                          rotary)
+from .token_moves import (embedding_backward, embedding_lookup, expert_balance, expert_balance_backward, expert_combine,
+                          expert_combine_backward, expert_dispatch, expert_sort, paged_append, paged_read, rotary)
 
 __all__ = [
     "BmmcError", "Plan", "bmmc_plan", "bmmc_plan_ex", "bmmc_plan_destroy", "bmmc_plan_info",
@@ -30,6 +30,7 @@ __all__ = [
     "bmmc_dims_permute_bits", "bmmc_copy", "bmmc_lmad_copy", "bmmc_lmad_bpc", "lmad_copy", "lmad_copy_query", "lmad_copy_tensor", "contiguous", "bmmc_parm_rows", "bmmc_inverse_rows", "bmmc_compose",
     "bmmc_status_string", "bmmc_version", "library_path",
     "expert_sort", "expert_dispatch", "expert_combine", "expert_combine_backward", "rotary", "paged_append",
+    "expert_balance", "expert_balance_backward", "embedding_lookup", "embedding_backward", "paged_read",
 ]
 
 CLASS_NAMES = {0: "identity", 1: "complement", 2: "bp", 3: "bpc", 4: "bmmc"}

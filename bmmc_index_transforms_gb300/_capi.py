@@ -80,16 +80,19 @@ class LmadCopyInfo(ctypes.Structure):
 
 
 # bmmc_dtype
-F32, F16, BF16 = range(3)
+F32, F16, BF16, E4M3, I8 = range(5)
 DEVICE_POINTERS = 0x100
 EXPERT_MAX_CHOICES = 64
 # rotary_turns_t.flags
 ROTARY_ADJACENT, ROTARY_INVERSE = 0x1, 0x2
-# rotary_args_t and paged_append_args_t, whose fields are all 8 bytes wide, as
+# rotary_args_t, paged_append_args_t, paged_append_quantised_args_t and
+# paged_read_args_t, whose fields are all 8 bytes wide, as
 # packed values (made in one call, where a ctypes.Structure stores one field
 # after another)
 ROTARY_ARGS = struct.Struct("=2q10q8q")
 PAGED_APPEND_ARGS = struct.Struct("=2q20q8q3q5q8q")
+PAGED_APPEND_QUANTISED_ARGS = struct.Struct("=2q20q8q3q5q8q9q")
+PAGED_READ_ARGS = struct.Struct("=3q10q3q5q16q")
 
 
 class BoundsReport(ctypes.Structure):
@@ -150,6 +153,18 @@ SIGNATURES = {
                                                ctypes.c_int, vp, i64, vp, vp]),
     "rotary": (ctypes.c_int, [vp, vp]),
     "paged_append": (ctypes.c_int, [vp, vp]),
+    "paged_append_quantised": (ctypes.c_int, [vp, vp]),
+    "paged_read": (ctypes.c_int, [vp, vp]),
+    "expert_balance_workspace": (ctypes.c_int, [i64, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
+    "expert_balance": (ctypes.c_int, [vp, i64, ctypes.c_int, vp, ctypes.c_int, i64, ctypes.c_int, ctypes.c_int, vp, vp,
+                                      vp, ctypes.c_size_t, vp]),
+    "expert_balance_backward": (ctypes.c_int, [vp, vp, i64, ctypes.c_int, vp, ctypes.c_int, i64, ctypes.c_int,
+                                               ctypes.c_int, vp, vp, i64, vp]),
+    "embedding_lookup": (ctypes.c_int, [vp, i64, i64, vp, ctypes.c_int, i64, i64, ctypes.c_int, ctypes.c_float, vp, i64,
+                                        vp]),
+    "embedding_backward_workspace": (ctypes.c_int, [i64, i64, i64, ctypes.POINTER(ctypes.c_size_t)]),
+    "embedding_backward": (ctypes.c_int, [vp, i64, vp, ctypes.c_int, i64, i64, ctypes.c_int, ctypes.c_float,
+                                          ctypes.c_int, vp, i64, i64, ctypes.c_int, vp, ctypes.c_size_t, vp]),
     "bmmc_bounds_report": (ctypes.c_int, [ctypes.POINTER(BoundsReport), ctypes.c_int]),
     "bmmc_bounds_selftest": (ctypes.c_int, [vp, vp]),
 }

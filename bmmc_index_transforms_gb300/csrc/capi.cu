@@ -520,7 +520,7 @@ bmmc_status bmmc_bounds_report(bmmc_bounds_report_t* report, int reset) {
 #ifdef BMMC_BOUNDS_CHECK
     r.enabled = 1;
 #endif
-    unsigned long long rec[7][6] = {};
+    unsigned long long rec[10][6] = {};
     if (r.enabled) {
         if (cudaDeviceSynchronize() != cudaSuccess || bounds_record_kernels(rec[0], reset != 0) != cudaSuccess ||
             bounds_record_lmad(rec[1], reset != 0) != cudaSuccess ||
@@ -528,7 +528,10 @@ bmmc_status bmmc_bounds_report(bmmc_bounds_report_t* report, int reset) {
             bounds_record_lmad_transpose_4_8_16(rec[3], reset != 0) != cudaSuccess ||
             bounds_record_lmad_block(rec[4], reset != 0) != cudaSuccess ||
             bounds_record_experts(rec[5], reset != 0) != cudaSuccess ||
-            bounds_record_rotary(rec[6], reset != 0) != cudaSuccess) {
+            bounds_record_rotary(rec[6], reset != 0) != cudaSuccess ||
+            bounds_record_embedding(rec[7], reset != 0) != cudaSuccess ||
+            bounds_record_balance(rec[8], reset != 0) != cudaSuccess ||
+            bounds_record_paged_cache8(rec[9], reset != 0) != cudaSuccess) {
             cudaGetLastError();
             return BMMC_ERR_CUDA;
         }

@@ -422,32 +422,6 @@ Parts parts_of(int64_t hidden, int most) {
 
 // ---- dispatch ----------------------------------------------------------------
 
-// How the words of the tokens' rows are dealt out: blocks of x * y threads
-// take y tokens and x words of each; gridDim.y parts make up a row.
-struct Cover {
-    dim3 grid, block;
-};
-
-constexpr int kMostParts = 65535;
-
-// Up to this many words (one for every thread of the machine) the blocks are
-// smaller, so that more of the machine takes part.
-constexpr int64_t kFewWords = kSms * 2048;
-
-Cover cover(int64_t tokens, int words, int most) {
-    // a grid has 65535 parts at most: rows of 2^24 elements are up to 2^23 words
-    while ((words + most - 1) / most > kMostParts) most <<= 1;
-    const int parts = (words + most - 1) / most, need = (words + parts - 1) / parts;
-    int x = 4;
-    while (x < 32 && x < need) x <<= 1;
-    if (x < need) x = (need + 31) / 32 * 32;
-    const int y = x >= most ? 1 : most / x;
-    Cover c;
-    c.block = dim3(x, y);
-    c.grid = dim3((unsigned)((tokens + y - 1) / y), (unsigned)((words + x - 1) / x));
-    return c;
-}
-
 // Pure movement: a token's row is read once and written to the rows of its
 // choices, one word a thread.  Bound by HBM: 16384 tokens of 4096 bf16 to 8
 // rows each, 1.21 GB, 180.8 us = 6685 GB/s, a plain copy's rate; to 2 rows
@@ -910,39 +884,6 @@ __global__ void __launch_bounds__(kStagedThreads)
     }
 }
 
-// How rows of `hidden` elements are walked: in words of 16 or 8 bytes where
-// all addresses, strides and lengths (or'ed into `bits`, in bytes) are
-// multiples of them, else across the words' bounds.
-struct Way {
-    int bytes;   // 16, 8 or 0: across
-    int words;   // of a row; across: at most
-};
-
-Way way_of(int64_t hidden, int es, std::initializer_list<uint64_t> bits) {
-    const int wb = word_bytes(es, bits);
-    if (wb >= 8) return {wb, (int)(hidden * es / wb)};
-    const int W = 16 / es;
-    return {0, (int)((hidden + 2 * (W - 1)) / W)};
-}
-
-// Calls f(T{}, elements per word, across).
-template <class T, class F>
-void by_way(const Way& way, F&& f) {
-    constexpr int es = sizeof(T);
-    if (way.bytes == 16) f(T{}, std::integral_constant<int, 16 / es>{}, std::false_type{});
-    else if (way.bytes == 8) f(T{}, std::integral_constant<int, 8 / es>{}, std::false_type{});
-    else f(T{}, std::integral_constant<int, 16 / es>{}, std::true_type{});
-}
-
-template <class F>
-void by_type(int type, const Way& way, F&& f) {
-    switch (type) {
-        case BMMC_F32: by_way<float>(way, f); break;
-        case BMMC_F16: by_way<__half>(way, f); break;
-        default: by_way<__nv_bfloat16>(way, f); break;
-    }
-}
-
 bmmc_status check_moves(int64_t tokens, int choices, int64_t hidden, int64_t n_rows, int type, int* es) {
     if (!(*es = dtype_bytes(type))) return BMMC_ERR_UNSUPPORTED_ELEM;
     if (tokens < 0 || choices < 1 || choices > EXPERT_MAX_CHOICES || tokens > kMaxTokens / choices || hidden < 1 ||
@@ -950,13 +891,6 @@ bmmc_status check_moves(int64_t tokens, int choices, int64_t hidden, int64_t n_r
         return BMMC_ERR_INVALID_ARG;
     return BMMC_OK;
 }
-
-// Rows that are written lie apart.
-bool bad_output_stride(int64_t stride, int64_t hidden, int64_t rows) {
-    return bad_stride(stride, rows) || (rows > 1 && stride < hidden);
-}
-
-bool misaligned(const void* p, size_t bytes) { return (uintptr_t)p & (bytes - 1); }
 
 }  // namespace
 

@@ -1,0 +1,365 @@
+// Keys and values in a paged cache of 8 bits, written with a scale for each
+// head of each entry, and a cache's entries read back in the order of the
+// sequences: paged_append_quantised and paged_read (declared in
+// include/bmmc.h).
+//
+// A head y of D elements has the scale s = max |y| / M, M the largest value of
+// the 8-bit type, and the values round(y / s).
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <type_traits>
+
+#include "../../include/bmmc.h"
+#define BMMC_CHK_FILE 10  // site tag of this file in bounds-checked builds
+#include "bounds.cuh"
+#include "paged_places.cuh"
+#include "token_moves.hpp"
+#include "token_words.cuh"
+
+using namespace bmmc;
+
+namespace {
+
+constexpr int kThreads = 128, kWarps = kThreads / 32;
+
+// The 8-bit types: the factor 1 / M of a scale, a value and what it stands for.
+struct E4m3 {
+    using Code = unsigned char;
+    static constexpr float kOver = 1.0f / 448.0f;
+    static __device__ __forceinline__ Code encode(float y) { return __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3); }
+    static __device__ __forceinline__ float decode(Code c) {
+        return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+    }
+};
+struct I8 {
+    using Code = signed char;
+    static constexpr float kOver = 1.0f / 127.0f;
+    static __device__ __forceinline__ Code encode(float y) { return (Code)max(-127, min(127, __float2int_rn(y))); }
+    static __device__ __forceinline__ float decode(Code c) { return (float)c; }
+};
+
+constexpr float kLeastScale = 0x1p-126f;  // so that 1 / scale is finite, and zeros have one
+
+// The scale of a head whose largest |y| has these bits (as whole numbers they
+// are in the order of the values, with infinities and NaN above all others).
+// A head that holds one of those has the scale NaN.
+template <class Q>
+__device__ __forceinline__ float scale_of(unsigned most) {
+    return most >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : fmaxf(__fmul_rn(__uint_as_float(most), Q::kOver), kLeastScale);
+}
+
+__device__ __forceinline__ unsigned magnitude(float y) { return __float_as_uint(y) & 0x7fffffffu; }
+
+// Where the scales of a cache lie; strides in bytes.
+struct Scales {
+    char* data;
+    int64_t page, slot, head;
+    __device__ __forceinline__ float* at(int p, int s, int h) const {
+        return reinterpret_cast<float*>(data + p * page + s * slot + h * head);
+    }
+};
+
+// ---- append --------------------------------------------------------------------
+
+struct QuantisedParams {
+    MoveParams p;
+    Scales scales[2];
+    int dims[3];
+    int stage;  // floats of a warp's staged head
+};
+
+// Any heads: a warp turns a head, an element a lane, stages it in shared
+// memory in 32 bits, and writes its values with their scale.
+template <class T, class Q>
+__global__ void __launch_bounds__(kThreads) append_heads_kernel(const __grid_constant__ QuantisedParams qp BMMC_SPANS_PARAM) {
+    extern __shared__ float2 s_turn[];  // [tokens of the block][pairs] cos, sin; then a head a warp
+    __shared__ int64_t s_place[2][kMaxTokensPerBlock];
+    __shared__ float s_position[kMaxTokensPerBlock];
+    __shared__ int s_slot[2][kMaxTokensPerBlock];
+    BMMC_SPANS_ENTER(s_turn, chk::dyn_smem_bytes(), s_place, sizeof(s_place), s_position, sizeof(s_position), s_slot,
+                     sizeof(s_slot));
+    using Code = typename Q::Code;
+    const MoveParams& p = qp.p;
+    const int tid = threadIdx.x, lane = tid & 31, per_block = blockDim.x >> p.group_log2;
+    const Slots<float2> turns(s_turn, per_block * p.pairs);
+    const Slots<int64_t> places(&s_place[0][0], 2 * kMaxTokensPerBlock);
+    const Slots<float> place_numbers(s_position, kMaxTokensPerBlock);
+    const Slots<int> slots(&s_slot[0][0], 2 * kMaxTokensPerBlock);
+    const Slots<float> stage(reinterpret_cast<float*>(s_turn + per_block * p.pairs) + (tid >> 5) * qp.stage, qp.stage);
+    const int64_t t0 = (int64_t)blockIdx.x * per_block;
+    const int nt = (int)min((int64_t)per_block, p.tokens - t0);
+    begin_block(p, t0, nt, 0, p.parts, turns, places, place_numbers, slots);
+    int rows = 0;
+    for (int q = 0; q < p.parts; ++q) rows += nt * p.part[q].heads;
+    for (int r = tid >> 5; r < rows; r += kWarps) {
+        int q = 0, i = r;
+        while (i >= nt * p.part[q].heads) i -= nt * p.part[q++].heads;
+        const Heads& h = p.part[q];
+        const int k = i / h.heads, head = i - k * h.heads, dim = qp.dims[q], pairs = h.turned ? p.pairs : 0;
+        const int64_t to = h.place ? places.get((h.place - 1) * kMaxTokensPerBlock + k) : (t0 + k) * h.dst_token;
+        if (to < 0) continue;
+        const T* const src = reinterpret_cast<const T*>(h.src + (t0 + k) * h.src_token + head * h.src_head);
+        char* const dst = h.dst + to + head * h.dst_head;
+        const auto value = [&](int e) { return BMMC_RD_OK(src + e, sizeof(T)) ? to_f32(src[e]) : 0.0f; };
+        const auto keep = [&](int e, float y) {
+            if (h.place) stage.set(e, y);
+            else if (BMMC_WR_OK(dst + e * sizeof(T), sizeof(T))) reinterpret_cast<T*>(dst)[e] = from_f32<T>(y);
+        };
+        unsigned most = 0;
+        // (queries turned in place: a pair's elements are read before they are written)
+        for (int j = lane; j < pairs; j += 32) {
+            const int a = p.adjacent ? 2 * j : j, b = a + (p.adjacent ? 1 : pairs);
+            const float2 turn = turns.get(k * p.pairs + j);
+            const float x = value(a), y = value(b), u = turned_first(x, y, turn), v = turned_second(x, y, turn);
+            keep(a, u), keep(b, v);
+            most = max(most, max(magnitude(u), magnitude(v)));
+        }
+        for (int e = 2 * pairs + lane; e < dim; e += 32) {
+            const float y = value(e);
+            keep(e, y);
+            most = max(most, magnitude(y));
+        }
+        if (!h.place) continue;
+        most = __reduce_max_sync(~0u, most);
+        const float scale = scale_of<Q>(most), over = __frcp_rn(scale);
+        __syncwarp();
+        for (int e = lane; e < dim; e += 32)
+            if (BMMC_WR_OK(dst + e, 1)) reinterpret_cast<Code*>(dst)[e] = Q::encode(__fmul_rn(stage.get(e), over));
+        float* const s = qp.scales[h.place - 1].at(slots.get(k), slots.get(kMaxTokensPerBlock + k), head);
+        if (lane == 0 && BMMC_WR_OK(s, 4)) *s = scale;
+        __syncwarp();
+    }
+}
+
+template <class T, class Q>
+bmmc_status launch_append(QuantisedParams& qp, const chk::Spans& spans, cudaStream_t st) {
+    (void)spans;
+    MoveParams& p = qp.p;
+    int per_block = p.tokens >= kSms * 32 ? 4 : 1;
+    while (per_block > 1 && per_block * p.pairs * sizeof(float2) > 32 * 1024) per_block >>= 1;
+    p.group_log2 = per_block == 4 ? 5 : per_block == 2 ? 6 : 7;
+    qp.stage = std::max(qp.dims[0], qp.dims[1]);
+    const size_t smem = (size_t)per_block * p.pairs * sizeof(float2) + (size_t)kWarps * qp.stage * 4;
+    const auto kernel = append_heads_kernel<T, Q>;
+    if (smem > 40 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+        cudaGetLastError();
+        return BMMC_ERR_CUDA;
+    }
+    return launch(kernel, dim3((unsigned)((p.tokens + per_block - 1) / per_block)), dim3(kThreads), smem, st, nullptr,
+                  qp BMMC_SPANS_ARG(spans));
+}
+
+// ---- read ----------------------------------------------------------------------
+
+struct ReadParams {
+    MoveParams p;  // part[0], part[1]: from the caches to the rows; lengths: each sequence's first entry
+    Scales scales[2];
+    int dims[2];
+};
+
+// A value of 8 bits or of the result's type as the result's type.
+template <class T, class Q>
+__device__ __forceinline__ T read_value(const char* from, int e, float scale) {
+    if constexpr (std::is_void_v<Q>) {
+        return BMMC_RD_OK(from + e * sizeof(T), sizeof(T)) ? reinterpret_cast<const T*>(from)[e] : from_f32<T>(0.0f);
+    } else {
+        using Code = typename Q::Code;
+        return from_f32<T>(BMMC_RD_OK(from + e, 1) ? __fmul_rn(Q::decode(reinterpret_cast<const Code*>(from)[e]), scale) : 0.0f);
+    }
+}
+
+// A warp a row, an element a lane.
+template <class T, class Q>
+__global__ void __launch_bounds__(kThreads) read_rows_kernel(const __grid_constant__ ReadParams rp BMMC_SPANS_PARAM) {
+    BMMC_SPANS_ENTER_GLOBAL();
+    const MoveParams& p = rp.p;
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (t >= p.tokens) return;
+    const Place place = place_of(p, t, find_sequence_warp(p.starts, p.sequences, t, lane));
+    for (int q = 0; q < 2; ++q) {
+        const Heads& h = p.part[q];
+        for (int head = 0; head < h.heads; ++head) {
+            T* const to = reinterpret_cast<T*>(h.dst + t * h.dst_token + head * h.dst_head);
+            const char* const from = h.src + place.byte[q] + head * h.src_head;
+            float scale = 0.0f;
+            if (!std::is_void_v<Q> && place.page >= 0) {
+                const float* const s = rp.scales[q].at(place.page, place.slot, head);
+                if (BMMC_RD_OK(s, 4)) scale = *s;
+            }
+            for (int e = lane; e < rp.dims[q]; e += 32)
+                if (BMMC_WR_OK(to + e, sizeof(T))) to[e] = place.page < 0 ? from_f32<T>(0.0f) : read_value<T, Q>(from, e, scale);
+        }
+    }
+}
+
+template <class T, class Q>
+bmmc_status launch_read(const ReadParams& rp, const chk::Spans& spans, cudaStream_t st) {
+    (void)spans;
+    return launch(read_rows_kernel<T, Q>, dim3((unsigned)((rp.p.tokens + kWarps - 1) / kWarps)), dim3(kThreads), 0, st, nullptr,
+                  rp BMMC_SPANS_ARG(spans));
+}
+
+// ---- host ----------------------------------------------------------------------
+
+// Checks the scales of a cache of these pages, [pages][page_size][heads] floats.
+bmmc_status read_scales(const paged_cache_t& s, int64_t pages, int64_t page_size, int64_t heads, Scales& to, Rows& rows) {
+    const bmmc_status status = check_cache(s, pages, page_size, heads, 1, 4);
+    if (status != BMMC_OK) return status;
+    to = Scales{static_cast<char*>(s.data), s.page_stride * 4, s.slot_stride * 4, s.head_stride * 4};
+    rows = cache_rows(s, pages, page_size, heads, 1, 4);
+    return BMMC_OK;
+}
+
+// Whether two results lie between each other, by token or by head.
+bool heads_between(const token_heads_t& k, const token_heads_t& v, int64_t tokens, int es) {
+    if ((tokens > 1 && k.token_stride != v.token_stride) || (k.heads > 1 && k.head_stride != v.head_stride)) return false;
+    const int64_t sizes[2] = {tokens, k.heads}, strides[2] = {k.token_stride * es, k.head_stride * es};
+    return lie_between(k.dim * es, v.dim * es, sizes, strides, (int64_t)((uintptr_t)v.data - (uintptr_t)k.data));
+}
+
+template <class F>
+bmmc_status by_cache_type(int type, int64_t cache_type, F&& f) {
+    const auto cache = [&](auto t) { return cache_type == BMMC_I8 ? f(t, I8{}) : f(t, E4m3{}); };
+    if (type == BMMC_F32) return cache(float{});
+    return type == BMMC_F16 ? cache(__half{}) : cache(__nv_bfloat16{});
+}
+
+}  // namespace
+
+extern "C" {
+
+bmmc_status paged_append_quantised(const paged_append_quantised_args_t* args, void* stream) {
+    if (!args) return BMMC_ERR_INVALID_ARG;
+    const paged_append_args_t& a = args->append;
+    if (a.tokens < 0 || a.tokens > kMaxTokens) return BMMC_ERR_INVALID_ARG;
+    int type = a.type < 0 || a.type > 0xfff ? -1 : (int)a.type;
+    const bool device = device_pointers(type);
+    const int es = dtype_bytes(type);
+    if (!es || (args->cache_type != BMMC_E4M3 && args->cache_type != BMMC_I8)) return BMMC_ERR_UNSUPPORTED_ELEM;
+    if (!a.tokens) return BMMC_OK;
+    AppendCall c;
+    bmmc_status s = read_append(a, es, 1, device, c);
+    if (s != BMMC_OK) return s;
+    QuantisedParams qp{};
+    Rows scales[2];
+    const paged_cache_t* from[2] = {&args->k_scales, &args->v_scales};
+    for (int i = 0; i < 2; ++i)
+        if ((s = read_scales(*from[i], a.pages, a.page_size, a.k.heads, qp.scales[i], scales[i])) != BMMC_OK) return s;
+    for (const Rows& r : scales) {
+        for (const Rows& w : c.written)
+            if (may_overlap(r, w)) return BMMC_ERR_ALIAS;
+        for (const Rows& m : c.maps)
+            if (may_overlap(r, m)) return BMMC_ERR_ALIAS;
+        if (may_overlap(r, c.k) || may_overlap(r, c.v) || may_overlap(r, c.q) || meets_turns(r, a.turns, a.tokens))
+            return BMMC_ERR_ALIAS;
+    }
+    if (may_overlap(scales[0], scales[1])) return BMMC_ERR_ALIAS;
+    if ((s = all_reachable(device, {args->k_scales.data, args->v_scales.data})) != BMMC_OK) return s;
+    qp.p = c.moves;
+    qp.p.adjacent = a.turns.flags & ROTARY_ADJACENT;
+    for (int i = 0; i < 3; ++i) qp.dims[i] = c.dims[i];
+    const chk::Spans spans = spans_of({c.k, c.v, c.q, turn_rows(a.turns, a.tokens, 0), turn_rows(a.turns, a.tokens, 1),
+                                       turn_rows(a.turns, a.tokens, 2), c.maps[0], c.maps[1], c.maps[2]},
+                                      {c.written[0], c.written[1], c.written[2], scales[0], scales[1]});
+    return by_cache_type(type, args->cache_type, [&](auto t, auto q) {
+        return launch_append<decltype(t), decltype(q)>(qp, spans, static_cast<cudaStream_t>(stream));
+    });
+}
+
+bmmc_status paged_read(const paged_read_args_t* a, void* stream) {
+    if (!a || a->tokens < 0 || a->tokens > kMaxTokens) return BMMC_ERR_INVALID_ARG;
+    int type = a->type < 0 || a->type > 0xfff ? -1 : (int)a->type;
+    const bool device = device_pointers(type);
+    const int es = dtype_bytes(type);
+    if (!es) return BMMC_ERR_UNSUPPORTED_ELEM;
+    const bool quantised = a->cache_type == BMMC_E4M3 || a->cache_type == BMMC_I8;
+    if (!quantised && a->cache_type != type) return BMMC_ERR_UNSUPPORTED_ELEM;
+    const int cs = quantised ? 1 : es;
+    if (!a->tokens) return BMMC_OK;
+    if (a->sequences < 0 || a->sequences > kMaxTokens || !a->starts || (a->sequences && a->table_columns && !a->table) ||
+        a->table_columns < 0 || a->table_columns > kMaxTokens || bad_stride(a->table_stride, a->sequences) || a->pages < 0 ||
+        a->pages > kMaxTokens || a->page_size < 1 || a->page_size > kMaxTokens || a->k.heads != a->v.heads)
+        return BMMC_ERR_INVALID_ARG;
+    if ((uintptr_t)a->starts % 4 || (uintptr_t)a->firsts % 4 || (uintptr_t)a->table % 4) return BMMC_ERR_MISALIGNED;
+    const token_heads_t* to[2] = {&a->k, &a->v};
+    const paged_cache_t *cache[2] = {&a->k_cache, &a->v_cache}, *scale[2] = {&a->k_scales, &a->v_scales};
+    ReadParams rp{};
+    MoveParams& p = rp.p;
+    Rows in[7] = {}, out[2];
+    uint64_t cache_bits = 0, out_bits = 0;
+    bmmc_status s;
+    for (int i = 0; i < 2; ++i) {
+        if ((s = check_heads(*to[i], a->tokens, es)) != BMMC_OK) return s;
+        if (!writable(*to[i], a->tokens)) return BMMC_ERR_INVALID_ARG;
+        // (a cache that is only read may hold an entry's elements at one address)
+        const paged_cache_t& m = *cache[i];
+        if ((!m.data && a->pages) || bad_stride(m.page_stride, a->pages) || bad_stride(m.slot_stride, a->page_size) ||
+            bad_stride(m.head_stride, to[i]->heads))
+            return BMMC_ERR_INVALID_ARG;
+        if ((uintptr_t)m.data % cs) return BMMC_ERR_MISALIGNED;
+        out[i] = rows_of(*to[i], a->tokens, es);
+        in[i] = cache_rows(m, a->pages, a->page_size, to[i]->heads, to[i]->dim, cs);
+        if (quantised) {
+            const paged_cache_t& x = *scale[i];
+            if ((!x.data && a->pages) || bad_stride(x.page_stride, a->pages) || bad_stride(x.slot_stride, a->page_size) ||
+                bad_stride(x.head_stride, to[i]->heads))
+                return BMMC_ERR_INVALID_ARG;
+            if ((uintptr_t)x.data % 4) return BMMC_ERR_MISALIGNED;
+            rp.scales[i] = Scales{static_cast<char*>(x.data), x.page_stride * 4, x.slot_stride * 4, x.head_stride * 4};
+            in[2 + i] = cache_rows(x, a->pages, a->page_size, to[i]->heads, 1, 4);
+        } else if (scale[i]->data) {
+            return BMMC_ERR_INVALID_ARG;
+        }
+        Heads& h = p.part[i];
+        h.src = static_cast<const char*>(m.data);
+        h.src_head = m.head_stride * cs;
+        h.dst = static_cast<char*>(to[i]->data);
+        h.dst_token = to[i]->token_stride * es;
+        h.dst_head = to[i]->head_stride * es;
+        h.heads = (int)to[i]->heads;
+        p.page_stride[i] = m.page_stride * cs;
+        p.slot_stride[i] = m.slot_stride * cs;
+        rp.dims[i] = (int)to[i]->dim;
+        cache_bits |= (uint64_t)(uintptr_t)m.data | (uint64_t)p.page_stride[i] | (uint64_t)p.slot_stride[i] | (uint64_t)h.src_head;
+        out_bits |= address_bits(*to[i], es);
+    }
+    in[4] = Rows{a->starts, 1, 0, (a->sequences + 1) * 4};
+    in[5] = Rows{a->firsts, 1, 0, a->sequences * 4};
+    in[6] = Rows{a->table, a->sequences, a->table_stride * 4, a->table_columns * 4};
+    for (const Rows& r : in)
+        if (may_overlap(r, out[0]) || may_overlap(r, out[1])) return BMMC_ERR_ALIAS;
+    if (may_overlap(out[0], out[1]) && !heads_between(a->k, a->v, a->tokens, es)) return BMMC_ERR_ALIAS;
+    if ((s = all_reachable(device, {a->k.data, a->v.data, a->k_cache.data, a->v_cache.data, a->k_scales.data, a->v_scales.data,
+                                    a->starts, a->firsts, a->table})) != BMMC_OK)
+        return s;
+    p.parts = 2;
+    p.device = device;
+    p.tokens = a->tokens;
+    p.starts = a->starts;
+    p.lengths = a->firsts;
+    p.table = a->table;
+    p.sequences = a->sequences;
+    p.table_stride = a->table_stride;
+    p.table_columns = a->table_columns;
+    p.pages = a->pages;
+    p.page_size = (int)a->page_size;
+    const chk::Spans spans = spans_of({in[0], in[1], in[2], in[3], in[4], in[5], in[6]}, {out[0], out[1]});
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (quantised)
+        return by_cache_type(type, a->cache_type,
+                             [&](auto t, auto q) { return launch_read<decltype(t), decltype(q)>(rp, spans, st); });
+    // (values of the result's own type are only moved)
+    return es == 4 ? launch_read<float, void>(rp, spans, st) : launch_read<__half, void>(rp, spans, st);
+}
+
+}  // extern "C"
+
+namespace bmmc {
+cudaError_t bounds_record_paged_cache8(unsigned long long out[chk::kRecordWords], bool clear) {
+    return chk::read_record(out, clear);
+}
+}  // namespace bmmc

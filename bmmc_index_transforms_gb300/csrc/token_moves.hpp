@@ -1,13 +1,17 @@
 // Host-side checks shared by the entry points that move tokens by maps held
-// on the device (experts.cu, rotary.cu).  Each includes bounds.cuh before this
+// on the device (experts.cu, rotary.cu, paged_cache8.cu, embedding.cu,
+// balance.cu).  Each includes bounds.cuh before this
 // header.
 #pragma once
 
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
 #include <initializer_list>
+#include <type_traits>
 
 #include "../../include/bmmc.h"
 #include "launch.hpp"
@@ -165,5 +169,71 @@ bmmc_status launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cud
     cudaGetLastError();
     return BMMC_ERR_CUDA;
 }
+
+// How the words of the tokens' rows are dealt out: blocks of x * y threads
+// take y tokens and x words of each; gridDim.y parts make up a row.
+struct Cover {
+    dim3 grid, block;
+};
+
+constexpr int kMostParts = 65535;
+
+// Up to this many words (one for every thread of the machine) the blocks are
+// smaller, so that more of the machine takes part.
+constexpr int64_t kFewWords = kSms * 2048;
+
+inline Cover cover(int64_t tokens, int words, int most) {
+    // a grid has 65535 parts at most: rows of 2^24 elements are up to 2^23 words
+    while ((words + most - 1) / most > kMostParts) most <<= 1;
+    const int parts = (words + most - 1) / most, need = (words + parts - 1) / parts;
+    int x = 4;
+    while (x < 32 && x < need) x <<= 1;
+    if (x < need) x = (need + 31) / 32 * 32;
+    const int y = x >= most ? 1 : most / x;
+    Cover c;
+    c.block = dim3(x, y);
+    c.grid = dim3((unsigned)((tokens + y - 1) / y), (unsigned)((words + x - 1) / x));
+    return c;
+}
+
+// How rows of `hidden` elements are walked: in words of 16 or 8 bytes where
+// all addresses, strides and lengths (or'ed into `bits`, in bytes) are
+// multiples of them, else across the words' bounds.
+struct Way {
+    int bytes;   // 16, 8 or 0: across
+    int words;   // of a row; across: at most
+};
+
+inline Way way_of(int64_t hidden, int es, std::initializer_list<uint64_t> bits) {
+    const int wb = word_bytes(es, bits);
+    if (wb >= 8) return {wb, (int)(hidden * es / wb)};
+    const int W = 16 / es;
+    return {0, (int)((hidden + 2 * (W - 1)) / W)};
+}
+
+// Calls f(T{}, elements per word, across).
+template <class T, class F>
+void by_way(const Way& way, F&& f) {
+    constexpr int es = sizeof(T);
+    if (way.bytes == 16) f(T{}, std::integral_constant<int, 16 / es>{}, std::false_type{});
+    else if (way.bytes == 8) f(T{}, std::integral_constant<int, 8 / es>{}, std::false_type{});
+    else f(T{}, std::integral_constant<int, 16 / es>{}, std::true_type{});
+}
+
+template <class F>
+void by_type(int type, const Way& way, F&& f) {
+    switch (type) {
+        case BMMC_F32: by_way<float>(way, f); break;
+        case BMMC_F16: by_way<__half>(way, f); break;
+        default: by_way<__nv_bfloat16>(way, f); break;
+    }
+}
+
+// Rows that are written lie apart.
+inline bool bad_output_stride(int64_t stride, int64_t hidden, int64_t rows) {
+    return bad_stride(stride, rows) || (rows > 1 && stride < hidden);
+}
+
+inline bool misaligned(const void* p, size_t bytes) { return (uintptr_t)p & (bytes - 1); }
 
 }  // namespace bmmc

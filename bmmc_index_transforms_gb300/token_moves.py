@@ -1,5 +1,5 @@
-"""Moves of tokens by maps held on the device, on torch tensors: by expert
-and back, and into the pages of a cache.
+"""Moves of tokens by maps held on the device, on torch tensors: out of a table
+of rows and back, by expert and back, and into the pages of a cache and back.
 
 Argument marshalling for the entry points of the same names in
 ``include/bmmc.h``: tensors become pointers, sizes and strides, and outputs
@@ -28,12 +28,14 @@ import ctypes
 from . import _capi
 from ._streams import empty_on
 
-__all__ = ["expert_sort", "expert_dispatch", "expert_combine", "expert_combine_backward", "rotary", "paged_append"]
+__all__ = ["expert_sort", "expert_dispatch", "expert_combine", "expert_combine_backward", "expert_balance",
+           "expert_balance_backward", "embedding_lookup", "embedding_backward", "rotary", "paged_append", "paged_read"]
 
 _torch = _empty = _library = _raw_stream = _current_device = _int32 = _int64 = _float32 = None
 _types = {}       # torch dtype -> bmmc_dtype, with the flag of device pointers
 _widths = {}      # integer torch dtype -> its bytes
-_workspaces = {}  # (tokens, choices, experts) -> bytes that expert_sort asks for
+_cache_types = {}  # torch dtype of 8 bits -> bmmc_dtype
+_workspaces = {}  # (tokens, choices, experts) -> bytes that expert_sort asks for; (name, *sizes) -> those of other calls
 _DEVICE = _capi.DEVICE_POINTERS
 _F32 = _capi.F32 | _DEVICE
 
@@ -44,6 +46,7 @@ def _setup():
     import torch
 
     _types.update({torch.float32: _F32, torch.float16: _capi.F16 | _DEVICE, torch.bfloat16: _capi.BF16 | _DEVICE})
+    _cache_types.update({torch.float8_e4m3fn: _capi.E4M3, torch.int8: _capi.I8})
     _int32, _int64, _float32 = torch.int32, torch.int64, torch.float32
     _widths.update({_int32: 4, _int64: 8})
     _empty, _current_device = torch.empty, torch.cuda.current_device
@@ -251,6 +254,167 @@ def expert_combine_backward(grad, rows, slot, weights, stream=None):
     return grad_rows, grad_weights
 
 
+def _workspace(name: str, where: str, *sizes) -> int:
+    """The bytes of workspace that a call of these sizes asks for."""
+    need = _workspaces.get((name, *sizes))
+    if need is None:
+        size = ctypes.c_size_t()
+        _check(getattr(_library, name)(*sizes, size), where)
+        if len(_workspaces) > 1000:
+            _workspaces.clear()
+        need = _workspaces[(name, *sizes)] = size.value
+    return need
+
+
+def _router(logits, experts, where: str):
+    """Tokens, choices, experts, the logits' stride and type, the width of the
+    choices' ids."""
+    T, E, stride = _matrix(logits, where, "logits")
+    t = _types.get(logits.dtype)
+    if t is None:
+        _no_type(logits, where, "logits")
+    width = _widths.get(experts.dtype)
+    if width is None or experts.dim() != 2 or not experts.is_contiguous() or experts.shape[0] != T:
+        _no(where, f"experts must be a contiguous int32 or int64 tensor [{T}, choices]")
+    return T, experts.shape[1], E, stride, t, width
+
+
+def expert_balance(logits, experts, stream=None):
+    """(loss, counts) of a router's logits [tokens, num_experts] and its
+    choices ``experts`` [tokens, choices] (int32 or int64; ids outside [0,
+    num_experts) are not routed).
+
+    ``counts`` [num_experts + 1]: each expert's routed choices and, behind
+    them, the number of tokens that have any.  ``loss`` (float32, 0-D):
+    num_experts times the sum over the experts of their share of the choices
+    times their mean share of the softmax, over those tokens; 1 where all are
+    chosen alike."""
+    if _torch is None:
+        _setup()
+    where = "expert_balance"
+    T, K, E, stride, t, width = _router(logits, experts, where)
+    st = _stream(logits.get_device(), stream, where, experts)
+    need = _workspace("expert_balance_workspace", where, T, K, E)
+    device = logits.device
+    empty = _empty if stream is None else _empty_there(stream, st)
+    loss = empty((), dtype=_float32, device=device)
+    counts = empty(E + 1, dtype=_int32, device=device)
+    work = empty(need // 4, dtype=_int32, device=device)
+    status = _library.expert_balance(logits.data_ptr(), stride, t, experts.data_ptr(), width, T, K, E, loss.data_ptr(),
+                                     counts.data_ptr(), work.data_ptr(), need, st)
+    if status:
+        _check(status, where)
+    return loss, counts
+
+
+def expert_balance_backward(grad, logits, experts, counts, out=None, stream=None):
+    """The gradient of expert_balance's loss by the logits, from the gradient
+    ``grad`` (float32, one element) by the loss and the counts it gave."""
+    if _torch is None:
+        _setup()
+    where = "expert_balance_backward"
+    T, K, E, stride, t, width = _router(logits, experts, where)
+    if grad.dtype is not _float32 or grad.numel() != 1:
+        _no(where, "grad must be a float32 tensor of one element")
+    if counts.dtype is not _int32 or counts.shape != (E + 1,) or not counts.is_contiguous():
+        _no(where, f"counts must be a contiguous int32 tensor [{E + 1}]")
+    st = _stream(logits.get_device(), stream, where, grad, experts, counts, out)
+    if out is None:
+        empty = _empty if stream is None else _empty_there(stream, st)
+        out, out_stride = empty((T, E), dtype=logits.dtype, device=logits.device), E
+    else:
+        out_stride = _output(out, T, E, logits, where)
+    status = _library.expert_balance_backward(grad.data_ptr(), logits.data_ptr(), stride, t, experts.data_ptr(), width, T,
+                                              K, E, counts.data_ptr(), out.data_ptr(), out_stride, st)
+    if status:
+        _check(status, where)
+    return out
+
+
+def _ids(ids, where: str) -> int:
+    width = _widths.get(ids.dtype)
+    if width is None or ids.dim() != 1 or not ids.is_contiguous():
+        _no(where, "ids must be a contiguous int32 or int64 tensor [tokens]")
+    return width
+
+
+def embedding_lookup(table, ids, scale: float = 1.0, out=None, stream=None):
+    """out[t] = scale * table[ids[t]], rounded once; zero where ids[t] (int32
+    or int64) names no row of the table [rows, hidden]."""
+    if _torch is None:
+        _setup()
+    where = "embedding_lookup"
+    width = _ids(ids, where)
+    V, H, stride = _matrix(table, where, "table")
+    t = _types.get(table.dtype)
+    if t is None:
+        _no_type(table, where, "table")
+    T = ids.shape[0]
+    st = _stream(table.get_device(), stream, where, ids, out)
+    if out is None:
+        empty = _empty if stream is None else _empty_there(stream, st)
+        out, out_stride = empty((T, H), dtype=table.dtype, device=table.device), H
+    else:
+        out_stride = _output(out, T, H, table, where)
+    status = _library.embedding_lookup(table.data_ptr(), stride, V, ids.data_ptr(), width, T, H, t, scale, out.data_ptr(),
+                                       out_stride, st)
+    if status:
+        _check(status, where)
+    return out
+
+
+def embedding_backward(grad, ids, num_rows=None, *, scale: float = 1.0, dtype=None, out=None, accumulate: bool = False,
+                       stream=None):
+    """The gradient of embedding_lookup by its table: row v is scale times the
+    sum of the rows of grad [tokens, hidden] with ids[t] = v, held in 32 bits
+    and rounded once.
+
+    Without ``out``: a new tensor [num_rows, hidden] of ``dtype`` (float32 or
+    grad's type, which is the default), rows without a token zero.  With it,
+    the same written there or, with ``accumulate``, added to it; rows without
+    a token are then left as they are."""
+    if _torch is None:
+        _setup()
+    where = "embedding_backward"
+    width = _ids(ids, where)
+    T, H, stride = _matrix(grad, where, "grad")
+    t = _types.get(grad.dtype)
+    if t is None:
+        _no_type(grad, where, "grad")
+    if ids.shape[0] != T:
+        _no(where, f"grad has {T} rows for {ids.shape[0]} ids")
+    st = _stream(grad.get_device(), stream, where, ids, out)
+    device = grad.device
+    empty = _empty if stream is None else _empty_there(stream, st)
+    if out is None:
+        if accumulate or num_rows is None:
+            _no(where, "accumulate needs out" if accumulate else "num_rows or out is needed")
+        out_type = grad.dtype if dtype is None else dtype
+        if out_type is not _float32 and out_type != grad.dtype:
+            _no(where, "dtype must be float32 or grad's type")
+        V = int(num_rows)
+        if V < 0:
+            _no(where, f"num_rows {V} is negative")
+        out, out_stride = empty((V, H), dtype=out_type, device=device), H
+    else:
+        V, cols, out_stride = _matrix(out, where, "out")
+        out_type = out.dtype
+        if cols != H or (num_rows is not None and V != num_rows):
+            _no(where, f"out has shape {tuple(out.shape)}, expected ({V if num_rows is None else num_rows}, {H})")
+        if (out_type is not _float32 and out_type != grad.dtype) or (dtype is not None and dtype != out_type):
+            _no(where, f"out has type {out_type}")
+    need = _workspace("embedding_backward_workspace", where, T, V, H)
+    work_ptr = None
+    if need:
+        work = empty(need // 4, dtype=_int32, device=device)
+        work_ptr = work.data_ptr()
+    status = _library.embedding_backward(grad.data_ptr(), stride, ids.data_ptr(), width, T, H, t, scale, int(accumulate),
+                                         out.data_ptr(), out_stride, V, _types[out_type] & ~_DEVICE, work_ptr, need, st)
+    if status:
+        _check(status, where)
+    return out
+
+
 def _heads(x, where: str, name: str):
     """token_heads_t of a tensor [tokens, heads, dim] with dense heads, and
     its tokens."""
@@ -338,9 +502,10 @@ def rotary(x, positions, inv_freq, pair_axes=None, *, interleaved: bool = False,
 
 
 def _cache(c, X, dtype, head_major: bool, where: str, name: str):
-    """(pages, page_size) and paged_cache_t of a cache."""
+    """(pages, page_size) and paged_cache_t of a cache for heads X."""
     if c.dim() != 4 or c.dtype != dtype:
-        _no(where, f"{name} must be 4-D of k's type with dense heads")
+        _no(where, f"{name} must be 4-D of k's type with dense heads" if dtype in _types else
+                   f"{name} must be 4-D of type {dtype} with dense heads")
     (pages, page, heads, dim), (page_stride, slot_stride, head_stride, inner) = c.shape, c.stride()
     if inner != 1 and dim > 1:
         _no(where, f"{name} must be 4-D of k's type with dense heads")
@@ -351,8 +516,28 @@ def _cache(c, X, dtype, head_major: bool, where: str, name: str):
     return (pages, page), (c.data_ptr(), page_stride, slot_stride, head_stride)
 
 
+def _cache_scales(s, geometry, heads: int, head_major: bool, where: str, name: str):
+    """paged_cache_t of a cache's scales."""
+    pages, page = geometry
+    shape = (pages, heads, page) if head_major else (pages, page, heads)
+    if s is None or s.dtype is not _float32 or s.shape != shape:
+        _no(where, f"a cache of 8 bits needs {name}, a float32 tensor {shape}")
+    page_stride, slot_stride, head_stride = s.stride()
+    if head_major:
+        slot_stride, head_stride = head_stride, slot_stride
+    return s.data_ptr(), page_stride, slot_stride, head_stride
+
+
+def _table(page_table, where: str):
+    B, columns, stride = _matrix(page_table, where, "page_table")
+    if page_table.dtype is not _int32:
+        _no(where, "page_table must be an int32 tensor [sequences, columns]")
+    return B, columns, stride
+
+
 def paged_append(k, v, k_cache, v_cache, page_table, lengths, *, starts=None, q=None, q_out=None, positions=None,
-                 inv_freq=None, pair_axes=None, interleaved: bool = False, head_major: bool = False, stream=None):
+                 inv_freq=None, pair_axes=None, interleaved: bool = False, head_major: bool = False, k_scales=None,
+                 v_scales=None, stream=None):
     """Append new keys and values [tokens, kv_heads, dim] to a paged cache,
     the keys turned on the way as by rotary (without inv_freq: as they are).
 
@@ -364,7 +549,12 @@ def paged_append(k, v, k_cache, v_cache, page_table, lengths, *, starts=None, q=
     negative entry, or beyond the table) or outside every sequence are not
     written.  Without positions a token's position is its entry's number.
     Returns the queries q [tokens, q_heads, dim] turned alike (in q_out, which
-    may be q), or None without q.  lengths is left as it is."""
+    may be q), or None without q.  lengths is left as it is.
+
+    Caches of 8 bits (float8_e4m3fn or int8) come with k_scales and v_scales,
+    float32 [pages, page_size, kv_heads], or [pages, kv_heads, page_size] if
+    head_major, of any strides: a head is written as values times a scale, its
+    largest element over the type's (448 or 127).  paged_read reads them back."""
     if _torch is None:
         _setup()
     where = "paged_append"
@@ -376,13 +566,18 @@ def paged_append(k, v, k_cache, v_cache, page_table, lengths, *, starts=None, q=
     V = _alike(v, T, dtype, where, "v")
     if K[1] != V[1]:
         _no(where, "k and v must have the same heads")
-    geometry, k_at = _cache(k_cache, K, dtype, head_major, where, "k_cache")
-    other, v_at = _cache(v_cache, V, dtype, head_major, where, "v_cache")
+    cache_type = _cache_types.get(k_cache.dtype)
+    cache_dtype = dtype if cache_type is None else k_cache.dtype
+    geometry, k_at = _cache(k_cache, K, cache_dtype, head_major, where, "k_cache")
+    other, v_at = _cache(v_cache, V, cache_dtype, head_major, where, "v_cache")
     if geometry != other:
         _no(where, f"v_cache has shape {tuple(v_cache.shape)}, which does not fit k_cache's pages")
-    B, columns, table_stride = _matrix(page_table, where, "page_table")
-    if page_table.dtype is not _int32:
-        _no(where, "page_table must be an int32 tensor [sequences, columns]")
+    if cache_type is not None:
+        scales = (*_cache_scales(k_scales, geometry, K[1], head_major, where, "k_scales"),
+                  *_cache_scales(v_scales, geometry, V[1], head_major, where, "v_scales"))
+    elif k_scales is not None or v_scales is not None:
+        _no(where, "scales are of caches of 8 bits")
+    B, columns, table_stride = _table(page_table, where)
     if lengths.dtype is not _int32 or lengths.shape != (B,) or not lengths.is_contiguous():
         _no(where, "lengths must be a contiguous int32 tensor [sequences]")
     starts_ptr = 0
@@ -395,16 +590,86 @@ def paged_append(k, v, k_cache, v_cache, page_table, lengths, *, starts=None, q=
         starts_ptr = starts.data_ptr()
     turns = _turns(T, positions, inv_freq, pair_axes, _capi.ROTARY_ADJACENT if interleaved else 0, where)
     st = _stream(k.get_device(), stream, where, v, k_cache, v_cache, page_table, lengths, starts, q, q_out, positions,
-                 inv_freq, pair_axes)
+                 inv_freq, pair_axes, k_scales, v_scales)
     Q = O = _NO_HEADS
     if q is not None:
         Q = _alike(q, T, dtype, where, "q")
         q_out, O = _turned_output(q, Q, q_out, T, stream, st, where, "q_out")
     elif q_out is not None:
         _no(where, "q_out without q")
-    status = _library.paged_append(_capi.PAGED_APPEND_ARGS.pack(
-        T, t, *K, *V, *Q, *O, *turns, starts_ptr, lengths.data_ptr(), B, page_table.data_ptr(), table_stride, columns,
-        *geometry, *k_at, *v_at), st)
+    args = (T, t, *K, *V, *Q, *O, *turns, starts_ptr, lengths.data_ptr(), B, page_table.data_ptr(), table_stride, columns,
+            *geometry, *k_at, *v_at)
+    if cache_type is None:
+        status = _library.paged_append(_capi.PAGED_APPEND_ARGS.pack(*args), st)
+    else:
+        status = _library.paged_append_quantised(_capi.PAGED_APPEND_QUANTISED_ARGS.pack(*args, cache_type, *scales), st)
     if status:
         _check(status, where)
     return q_out
+
+
+def paged_read(k_cache, v_cache, page_table, starts, num_rows=None, *, firsts=None, k_scales=None, v_scales=None,
+               dtype=None, k_out=None, v_out=None, head_major: bool = False, stream=None):
+    """(k, v) [num_rows, kv_heads, dim]: the entries of paged caches in the
+    order of the sequences.
+
+    Caches, table and scales are as for paged_append.  Row starts[b] + j
+    receives sequence b's entry firsts[b] + j (without firsts: j), up to row
+    starts[b + 1] - 1; zeros where a row belongs to no sequence or its entry
+    has no page.  The result is of the caches' type or, from caches of 8 bits,
+    of ``dtype`` (or that of k_out and v_out, where they are given)."""
+    if _torch is None:
+        _setup()
+    where = "paged_read"
+    cache_type = _cache_types.get(k_cache.dtype)
+    if k_cache.dim() != 4 or v_cache.dim() != 4:
+        _no(where, "the caches must be 4-D")
+    out_dtype = dtype if dtype is not None else k_out.dtype if k_out is not None else k_cache.dtype
+    t = _types.get(out_dtype)
+    if t is None or (cache_type is None and out_dtype != k_cache.dtype):
+        _no(where, f"caches of {k_cache.dtype} are read back as "
+                   f"{k_cache.dtype if cache_type is None else 'the float32, float16 or bfloat16 that dtype says'}")
+    if num_rows is None:
+        if k_out is None:
+            _no(where, "num_rows or k_out is needed")
+        num_rows = k_out.shape[0]
+    heads = k_cache.shape[1 if head_major else 2]
+    B, columns, table_stride = _table(page_table, where)
+    if starts.dtype is not _int32 or starts.shape != (B + 1,) or not starts.is_contiguous():
+        _no(where, "starts must be a contiguous int32 tensor [sequences + 1]")
+    firsts_ptr = 0
+    if firsts is not None:
+        if firsts.dtype is not _int32 or firsts.shape != (B,) or not firsts.is_contiguous():
+            _no(where, "firsts must be a contiguous int32 tensor [sequences]")
+        firsts_ptr = firsts.data_ptr()
+    st = _stream(k_cache.get_device(), stream, where, v_cache, page_table, starts, firsts, k_scales, v_scales, k_out, v_out)
+    empty = _empty if stream is None else _empty_there(stream, st)
+    outs, at = [], []
+    for out, c, name in ((k_out, k_cache, "k_out"), (v_out, v_cache, "v_out")):
+        dim = c.shape[3]
+        if out is None:
+            out = empty((num_rows, heads, dim), dtype=out_dtype, device=k_cache.device)
+            at.append((out.data_ptr(), heads, dim, heads * dim, dim))
+        else:
+            h, n = _heads(out, where, name)
+            if n != num_rows or h[1] != heads or h[2] != dim or out.dtype != out_dtype:
+                _no(where, f"{name} must be of type {out_dtype} and shape ({num_rows}, {heads}, {dim})")
+            at.append(h)
+        outs.append(out)
+    geometry, k_at = _cache(k_cache, at[0], k_cache.dtype, head_major, where, "k_cache")
+    other, v_at = _cache(v_cache, at[1], k_cache.dtype, head_major, where, "v_cache")
+    if geometry != other:
+        _no(where, f"v_cache has shape {tuple(v_cache.shape)}, which does not fit k_cache's pages")
+    if cache_type is not None:
+        scales = (*_cache_scales(k_scales, geometry, heads, head_major, where, "k_scales"),
+                  *_cache_scales(v_scales, geometry, heads, head_major, where, "v_scales"))
+    else:
+        if k_scales is not None or v_scales is not None:
+            _no(where, "scales are of caches of 8 bits")
+        cache_type, scales = t & ~_DEVICE, (0, 0, 0, 0, 0, 0, 0, 0)
+    status = _library.paged_read(_capi.PAGED_READ_ARGS.pack(
+        num_rows, t, cache_type, *at[0], *at[1], starts.data_ptr(), firsts_ptr, B, page_table.data_ptr(), table_stride,
+        columns, *geometry, *k_at, *v_at, *scales), st)
+    if status:
+        _check(status, where)
+    return outs[0], outs[1]

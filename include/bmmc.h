@@ -559,7 +559,10 @@ bmmc_status bmmc_copy(const void *in, void *out, size_t bytes, void *stream);
 typedef enum {
     BMMC_F32 = 0,
     BMMC_F16 = 1,
-    BMMC_BF16 = 2
+    BMMC_BF16 = 2,
+    BMMC_E4M3 = 3, /* 8 bits, of paged caches only: floating point with 4 bits of exponent and
+                      3 behind the leading one, up to 448 */
+    BMMC_I8 = 4    /* 8 bits, of paged caches only: whole numbers from -127 to 127 */
 } bmmc_dtype;
 
 /* Or'ed into `type` (into `id_bytes` of expert_sort): the caller has made sure
@@ -618,6 +621,54 @@ bmmc_status expert_combine_backward(const void *grad, int64_t grad_stride, const
                                     const void *weights, int weight_type, int64_t tokens,
                                     int choices, int64_t hidden, int type, void *grad_rows,
                                     int64_t grad_row_stride, void *grad_weights, void *stream);
+
+/* A router's balance loss, with the number of choices of each expert.  With
+ * p[t] the softmax of token t's logits (logits[t * stride + e], e < experts, of
+ * `type`), over the tokens with a routed choice (ids as for expert_sort), n of
+ * them, c[e] the routed choices of expert e and C their sum:
+ *   *loss     = experts * sum over e of (c[e] / C) * (sum over t of p[t][e]) / n,
+ *               1 where all experts are chosen alike; 0 where no choice is routed;
+ *   counts[e] = c[e], e < experts; counts[experts] = n.
+ * Logits of other tokens are not looked at.  An expert with the logit -inf has
+ * the share 0, also in a row of nothing else.  workspace: what
+ * expert_balance_workspace asks for (host only), free to reuse once the call's
+ * work is done. */
+bmmc_status expert_balance_workspace(int64_t tokens, int choices, int experts, size_t *bytes);
+bmmc_status expert_balance(const void *logits, int64_t stride, int type, const void *ids,
+                           int id_bytes, int64_t tokens, int choices, int experts, float *loss,
+                           int32_t *counts, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/* Its gradient, from *grad = the gradient by the loss and the counts that
+ * expert_balance gave for the same ids:
+ *   grad_logits[t][e] = *grad * experts / n * p[t][e] * (f[e] - sum over j of f[j] * p[t][j])
+ * with f[e] = c[e] / C; zero for tokens without a routed choice. */
+bmmc_status expert_balance_backward(const float *grad, const void *logits, int64_t stride, int type,
+                                    const void *ids, int id_bytes, int64_t tokens, int choices,
+                                    int experts, const int32_t *counts, void *grad_logits,
+                                    int64_t grad_stride, void *stream);
+
+/* out[t] = scale * table[ids[t]], a product in 32 bits, rounded once; a row of
+ * zeros where ids[t] (dense, id_bytes 4 or 8, signed) is outside [0, vocab). */
+bmmc_status embedding_lookup(const void *table, int64_t table_stride, int64_t vocab,
+                             const void *ids, int id_bytes, int64_t tokens, int64_t hidden,
+                             int type, float scale, void *out, int64_t out_stride, void *stream);
+
+/* The gradient of embedding_lookup by the table, from grad = the gradient by
+ * its result:
+ *   out[v] = scale * sum over the tokens t with ids[t] = v of grad[t],
+ * rows without a token zero; or, with accumulate, added to what out[v] holds,
+ * rows without a token left as they are.  out is of out_type, BMMC_F32 or
+ * `type`; sums (and what is added to) are held in 32 bits, in an order that
+ * depends on the ids only.  workspace: what embedding_backward_workspace asks
+ * for (host only), 16-byte aligned, free to reuse once the call's work is done. */
+bmmc_status embedding_backward_workspace(int64_t tokens, int64_t vocab, int64_t hidden,
+                                         size_t *bytes);
+bmmc_status embedding_backward(const void *grad, int64_t grad_stride, const void *ids,
+                               int id_bytes, int64_t tokens, int64_t hidden, int type, float scale,
+                               int accumulate, void *out, int64_t out_stride, int64_t vocab,
+                               int out_type, void *workspace, size_t workspace_bytes,
+                               void *stream);
 
 /* Heads of tokens: element d of head h of token t at
  * data[t * token_stride + h * head_stride + d]. */
@@ -688,6 +739,44 @@ typedef struct {
  * must not name the same entry of a page for their new tokens. */
 bmmc_status paged_append(const paged_append_args_t *args, void *stream);
 
+/* The same into caches of 8 bits, with a scale for each head of each entry. */
+typedef struct {
+    paged_append_args_t append;        /* the caches' strides in bytes, which are their elements */
+    int64_t cache_type;                /* BMMC_E4M3 or BMMC_I8 */
+    paged_cache_t k_scales, v_scales;  /* floats, [pages][page_size][heads] in any order of strides:
+                                          the scale of a head at data[p * page_stride + slot *
+                                          slot_stride + h * head_stride] */
+} paged_append_quantised_args_t;
+
+/* Append to caches of 8 bits: a head y (keys turned; 32 bits) has the scale
+ *   s = max |y| * (1 / M), at least 2^-126,   M = 448 (BMMC_E4M3) or 127 (BMMC_I8),
+ * and its elements are held as y * (1 / s) rounded to the nearest value of the
+ * cache's type, ties to even, at most M in magnitude; each product and
+ * quotient is rounded to 32 bits.  A head that holds an infinity or a NaN has
+ * the scale NaN, and reads back as NaN throughout. */
+bmmc_status paged_append_quantised(const paged_append_quantised_args_t *args, void *stream);
+
+typedef struct {
+    int64_t tokens, type;
+    int64_t cache_type;          /* `type`, or BMMC_E4M3 or BMMC_I8 */
+    token_heads_t k, v;          /* results, the same heads */
+    const int32_t *starts;       /* [sequences + 1]: sequence b's entries go to rows starts[b] ..
+                                    starts[b+1]-1 */
+    const int32_t *firsts;       /* [sequences]: the entry in sequence b's first row; NULL: 0 */
+    int64_t sequences;
+    const int32_t *table;        /* as for paged_append */
+    int64_t table_stride, table_columns, pages, page_size;
+    paged_cache_t k_cache, v_cache;
+    paged_cache_t k_scales, v_scales; /* of caches of 8 bits; else data NULL */
+} paged_read_args_t;
+
+/* Read back: row starts[b] + j of k and v receives entry firsts[b] + j of
+ * sequence b from its page, as it is or, from a cache of 8 bits, times its
+ * head's scale, a product in 32 bits, rounded once.  Every row is written: with zeros
+ * where it belongs to no sequence (outside starts) or its entry has no page
+ * (beyond the table, or a page outside [0, pages)).  Sequences may share pages. */
+bmmc_status paged_read(const paged_read_args_t *args, void *stream);
+
 /* ---- Bounds-checked builds --------------------------------------------------
  * A debugging build of the library (every source compiled with
  * -DBMMC_BOUNDS_CHECK) makes each global and shared-memory access of every
@@ -707,7 +796,8 @@ typedef struct {
     int site;           /* first failure: source file tag * 100000 + line
                            (tag 1: kernels.cu, 2: lmad.cu, 3: lmad_transpose_1_2.cu,
                            4: lmad_transpose_4_8_16.cu, 5: lmad_block.cu,
-                           6: experts.cu, 7: rotary.cu) */
+                           6: experts.cu, 7: rotary.cu, 8: embedding.cu,
+                           9: balance.cu, 10: paged_cache8.cu) */
     int bytes;          /* its access size */
     uint64_t address;   /* its address (a shared-memory offset for shared accesses) */
     uint64_t lo, hi;    /* the range [lo, hi) it was tested against */
