@@ -154,20 +154,27 @@ inline bmmc_status all_reachable(bool device, std::initializer_list<const void*>
     return BMMC_OK;
 }
 
-// Launch a kernel, with one attribute or none.
+// Launch a kernel with some attributes.
 template <class... P, class... A>
-bmmc_status launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                   cudaLaunchAttribute* attribute, const A&... args) {
+bmmc_status launch_with(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                        cudaLaunchAttribute* attributes, unsigned count, const A&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cfg.attrs = attribute;
-    cfg.numAttrs = attribute ? 1 : 0;
+    cfg.attrs = attributes;
+    cfg.numAttrs = count;
     if (cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess) return BMMC_OK;
     cudaGetLastError();
     return BMMC_ERR_CUDA;
+}
+
+// The same with one attribute or none.
+template <class... P, class... A>
+bmmc_status launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                   cudaLaunchAttribute* attribute, const A&... args) {
+    return launch_with(kernel, grid, block, smem, st, attribute, attribute ? 1 : 0, args...);
 }
 
 // How the words of the tokens' rows are dealt out: blocks of x * y threads

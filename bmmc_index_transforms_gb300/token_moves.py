@@ -299,9 +299,12 @@ def expert_balance(logits, experts, stream=None):
     empty = _empty if stream is None else _empty_there(stream, st)
     loss = empty((), dtype=_float32, device=device)
     counts = empty(E + 1, dtype=_int32, device=device)
-    work = empty(need // 4, dtype=_int32, device=device)
+    work_ptr = None
+    if need:
+        work = empty(need // 4, dtype=_int32, device=device)
+        work_ptr = work.data_ptr()
     status = _library.expert_balance(logits.data_ptr(), stride, t, experts.data_ptr(), width, T, K, E, loss.data_ptr(),
-                                     counts.data_ptr(), work.data_ptr(), need, st)
+                                     counts.data_ptr(), work_ptr, need, st)
     if status:
         _check(status, where)
     return loss, counts
