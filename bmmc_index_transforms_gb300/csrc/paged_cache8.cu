@@ -25,11 +25,16 @@ namespace {
 
 constexpr int kThreads = 128, kWarps = kThreads / 32;
 
-// The 8-bit types: the factor 1 / M of a scale, a value and what it stands for.
+// The 8-bit types: the factor 1 / M of a scale, two values side by side, and
+// what a value stands for.  What is encoded is at most M * (1 + 2^-22) in
+// magnitude (the three roundings of y * (1 / (max * (1 / M))) are 2^-24 each),
+// which rounds to M; or NaN, which becomes NaN, or 0 as a whole number.
 struct E4m3 {
     using Code = unsigned char;
     static constexpr float kOver = 1.0f / 448.0f;
-    static __device__ __forceinline__ Code encode(float y) { return __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3); }
+    static __device__ __forceinline__ unsigned encode(float a, float b) {
+        return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    }
     static __device__ __forceinline__ float decode(Code c) {
         return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
     }
@@ -37,21 +42,27 @@ struct E4m3 {
 struct I8 {
     using Code = signed char;
     static constexpr float kOver = 1.0f / 127.0f;
-    static __device__ __forceinline__ Code encode(float y) { return (Code)max(-127, min(127, __float2int_rn(y))); }
+    static __device__ __forceinline__ unsigned encode(float a, float b) {
+        return __byte_perm(__float2int_rn(a), __float2int_rn(b), 0x5540) & 0xffffu;
+    }
     static __device__ __forceinline__ float decode(Code c) { return (float)c; }
 };
 
 constexpr float kLeastScale = 0x1p-126f;  // so that 1 / scale is finite, and zeros have one
 
-// The scale of a head whose largest |y| has these bits (as whole numbers they
-// are in the order of the values, with infinities and NaN above all others).
-// A head that holds one of those has the scale NaN.
+// The scale of a head whose largest |y| is `most`.  A head that holds an
+// infinity or a NaN has the scale NaN.
 template <class Q>
-__device__ __forceinline__ float scale_of(unsigned most) {
-    return most >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : fmaxf(__fmul_rn(__uint_as_float(most), Q::kOver), kLeastScale);
+__device__ __forceinline__ float scale_of(float most) {
+    return most < INFINITY ? fmaxf(__fmul_rn(most, Q::kOver), kLeastScale) : __uint_as_float(0x7fffffffu);
 }
 
-__device__ __forceinline__ unsigned magnitude(float y) { return __float_as_uint(y) & 0x7fffffffu; }
+// The larger of a and |b|, NaN where one of them is.
+__device__ __forceinline__ float larger(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(fabsf(b)));
+    return y;
+}
 
 // Where the scales of a cache lie; strides in bytes.
 struct Scales {
@@ -70,6 +81,209 @@ struct QuantisedParams {
     int dims[3];
     int stage;  // floats of a warp's staged head
 };
+
+constexpr int kMostThreads = 256;
+constexpr int kHeadsAtOnce = 2;  // heads whose words a thread has in flight
+
+// W values times `over` as W codes, written as one word.
+template <class Q, int W>
+__device__ __forceinline__ void put_codes(char* to, const float (&y)[W], float over) {
+    unsigned c[W / 4];
+#pragma unroll
+    for (int i = 0; i < W; i += 4)
+        c[i / 4] = Q::encode(__fmul_rn(y[i], over), __fmul_rn(y[i + 1], over)) |
+                   Q::encode(__fmul_rn(y[i + 2], over), __fmul_rn(y[i + 3], over)) << 16;
+    if (!BMMC_WR_OK(to, W)) return;
+    if constexpr (W == 8) *reinterpret_cast<uint2*>(to) = make_uint2(c[0], c[1]);
+    else *reinterpret_cast<unsigned*>(to) = c[0];
+}
+
+// A word's elements (and, TWO, those half a head on) turned.
+template <int W, bool TWO, int N>
+__device__ __forceinline__ void turn_words(float (&x)[W], float (&y)[W], const float2 (&r)[N]) {
+    if constexpr (TWO) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const float v = x[i];
+            x[i] = turned_first(v, y[i], r[i]);
+            y[i] = turned_second(v, y[i], r[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; i += 2) {
+            const float v = x[i];
+            x[i] = turned_first(v, x[i + 1], r[i / 2]);
+            x[i + 1] = turned_second(v, x[i + 1], r[i / 2]);
+        }
+    }
+}
+
+// A thread's words of one kind of heads of its token: keys (Q 0, turned), values
+// (1) and queries (2, turned, not quantised).  The kind is known when this is
+// compiled, so that what describes it lies at fixed places: with one loop over
+// the kinds it was fetched again for every head, and the append of 16001 tokens
+// took 88 us.
+template <class T, class Q, bool ADJACENT, int PART>
+__device__ __forceinline__ void append_part(const QuantisedParams& qp, int64_t t, bool there, int in, Slots<float2> turn,
+                                            int64_t to, int page, int slot) {
+    constexpr int W = 16 / sizeof(T);
+    constexpr bool kTurned = PART != 1, kPlaced = PART != 2;
+    constexpr bool kTwo = kTurned && !ADJACENT;  // an item that is turned has two words
+    constexpr int kTurns = kTwo ? W : W / 2;
+    const MoveParams& p = qp.p;
+    const Heads& h = p.part[PART];
+    const int down = (in * h.magic) >> 16, step = (1 << p.group_log2) / h.across, j0 = in - down * h.across;
+    there = there && down < step;
+    const char* const src = h.src + t * h.src_token + down * h.src_head;
+    char* const dst = h.dst + to + down * h.dst_head;
+    const int64_t src_step = step * h.src_head, dst_step = step * h.dst_head;
+    const int half = p.pairs * (int)sizeof(T);
+    const auto load = [&](Pack<T, W>& y, bool want, const char* from) {
+        if (want && BMMC_RD_OK(from, 16)) y.load(from);
+        else y.word = uint4{};
+    };
+    // (a cache's heads have a thread for each word: one j)
+    for (int j = j0; j == j0 || j < h.items; j += h.across) {
+        const bool mine = there && j < h.items, turned = kTurned && mine && j < h.turning, two = kTwo && turned;
+        const int at = (kTwo && j >= h.turning ? j + h.turning : j) * W;
+        float2 r[kTurns];
+        if (turned)
+#pragma unroll
+            for (int i = 0; i < kTurns; ++i) r[i] = turn.get(j * kTurns + i);
+        const char* from = src + at * (int)sizeof(T);
+        char* row = dst + at * (kPlaced ? 1 : (int)sizeof(T));
+        // `first`: of the heads that the lanes of a warp take at once; the same for all of them
+        for (int first = 0; first < h.heads; first += kHeadsAtOnce * step) {
+            Pack<T, W> a[kHeadsAtOnce], b[kHeadsAtOnce];
+#pragma unroll
+            for (int u = 0; u < kHeadsAtOnce; ++u) {
+                const bool put = mine && first + u * step + down < h.heads;
+                load(a[u], put, from);
+                if (kTwo) load(b[u], put && two, from + half);
+                from += src_step;
+            }
+#pragma unroll
+            for (int u = 0; u < kHeadsAtOnce; ++u) {
+                if (u && first + u * step >= h.heads) break;  // no lane has one
+                const bool put = mine && first + u * step + down < h.heads;
+                float x[W], y[W];
+#pragma unroll
+                for (int i = 0; i < W; ++i) x[i] = a[u].get(i), y[i] = kTwo ? b[u].get(i) : 0.0f;
+                if (turned) turn_words<W, kTwo>(x, y, r);
+                if constexpr (!kPlaced) {
+                    a[u].set(x);
+                    if (put && BMMC_WR_OK(row, 16)) a[u].store(row);
+                    if (two) {
+                        b[u].set(y);
+                        if (put && BMMC_WR_OK(row + half, 16)) b[u].store(row + half);
+                    }
+                } else {
+                    float most = 0.0f;  // (lanes without a word have zeros)
+#pragma unroll
+                    for (int i = 0; i < W; ++i) most = larger(most, x[i]);
+                    if (two)
+#pragma unroll
+                        for (int i = 0; i < W; ++i) most = larger(most, y[i]);
+                    for (int d = h.across >> 1; d; d >>= 1) most = larger(most, __shfl_xor_sync(~0u, most, d));
+                    const float scale = scale_of<Q>(most), over = __frcp_rn(scale);
+                    if (put) {
+                        put_codes<Q, W>(row, x, over);
+                        if (two) put_codes<Q, W>(row + p.pairs, y, over);
+                        if (j == 0) {
+                            float* const s = qp.scales[PART == 1].at(page, slot, first + u * step + down);
+                            if (BMMC_WR_OK(s, 4)) *s = scale;
+                        }
+                    }
+                }
+                row += dst_step;
+            }
+        }
+    }
+}
+
+// Heads made of words of 16 bytes: a block takes some tokens, a group of
+// threads each, and a thread its word (two, where a pair's elements lie half a
+// head apart) of one head after another, two at a time, its cosines and sines
+// in registers.  The threads of a head are neighbouring lanes, a power of two of
+// them, which find its largest element by exchange.  Nothing of a head is kept
+// anywhere but in registers.
+template <class T, class Q, bool ADJACENT>
+__global__ void __launch_bounds__(kMostThreads, 3) append_words_kernel(const __grid_constant__ QuantisedParams qp BMMC_SPANS_PARAM) {
+    extern __shared__ float2 s_turn[];  // [tokens of the block][pairs] cos, sin
+    __shared__ int64_t s_place[2][kMaxTokensPerBlock];
+    __shared__ float s_position[kMaxTokensPerBlock];
+    __shared__ int s_slot[2][kMaxTokensPerBlock];
+    BMMC_SPANS_ENTER(s_turn, chk::dyn_smem_bytes(), s_place, sizeof(s_place), s_position, sizeof(s_position), s_slot,
+                     sizeof(s_slot));
+    const MoveParams& p = qp.p;
+    const int tid = threadIdx.x, per_block = blockDim.x >> p.group_log2;
+    const Slots<float2> turns(s_turn, per_block * p.pairs);
+    const Slots<int64_t> places(&s_place[0][0], 2 * kMaxTokensPerBlock);
+    const Slots<float> place_numbers(s_position, kMaxTokensPerBlock);
+    const Slots<int> slots(&s_slot[0][0], 2 * kMaxTokensPerBlock);
+    const int64_t t0 = (int64_t)blockIdx.x * per_block;
+    const int nt = (int)min((int64_t)per_block, p.tokens - t0);
+    // a block of a small call takes one part only
+    const int first_part = gridDim.y > 1 ? blockIdx.y : 0, last_part = gridDim.y > 1 ? first_part + 1 : p.parts;
+    begin_block(p, t0, nt, first_part, last_part, turns, places, place_numbers, slots);
+    const int k = tid >> p.group_log2, in = tid & ((1 << p.group_log2) - 1);
+    const bool there = k < nt;
+    const int64_t t = there ? t0 + k : t0;
+    const Slots<float2> turn = turns.part(there ? k * p.pairs : 0, p.pairs);
+    if (first_part <= 1) {
+        const int page = there ? slots.get(k) : -1, slot = there ? slots.get(kMaxTokensPerBlock + k) : 0;
+        const int64_t key_at = places.get(there ? k : 0), value_at = places.get(kMaxTokensPerBlock + (there ? k : 0));
+        if (first_part == 0) append_part<T, Q, ADJACENT, 0>(qp, t, there && page >= 0, in, turn, key_at, page, slot);
+        if (last_part > 1) append_part<T, Q, ADJACENT, 1>(qp, t, there && page >= 0, in, turn, value_at, page, slot);
+    }
+    if (last_part > 2) append_part<T, Q, ADJACENT, 2>(qp, t, there, in, turn, t * p.part[2].dst_token, 0, 0);
+}
+
+// Threads of a token and of a head, as for heads that are only moved: in a
+// small call as many as a part has words, so that all its loads are in flight at
+// once, and the parts go to blocks of their own; in one that fills the machine a
+// quarter, so that cosines and sines serve several heads.
+template <class T, class Q>
+bmmc_status launch_append_words(QuantisedParams& qp, const chk::Spans& spans, cudaStream_t st) {
+    (void)spans;
+    constexpr int W = 16 / sizeof(T);
+    MoveParams& p = qp.p;
+    int64_t most = std::max(1, p.pairs / kAhead);
+    int least = 2;
+    for (int q = 0; q < p.parts; ++q) {
+        Heads& h = p.part[q];
+        const int pairs = h.turned ? p.pairs : 0;
+        h.turning = p.adjacent ? 2 * pairs / W : pairs / W;
+        h.items = h.turning + (qp.dims[q] - 2 * pairs) / W;
+        most = std::max(most, (int64_t)h.heads * h.items);
+        if (h.place)
+            while ((1 << least) < h.items) ++least;
+    }
+    int full = 2;
+    while (full < 8 && (1 << full) < most) ++full;
+    const bool small = (p.tokens << full) <= kSms * 1024;
+    int group = std::max(least, small ? std::min(full, 7) : most > 1024 ? full : std::max(2, full - 2));
+    int threads = small ? std::max(64, 1 << group) : std::max(kThreads, 1 << group);
+    while ((threads >> group) > kMaxTokensPerBlock) ++group;
+    while ((threads >> group) > 1 && (threads >> group) * p.pairs * sizeof(float2) > 32 * 1024) ++group;
+    p.group_log2 = group;
+    for (int q = 0; q < p.parts; ++q) {
+        Heads& h = p.part[q];
+        h.across = 1;
+        if (h.place)
+            while (h.across < h.items) h.across <<= 1;
+        else
+            h.across = std::min(h.items, 1 << group);
+        h.magic = (65536 + h.across - 1) / h.across;
+        const bool dense = p.device && (h.heads < 2 || h.src_head == (int64_t)qp.dims[q] * (int)sizeof(T));
+        h.ahead = dense ? std::min((unsigned)(h.heads * qp.dims[q] * sizeof(T)), 65536u) : 0u;
+    }
+    const int per_block = threads >> group;
+    const bool split = p.tokens / per_block * p.parts * threads <= kSms * 1024;
+    const dim3 grid((unsigned)((p.tokens + per_block - 1) / per_block), split ? p.parts : 1);
+    const auto kernel = p.adjacent ? append_words_kernel<T, Q, true> : append_words_kernel<T, Q, false>;
+    return launch(kernel, grid, dim3(threads), (size_t)per_block * p.pairs * sizeof(float2), st, nullptr, qp BMMC_SPANS_ARG(spans));
+}
 
 // Any heads: a warp turns a head, an element a lane, stages it in shared
 // memory in 32 bits, and writes its values with their scale.
@@ -108,26 +322,26 @@ __global__ void __launch_bounds__(kThreads) append_heads_kernel(const __grid_con
             if (h.place) stage.set(e, y);
             else if (BMMC_WR_OK(dst + e * sizeof(T), sizeof(T))) reinterpret_cast<T*>(dst)[e] = from_f32<T>(y);
         };
-        unsigned most = 0;
+        float most = 0.0f;
         // (queries turned in place: a pair's elements are read before they are written)
         for (int j = lane; j < pairs; j += 32) {
             const int a = p.adjacent ? 2 * j : j, b = a + (p.adjacent ? 1 : pairs);
             const float2 turn = turns.get(k * p.pairs + j);
             const float x = value(a), y = value(b), u = turned_first(x, y, turn), v = turned_second(x, y, turn);
             keep(a, u), keep(b, v);
-            most = max(most, max(magnitude(u), magnitude(v)));
+            most = larger(larger(most, u), v);
         }
         for (int e = 2 * pairs + lane; e < dim; e += 32) {
             const float y = value(e);
             keep(e, y);
-            most = max(most, magnitude(y));
+            most = larger(most, y);
         }
         if (!h.place) continue;
-        most = __reduce_max_sync(~0u, most);
+        for (int d = 16; d; d >>= 1) most = larger(most, __shfl_xor_sync(~0u, most, d));
         const float scale = scale_of<Q>(most), over = __frcp_rn(scale);
         __syncwarp();
         for (int e = lane; e < dim; e += 32)
-            if (BMMC_WR_OK(dst + e, 1)) reinterpret_cast<Code*>(dst)[e] = Q::encode(__fmul_rn(stage.get(e), over));
+            if (BMMC_WR_OK(dst + e, 1)) reinterpret_cast<Code*>(dst)[e] = (Code)Q::encode(__fmul_rn(stage.get(e), over), 0.0f);
         float* const s = qp.scales[h.place - 1].at(slots.get(k), slots.get(kMaxTokensPerBlock + k), head);
         if (lane == 0 && BMMC_WR_OK(s, 4)) *s = scale;
         __syncwarp();
@@ -265,7 +479,16 @@ bmmc_status paged_append_quantised(const paged_append_quantised_args_t* args, vo
     const chk::Spans spans = spans_of({c.k, c.v, c.q, turn_rows(a.turns, a.tokens, 0), turn_rows(a.turns, a.tokens, 1),
                                        turn_rows(a.turns, a.tokens, 2), c.maps[0], c.maps[1], c.maps[2]},
                                       {c.written[0], c.written[1], c.written[2], scales[0], scales[1]});
+    // heads of words: their lengths, addresses and pairs in words of 16 bytes, their values in what those become
+    const int W = 16 / es;
+    bool words = word_bytes(es, {c.in_bits, c.q_bits, pair_bits(a.turns, es)}) == 16 &&
+                 !(c.cache_bits & (uint64_t)(W - 1));
+    for (int i = 0; i < 2; ++i) {
+        const int64_t two = i == 0 && !qp.p.adjacent ? a.turns.pairs : 0;  // elements in an item's second word
+        words = words && (c.dims[i] - two) / W <= 32;
+    }
     return by_cache_type(type, args->cache_type, [&](auto t, auto q) {
+        if (words) return launch_append_words<decltype(t), decltype(q)>(qp, spans, static_cast<cudaStream_t>(stream));
         return launch_append<decltype(t), decltype(q)>(qp, spans, static_cast<cudaStream_t>(stream));
     });
 }
