@@ -35,8 +35,9 @@ struct E4m3 {
     static __device__ __forceinline__ unsigned encode(float a, float b) {
         return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
     }
-    static __device__ __forceinline__ float decode(Code c) {
-        return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+    // the values of the codes in the low half of c
+    static __device__ __forceinline__ float2 decode(unsigned c) {
+        return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3)));
     }
 };
 struct I8 {
@@ -45,7 +46,13 @@ struct I8 {
     static __device__ __forceinline__ unsigned encode(float a, float b) {
         return __byte_perm(__float2int_rn(a), __float2int_rn(b), 0x5540) & 0xffffu;
     }
-    static __device__ __forceinline__ float decode(Code c) { return (float)c; }
+    // (c + 128 in the last bits of 2^23, less 2^23 + 128: the conversion of a
+    // byte has a quarter of the rate)
+    static __device__ __forceinline__ float2 decode(unsigned c) {
+        c ^= 0x8080u;
+        return make_float2(__uint_as_float(__byte_perm(c, 0x4b000000u, 0x7440)) - 8388736.0f,
+                           __uint_as_float(__byte_perm(c, 0x4b000000u, 0x7441)) - 8388736.0f);
+    }
 };
 
 constexpr float kLeastScale = 0x1p-126f;  // so that 1 / scale is finite, and zeros have one
@@ -368,53 +375,159 @@ bmmc_status launch_append(QuantisedParams& qp, const chk::Spans& spans, cudaStre
 
 // ---- read ----------------------------------------------------------------------
 
+constexpr int kReadThreads = 256;
+constexpr int kReadRows = 8;   // rows of a block, at most
+constexpr int kReadAhead = 4;  // rows whose words a thread has in flight
+
 struct ReadParams {
     MoveParams p;  // part[0], part[1]: from the caches to the rows; lengths: each sequence's first entry
     Scales scales[2];
     int dims[2];
+    int rows;           // of a block
+    int words[2];       // of a head
+    unsigned magic[2];  // 2^32 / words rounded up
 };
 
-// A value of 8 bits or of the result's type as the result's type.
-template <class T, class Q>
-__device__ __forceinline__ T read_value(const char* from, int e, float scale) {
-    if constexpr (std::is_void_v<Q>) {
-        return BMMC_RD_OK(from + e * sizeof(T), sizeof(T)) ? reinterpret_cast<const T*>(from)[e] : from_f32<T>(0.0f);
-    } else {
-        using Code = typename Q::Code;
-        return from_f32<T>(BMMC_RD_OK(from + e, 1) ? __fmul_rn(Q::decode(reinterpret_cast<const Code*>(from)[e]), scale) : 0.0f);
+// W elements of the result from what the cache holds: themselves, or W codes
+// and their scale.
+template <class T, class Q, int W>
+struct Held {
+    using Word = typename WordOf<W * (int)sizeof(T)>::type;
+    Word word;
+    __device__ __forceinline__ void load(const char* p) { word = *reinterpret_cast<const Word*>(p); }
+    __device__ __forceinline__ Pack<T, W> value(float) const {
+        Pack<T, W> y;
+        y.word = word;
+        return y;
     }
-}
-
-// A warp a row, an element a lane.
-template <class T, class Q>
-__global__ void __launch_bounds__(kThreads) read_rows_kernel(const __grid_constant__ ReadParams rp BMMC_SPANS_PARAM) {
-    BMMC_SPANS_ENTER_GLOBAL();
-    const MoveParams& p = rp.p;
-    const int lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (t >= p.tokens) return;
-    const Place place = place_of(p, t, find_sequence_warp(p.starts, p.sequences, t, lane));
-    for (int q = 0; q < 2; ++q) {
-        const Heads& h = p.part[q];
-        for (int head = 0; head < h.heads; ++head) {
-            T* const to = reinterpret_cast<T*>(h.dst + t * h.dst_token + head * h.dst_head);
-            const char* const from = h.src + place.byte[q] + head * h.src_head;
-            float scale = 0.0f;
-            if (!std::is_void_v<Q> && place.page >= 0) {
-                const float* const s = rp.scales[q].at(place.page, place.slot, head);
-                if (BMMC_RD_OK(s, 4)) scale = *s;
-            }
-            for (int e = lane; e < rp.dims[q]; e += 32)
-                if (BMMC_WR_OK(to + e, sizeof(T))) to[e] = place.page < 0 ? from_f32<T>(0.0f) : read_value<T, Q>(from, e, scale);
+    static constexpr int kBytes = W * (int)sizeof(T);
+};
+template <class T, class Q, int W>
+struct Coded {
+    static constexpr int kBytes = W;
+    unsigned c[W > 4 ? 2 : 1];
+    __device__ __forceinline__ void load(const char* p) {
+        if constexpr (W == 8) {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            c[0] = v.x, c[1] = v.y;
+        } else if constexpr (W == 4) {
+            c[0] = *reinterpret_cast<const unsigned*>(p);
+        } else if constexpr (W == 2) {
+            c[0] = *reinterpret_cast<const unsigned short*>(p);
+        } else {
+            c[0] = *reinterpret_cast<const unsigned char*>(p);
         }
     }
+    __device__ __forceinline__ Pack<T, W> value(float scale) const {
+        float v[W];
+        if constexpr (W == 1) {
+            v[0] = __fmul_rn(Q::decode(c[0]).x, scale);
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; i += 2) {
+                const float2 y = Q::decode(c[i / 4] >> (i % 4 * 8) & 0xffffu);
+                v[i] = __fmul_rn(y.x, scale), v[i + 1] = __fmul_rn(y.y, scale);
+            }
+        }
+        Pack<T, W> y;
+        y.set(v);
+        return y;
+    }
+};
+
+// A block takes some rows: its warps find their places, then a thread takes the
+// same word of each, several rows at a time.  Pure movement.
+template <class T, class Q, int W>
+__global__ void __launch_bounds__(kReadThreads) read_words_kernel(const __grid_constant__ ReadParams rp BMMC_SPANS_PARAM) {
+    __shared__ int64_t s_place[2][kReadRows];
+    __shared__ int s_page[kReadRows], s_slot[kReadRows];
+    BMMC_SPANS_ENTER(s_place, sizeof(s_place), s_page, sizeof(s_page), s_slot, sizeof(s_slot));
+    constexpr bool kCoded = !std::is_void_v<Q>;
+    using Word = std::conditional_t<kCoded, Coded<T, Q, W>, Held<T, Q, W>>;
+    const Slots<int64_t> places(&s_place[0][0], 2 * kReadRows);
+    const Slots<int> pages(s_page, kReadRows), slots(s_slot, kReadRows);
+    const MoveParams& p = rp.p;
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int64_t t0 = (int64_t)blockIdx.x * rp.rows;
+    const int n = (int)min((int64_t)rp.rows, p.tokens - t0);
+    for (int i = threadIdx.x >> 5; i < n; i += warps) {
+        const Place place = place_of(p, t0 + i, find_sequence_warp(p.starts, p.sequences, t0 + i, lane));
+        if (lane == 0) {
+            places.set(i, place.byte[0]), places.set(kReadRows + i, place.byte[1]);
+            pages.set(i, place.page), slots.set(i, place.slot);
+        }
+    }
+    __syncthreads();
+    const auto part = [&](auto which) {
+        constexpr int q = decltype(which)::value;
+        const Heads& h = p.part[q];
+        for (int j = threadIdx.x; j < h.heads * rp.words[q]; j += blockDim.x) {
+            const int head = rp.words[q] == 1 ? j : (int)__umulhi(j, rp.magic[q]), at = (j - head * rp.words[q]) * W;
+            const char* const src = h.src + head * h.src_head + at * (Word::kBytes / W);
+            char* to = h.dst + t0 * h.dst_token + head * h.dst_head + at * (int)sizeof(T);
+            for (int r = 0; r < n; r += kReadAhead) {
+                Word word[kReadAhead];
+                float scale[kReadAhead];
+                bool there[kReadAhead];
+#pragma unroll
+                for (int u = 0; u < kReadAhead; ++u) {
+                    const int page = r + u < n ? pages.get(r + u) : -1;
+                    there[u] = page >= 0;
+                    const char* const from = src + (there[u] ? places.get(q * kReadRows + r + u) : 0);
+                    there[u] = there[u] && BMMC_RD_OK(from, Word::kBytes);
+                    if (there[u]) word[u].load(from);
+                    scale[u] = 0.0f;
+                    if (kCoded && there[u]) {
+                        const float* const s = rp.scales[q].at(page, slots.get(r + u), head);
+                        if (BMMC_RD_OK(s, 4)) scale[u] = *s;
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kReadAhead; ++u) {
+                    if (r + u >= n) break;
+                    Pack<T, W> y;
+                    if (there[u]) y = word[u].value(scale[u]);
+                    else y.word = typename Pack<T, W>::Word{};
+                    if (BMMC_WR_OK(to, sizeof(y))) y.store(to);
+                    to += h.dst_token;
+                }
+            }
+        }
+    };
+    part(std::integral_constant<int, 0>{});
+    part(std::integral_constant<int, 1>{});
 }
 
-template <class T, class Q>
-bmmc_status launch_read(const ReadParams& rp, const chk::Spans& spans, cudaStream_t st) {
+template <class T, class Q, int W>
+bmmc_status launch_read_words(ReadParams& rp, const chk::Spans& spans, cudaStream_t st) {
     (void)spans;
-    return launch(read_rows_kernel<T, Q>, dim3((unsigned)((rp.p.tokens + kWarps - 1) / kWarps)), dim3(kThreads), 0, st, nullptr,
+    const int64_t tokens = rp.p.tokens;
+    int most = 1;
+    for (int q = 0; q < 2; ++q) {
+        rp.words[q] = rp.dims[q] / W;
+        rp.magic[q] = (unsigned)((((uint64_t)1 << 32) + rp.words[q] - 1) / rp.words[q]);
+        most = std::max(most, rp.p.part[q].heads * rp.words[q]);
+    }
+    int threads = 32;
+    while (threads < kReadThreads && threads < most) threads <<= 1;
+    rp.rows = 1;  // more where the blocks still fill the machine
+    while (rp.rows < kReadRows && tokens * threads >= kSms * 2048 * rp.rows * 2) rp.rows <<= 1;
+    return launch(read_words_kernel<T, Q, W>, dim3((unsigned)((tokens + rp.rows - 1) / rp.rows)), dim3(threads), 0, st, nullptr,
                   rp BMMC_SPANS_ARG(spans));
+}
+
+// Elements of a word: as many as out_bits (16 bytes at most) and cache_bits
+// (cs bytes an element) are multiples of.
+template <class T, class Q>
+bmmc_status launch_read(ReadParams& rp, uint64_t out_bits, uint64_t cache_bits, const chk::Spans& spans, cudaStream_t st) {
+    constexpr int es = sizeof(T), cs = std::is_void_v<Q> ? es : 1;
+    int W = word_bytes(es, {out_bits}) / es;
+    while (W > 1 && (cache_bits & (uint64_t)(W * cs - 1))) W >>= 1;
+    if constexpr (es == 2)
+        if (W == 8) return launch_read_words<T, Q, 8>(rp, spans, st);
+    if (W == 4) return launch_read_words<T, Q, 4>(rp, spans, st);
+    if (W == 2) return launch_read_words<T, Q, 2>(rp, spans, st);
+    return launch_read_words<T, Q, 1>(rp, spans, st);
 }
 
 // ---- host ----------------------------------------------------------------------
@@ -573,10 +686,12 @@ bmmc_status paged_read(const paged_read_args_t* a, void* stream) {
     const chk::Spans spans = spans_of({in[0], in[1], in[2], in[3], in[4], in[5], in[6]}, {out[0], out[1]});
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (quantised)
-        return by_cache_type(type, a->cache_type,
-                             [&](auto t, auto q) { return launch_read<decltype(t), decltype(q)>(rp, spans, st); });
+        return by_cache_type(type, a->cache_type, [&](auto t, auto q) {
+            return launch_read<decltype(t), decltype(q)>(rp, out_bits, cache_bits, spans, st);
+        });
     // (values of the result's own type are only moved)
-    return es == 4 ? launch_read<float, void>(rp, spans, st) : launch_read<__half, void>(rp, spans, st);
+    return es == 4 ? launch_read<float, void>(rp, out_bits, cache_bits, spans, st)
+                   : launch_read<__half, void>(rp, out_bits, cache_bits, spans, st);
 }
 
 }  // extern "C"
