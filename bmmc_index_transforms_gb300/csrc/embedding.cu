@@ -7,6 +7,7 @@
 // The lookup is a gather of rows, its gradient the gather's transpose.  Equal
 // tokens are brought together by a stable sort of the tokens by id; the rows
 // of a run are then added up in the order of the tokens.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -35,27 +36,36 @@ __device__ __forceinline__ int64_t row_named(Id id, int64_t vocab) {
 
 // ---- lookup ------------------------------------------------------------------
 
-// Pure movement but for one product: a word a thread.
-template <class T, int W, bool ACROSS, class Id>
+// Pure movement but for one product: K words of one token a thread.
+template <class T, int W, bool ACROSS, int K, class Id>
 __global__ void __launch_bounds__(256) lookup_kernel(const char* __restrict__ table, int64_t table_stride, int64_t vocab,
                                                      const Id* __restrict__ ids, int64_t tokens, int length, float scale,
                                                      char* __restrict__ out, int64_t out_stride BMMC_SPANS_PARAM) {
     BMMC_SPANS_ENTER_GLOBAL();
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    const int w = blockIdx.y * blockDim.x + threadIdx.x;
     if (t >= tokens) return;
     char* const to = out + t * out_stride;
     const Walk<T, W, ACROSS> walk(length, to);
-    if (!walk.in(w)) return;
     const int64_t row = BMMC_RD_OK(ids + t, sizeof(Id)) ? row_named(ids[t], vocab) : -1;
-    typename Walk<T, W, ACROSS>::Fetch f;
-    walk.fetch(f, row >= 0, table + (row < 0 ? 0 : row) * table_stride, w);
-    Pack<T, W> y = walk.get(f);
-    float v[W];
+    const char* const from = table + (row < 0 ? 0 : row) * table_stride;
+    const int w0 = blockIdx.y * blockDim.x * K + threadIdx.x;
+    typename Walk<T, W, ACROSS>::Fetch f[K];
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] = row < 0 ? 0.0f : y.get(i) * scale;
-    y.set(v);
-    walk.store(y, to, w);
+    for (int k = 0; k < K; ++k) {
+        const int w = w0 + k * blockDim.x;
+        walk.fetch(f[k], row >= 0 && walk.in(w), from, w);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int w = w0 + k * blockDim.x;
+        if (!walk.in(w)) break;
+        Pack<T, W> y = walk.get(f[k]);
+        float v[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = row < 0 ? 0.0f : y.get(i) * scale;
+        y.set(v);
+        walk.store(y, to, w);
+    }
 }
 
 // ---- the sort of the tokens --------------------------------------------------
@@ -228,9 +238,104 @@ __global__ void __launch_bounds__(kSortThreads) digit_place_kernel(Sorted<Id, FI
     }
 }
 
+// The whole sort as one cluster of blocks, R keys a thread: keys and tokens stay
+// in registers, and each pass hands them to their places in the shared memory
+// of the cluster's blocks.
+constexpr int kSortCluster = 8;
+
+template <class Id, int R>
+__global__ void __launch_bounds__(kSortThreads) sort_cluster_kernel(const Id* __restrict__ ids, int n, int64_t vocab, int passes,
+                                                                    int digit, uint32_t* __restrict__ keys,
+                                                                    uint32_t* __restrict__ order BMMC_SPANS_PARAM) {
+    constexpr int kWarps = kSortThreads / 32, kTile = kSortThreads * R;
+    extern __shared__ int s_mem[];
+    BMMC_SPANS_ENTER(s_mem, chk_dynamic_bytes());
+    const auto cluster = cooperative_groups::this_cluster();
+    const int bins = 1 << digit, blocks = (int)gridDim.x, rank_in = (int)blockIdx.x;
+    const Slots<int> mem(s_mem, 2 * bins + 32 + kWarps * bins / 2 + 2 * kTile);
+    const Slots<int> base = mem.part(0, bins), mine_of = mem.part(bins, bins), tmp = mem.part(2 * bins, 32);
+    const Slots<unsigned short> hist(reinterpret_cast<unsigned short*>(s_mem + 2 * bins + 32), kWarps * bins);
+    const Slots<int> key_at = mem.part(2 * bins + 32 + kWarps * bins / 2, kTile);
+    const Slots<int> token_at = mem.part(2 * bins + 32 + kWarps * bins / 2 + kTile, kTile);
+    cudaTriggerProgrammaticLaunchCompletion();  // the rows may be cleared meanwhile
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = warp * R * 32 + lane;
+    const Slots<unsigned short> mine = hist.part(warp * bins, bins);
+    const int here = min(kTile, n - rank_in * kTile);
+    uint32_t key[R], token[R];
+    int rank[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int i = first + r * 32;
+        token[r] = rank_in * kTile + i;
+        key[r] = i < here ? key_of(ids, token[r], vocab) : 0;
+    }
+    for (int pass = 0; pass < passes; ++pass) {
+        const int shift = pass * digit;
+        for (int d = lane; d < bins; d += 32) mine.set(d, 0);
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool there = first + r * 32 < here;
+            const int d = (key[r] >> shift) & (bins - 1);
+            const unsigned same = same_digit(d, digit) & __ballot_sync(~0u, there);
+            const int before = there ? mine.get(d) : 0;
+            rank[r] = before + __popc(same & ((1u << lane) - 1));
+            __syncwarp();
+            if (there && lane == __ffs(same) - 1) mine.set(d, (unsigned short)(before + __popc(same)));
+            __syncwarp();
+        }
+        __syncthreads();
+        for (int d = threadIdx.x; d < bins; d += kSortThreads) {
+            int in_tile = 0;
+#pragma unroll 8
+            for (int w = 0; w < kWarps; ++w) {
+                const int c = hist.get(w * bins + d);
+                hist.set(w * bins + d, (unsigned short)in_tile);
+                in_tile += c;
+            }
+            mine_of.set(d, in_tile);
+        }
+        cluster.sync();  // the counts are there, and all keys are in registers
+        int ahead = 0;
+        for (int d = threadIdx.x; d < bins; d += kSortThreads) {  // (a digit a thread at most)
+            int all = 0;
+            for (int b = 0; b < blocks; ++b) {
+                const int c = mine_of.ok(d) ? *cluster.map_shared_rank(mine_of.p + d, b) : 0;
+                all += c;
+                if (b < rank_in) ahead += c;
+            }
+            base.set(d, all);
+        }
+        __syncthreads();
+        exclusive_scan(base, bins, tmp);
+        if ((int)threadIdx.x < bins) base.set(threadIdx.x, base.get(threadIdx.x) + ahead);
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (first + r * 32 >= here) continue;
+            const int d = (key[r] >> shift) & (bins - 1);
+            const int to = base.get(d) + mine.get(d) + rank[r], b = to / kTile, at = to - b * kTile;
+            if (key_at.ok(at) && b < blocks) *cluster.map_shared_rank(key_at.p + at, b) = (int)key[r];
+            if (token_at.ok(at) && b < blocks) *cluster.map_shared_rank(token_at.p + at, b) = (int)token[r];
+        }
+        cluster.sync();  // everything is in its place, and no block's counts are read any more
+        if (pass + 1 == passes) break;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int i = first + r * 32;
+            if (i < here) key[r] = key_at.get(i), token[r] = token_at.get(i);
+        }
+    }
+    for (int i = threadIdx.x; i < here; i += kSortThreads) {
+        const int64_t to = (int64_t)rank_in * kTile + i;
+        if (BMMC_WR_OK(keys + to, 4)) keys[to] = key_at.get(i);
+        if (BMMC_WR_OK(order + to, 4)) order[to] = token_at.get(i);
+    }
+}
+
 // ---- the sums ------------------------------------------------------------------
 
-// A chunk is kChunk places of the sorted tokens.  A run of equal ids that
+// A chunk is some places (kChunk at most) of the sorted tokens.  A run of equal ids that
 // reaches over two chunks at most is added up by the block of the chunk in
 // which it starts.  One that reaches over three or more is long: each of its
 // chunks adds up its part (in partial: part 0 of a chunk belongs to a run that
@@ -248,49 +353,67 @@ struct Runs {
     }
 };
 
-// v (added to what is there) to W elements of a row, `left` of which it has.
-template <class O, int W, bool WORDS>
-__device__ __forceinline__ void put(float (&v)[W], O* p, int left, bool accumulate) {
+// Where sums go.
+struct SumTo {
+    char* out;
+    int64_t stride;  // bytes
+    int64_t vocab;
+    float scale;
+    int length, accumulate;
+    float* partial;
+    int partial_stride;
+};
+
+// v (added to what is there) to element p.
+template <class O>
+__device__ __forceinline__ void put_one(O* p, float v, bool accumulate) {
+    if (!BMMC_WR_OK(p, sizeof(O))) return;
+    *p = from_f32<O>(accumulate && BMMC_RD_OK(p, sizeof(O)) ? v + to_f32(*p) : v);
+}
+
+// The same to W elements, in words.
+template <class O, int W>
+__device__ __forceinline__ void put_words(const float (&v)[W], O* p, bool accumulate) {
     constexpr int P = 16 / sizeof(O) < W ? 16 / sizeof(O) : W;
-    if constexpr (WORDS) {
 #pragma unroll
-        for (int a = 0; a < W; a += P) {
-            Pack<O, P> y;
-            float u[P];
-            if (accumulate && BMMC_RD_OK(p + a, sizeof(y))) y.load(p + a);
+    for (int a = 0; a < W; a += P) {
+        Pack<O, P> y;
+        float u[P];
+        if (accumulate && BMMC_RD_OK(p + a, sizeof(y))) y.load(p + a);
 #pragma unroll
-            for (int i = 0; i < P; ++i) u[i] = accumulate ? v[a + i] + y.get(i) : v[a + i];
-            y.set(u);
-            if (BMMC_WR_OK(p + a, sizeof(y))) y.store(p + a);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < W; ++i)
-            if (i < left && BMMC_WR_OK(p + i, sizeof(O)))
-                p[i] = from_f32<O>(accumulate && BMMC_RD_OK(p + i, sizeof(O)) ? v[i] + to_f32(p[i]) : v[i]);
+        for (int i = 0; i < P; ++i) u[i] = accumulate ? v[a + i] + y.get(i) : v[a + i];
+        y.set(u);
+        if (BMMC_WR_OK(p + a, sizeof(y))) y.store(p + a);
     }
 }
 
+// A block adds the runs of a chunk, a thread a word of their rows.  Rows that
+// are not made of words of 16 bytes (WORDS false) are cut out of two words each;
+// their sums are exchanged in shared memory, so that a warp writes neighbouring
+// elements.
 template <class T, class O, int W, bool WORDS>
-__global__ void __launch_bounds__(kSumThreads) sum_rows_kernel(
-    const char* __restrict__ grad, int64_t grad_stride, const uint32_t* __restrict__ keys,
-    const uint32_t* __restrict__ order, int64_t n, int64_t vocab, int length, float scale, int accumulate,
-    char* __restrict__ out, int64_t out_stride, float* __restrict__ partial, int partial_stride BMMC_SPANS_PARAM) {
+__global__ void __launch_bounds__(kSumThreads) sum_rows_kernel(const char* __restrict__ grad, int64_t grad_stride,
+                                                               const uint32_t* __restrict__ keys,
+                                                               const uint32_t* __restrict__ order, int64_t n, int chunk,
+                                                               const SumTo o BMMC_SPANS_PARAM) {
     __shared__ int s_key[2 * kChunk + 1], s_token[2 * kChunk];
-    BMMC_SPANS_ENTER(s_key, sizeof(s_key), s_token, sizeof(s_token));
+    __shared__ float s_sum[WORDS ? 1 : kSumThreads * W];
+    BMMC_SPANS_ENTER(s_key, sizeof(s_key), s_token, sizeof(s_token), s_sum, sizeof(s_sum));
     const Slots<int> ids(s_key, 2 * kChunk + 1), tokens(s_token, 2 * kChunk);
+    const Slots<float> sums(s_sum, WORDS ? 1 : kSumThreads * W);
+    cudaTriggerProgrammaticLaunchCompletion();  // the join waits for the sums by itself
     const Runs runs{keys, n};
-    const int64_t lo = (int64_t)blockIdx.x * kChunk;
-    for (int i = threadIdx.x; i <= 2 * kChunk; i += blockDim.x) {
+    const int64_t lo = (int64_t)blockIdx.x * chunk;
+    for (int i = threadIdx.x; i <= 2 * chunk; i += blockDim.x) {
         ids.set(i, (int)runs.key(lo + i));
-        if (i < 2 * kChunk)
-            tokens.set(i, lo + i < n && BMMC_RD_OK(order + lo + i, 4) ? (int)order[lo + i] : 0);
+        if (i < 2 * chunk) tokens.set(i, lo + i < n && BMMC_RD_OK(order + lo + i, 4) ? (int)order[lo + i] : 0);
     }
-    const int64_t before = runs.key(lo - 1), far_before = runs.key(lo - kChunk - 1);
+    const int64_t before = runs.key(lo - 1), far_before = runs.key(lo - chunk - 1);
     __syncthreads();
-    const int here = (int)min((int64_t)kChunk, n - lo), w = blockIdx.y * blockDim.x + threadIdx.x;
-    if (w * W >= length) return;
-    const Walk<T, W, !WORDS> walk(length, nullptr);
+    const int here = (int)min((int64_t)chunk, n - lo), w = blockIdx.y * blockDim.x + threadIdx.x;
+    if ((w - (WORDS ? 0 : (int)(threadIdx.x & 31))) * W >= o.length) return;  // (the lanes of an exchange stay together)
+    const Walk<T, W, !WORDS> walk(o.length, nullptr);
+    const bool mine = w * W < o.length;
     // the run that goes on from the chunk before: its owner's, or a part of a long one
     int begin = 0, end = here, first_part = -1;
     const int first = ids.get(0), last = ids.get(here - 1);
@@ -301,24 +424,38 @@ __global__ void __launch_bounds__(kSumThreads) sum_rows_kernel(
     }
     // the run that goes on behind this chunk, where it starts in this one
     bool last_part = false;
-    if ((begin < here && first_part < here) && ids.get(here) == last) {
-        if (runs.key(lo + 2 * kChunk) == last && here == kChunk) last_part = true;
+    if (begin < here && first_part < here && ids.get(here) == last) {
+        if (here == chunk && ids.get(2 * chunk) == last) last_part = true;
         else
-            while (end < 2 * kChunk && ids.get(end) == last) ++end;
+            while (end < 2 * chunk && ids.get(end) == last) ++end;
     }
     float sum[W] = {};
     int id = ids.get(begin < here ? begin : 0);
     const auto put_out = [&](bool part, int which) {
-        if (id < 0 || id >= vocab) return;
-        if (part) {
-            float* const to = partial + ((int64_t)blockIdx.x * 2 + which) * partial_stride + w * W;
+        if (id >= 0 && id < o.vocab) {
+            if (part) {
+                float* const to = o.partial + ((int64_t)blockIdx.x * 2 + which) * o.partial_stride + w * W;
+                if (mine) put_words<float, W>(sum, to, false);
+            } else {
+                O* const row = reinterpret_cast<O*>(o.out + (int64_t)id * o.stride);
 #pragma unroll
-            for (int i = 0; i < W; ++i)
-                if (BMMC_WR_OK(to + i, 4)) to[i] = sum[i];
-        } else {
+                for (int i = 0; i < W; ++i) sum[i] *= o.scale;
+                if constexpr (WORDS) {
+                    put_words<O, W>(sum, row + w * W, o.accumulate);
+                } else {
+                    const int lane = threadIdx.x & 31, warp = threadIdx.x - lane, at = (w - lane) * W;
+                    __syncwarp();
 #pragma unroll
-            for (int i = 0; i < W; ++i) sum[i] *= scale;
-            put<O, W, WORDS>(sum, reinterpret_cast<O*>(out + (int64_t)id * out_stride) + w * W, length - w * W, accumulate);
+                    for (int i = 0; i < W; ++i) sums.set(threadIdx.x * W + (i ^ (lane / (32 / W) & (W - 1))), sum[i]);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < W; ++i) {
+                        const int e = i * 32 + lane, l = e / W;  // element e of the warp's, which lane l has
+                        if (at + e < o.length)
+                            put_one(row + at + e, sums.get((warp + l) * W + (e % W ^ (l / (32 / W) & (W - 1)))), o.accumulate);
+                    }
+                }
+            }
         }
 #pragma unroll
         for (int i = 0; i < W; ++i) sum[i] = 0.0f;
@@ -327,8 +464,8 @@ __global__ void __launch_bounds__(kSumThreads) sum_rows_kernel(
         typename Walk<T, W, !WORDS>::Fetch f[kSumAhead];
 #pragma unroll
         for (int u = 0; u < kSumAhead; ++u) {
-            const bool want = at + u < end && ids.get(at + u) < vocab;
-            walk.fetch(f[u], want, grad + (int64_t)(want ? tokens.get(at + u) : 0) * grad_stride, w);
+            const bool want = at + u < end && ids.get(at + u) < o.vocab;
+            walk.fetch(f[u], want && mine, grad + (int64_t)(want ? tokens.get(at + u) : 0) * grad_stride, w);
         }
 #pragma unroll
         for (int u = 0; u < kSumAhead; ++u) {
@@ -346,33 +483,39 @@ __global__ void __launch_bounds__(kSumThreads) sum_rows_kernel(
     if (begin < end) put_out(last_part || end == first_part, last_part ? 1 : 0);
 }
 
-// Joins the parts of the long runs: a block looks at kOwners chunks for runs
-// that start there, and takes 128 columns of each: its warps add every eighth
-// part, then the eight sums are added in order.
-constexpr int kOwners = 16;
-
+// Joins the parts of the long runs: a block looks at 32 chunks for runs that
+// start there, and takes 128 columns of each: its warps add every eighth part,
+// then the eight sums are added in order.
 template <class O>
-__global__ void __launch_bounds__(256) join_parts_kernel(const uint32_t* __restrict__ keys, int64_t n, int64_t vocab,
-                                                         int length, float scale, int accumulate, char* __restrict__ out,
-                                                         int64_t out_stride, const float* __restrict__ partial,
-                                                         int partial_stride BMMC_SPANS_PARAM) {
-    __shared__ float s_sum[8][128];
+__global__ void __launch_bounds__(256) join_parts_kernel(const uint32_t* __restrict__ keys, int64_t n, int chunk,
+                                                         const SumTo o BMMC_SPANS_PARAM) {
+    __shared__ float s_sum[8 * 128];
     BMMC_SPANS_ENTER(s_sum, sizeof(s_sum));
-    const Slots<float> sums(&s_sum[0][0], 8 * 128);
+    const Slots<float> sums(s_sum, 8 * 128);
     const Runs runs{keys, n};
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int c = 0; c < kOwners; ++c) {
-        const int64_t chunk = (int64_t)blockIdx.x * kOwners + c, lo = chunk * kChunk, hi = lo + kChunk;
-        const int64_t id = runs.key(hi - 1);
-        if (hi + kChunk >= n || runs.key(hi) != id || runs.key(hi + kChunk) != id || id >= vocab) continue;
-        if (runs.key(lo - 1) == id) continue;  // it goes on from the chunk before
-        for (int first = blockIdx.y * 128; first < length; first += gridDim.y * 128) {
+    cudaGridDependencySynchronize();
+    const int64_t c0 = (int64_t)blockIdx.x * 32;
+    const int64_t lo_of = (c0 + lane) * chunk, hi_of = lo_of + chunk, id_of = runs.key(hi_of - 1);
+    const bool starts = id_of >= 0 && id_of < o.vocab && runs.key(hi_of) == id_of && runs.key(hi_of + chunk) == id_of &&
+                        runs.key(lo_of - 1) != id_of;
+    for (unsigned owners = __ballot_sync(~0u, starts); owners; owners &= owners - 1) {
+        const int64_t c = c0 + __ffs(owners) - 1, id = runs.key((c + 1) * chunk - 1);
+        int64_t parts = 1;  // chunks of the run
+        for (bool all = true; all;) {
+            const unsigned more = __ballot_sync(~0u, runs.key((c + parts + lane) * chunk) == id);
+            all = more == ~0u;
+            parts += all ? 32 : __ffs(~more) - 1;
+        }
+        const float* const from = o.partial + (c * 2) * o.partial_stride;  // part 1 of the first chunk, part 0 of the others
+        for (int first = blockIdx.y * 128; first < o.length; first += gridDim.y * 128) {
             float4 sum = make_float4(0, 0, 0, 0);
             const int col = first + lane * 4;
-            for (int64_t k = warp; k == 0 || runs.key(lo + k * kChunk) == id; k += 8) {
-                const float* const from = partial + ((chunk + k) * 2 + (k == 0)) * partial_stride + col;
-                const float4 v = col < partial_stride && BMMC_RD_OK(from, 16) ? *reinterpret_cast<const float4*>(from)
-                                                                               : make_float4(0, 0, 0, 0);
+#pragma unroll 4
+            for (int64_t k = warp; k < parts; k += 8) {
+                const float* const p = from + (k * 2 + (k == 0)) * o.partial_stride + col;
+                const float4 v = col < o.partial_stride && BMMC_RD_OK(p, 16) ? __ldcg(reinterpret_cast<const float4*>(p))
+                                                                            : make_float4(0, 0, 0, 0);
                 sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
             }
             const float v4[4] = {sum.x, sum.y, sum.z, sum.w};
@@ -380,31 +523,42 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const uint32_t* __restr
             for (int i = 0; i < 4; ++i) sums.set(warp * 128 + lane * 4 + i, v4[i]);
             __syncthreads();
             const int at = first + threadIdx.x;
-            if (threadIdx.x < 128 && at < length) {
-                float v[1] = {0.0f};
-                for (int g = 0; g < 8; ++g) v[0] += sums.get(g * 128 + threadIdx.x);
-                v[0] *= scale;
-                put<O, 1, false>(v, reinterpret_cast<O*>(out + id * out_stride) + at, 1, accumulate);
+            if (threadIdx.x < 128 && at < o.length) {
+                float v = 0.0f;
+                for (int g = 0; g < 8; ++g) v += sums.get(g * 128 + threadIdx.x);
+                put_one(reinterpret_cast<O*>(o.out + id * o.stride) + at, v * o.scale, o.accumulate);
             }
             __syncthreads();
         }
     }
 }
 
-// Rows of zeros.
+// Rows of zeros; rows without gaps are one long one, in words from the first
+// aligned address on.  A wave of blocks, which started beside the sort and ends
+// behind it (what comes next on the stream may count on both).
 template <class T>
-__global__ void __launch_bounds__(256) clear_rows_kernel(char* __restrict__ out, int64_t out_stride, int64_t rows, int length
-                                                             BMMC_SPANS_PARAM) {
+__global__ void __launch_bounds__(256) clear_rows_kernel(char* __restrict__ out, int64_t out_stride, int64_t rows,
+                                                         int64_t row_bytes BMMC_SPANS_PARAM) {
     BMMC_SPANS_ENTER_GLOBAL();
-    constexpr int W = 16 / sizeof(T);
-    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    const int w = blockIdx.y * blockDim.x + threadIdx.x;
-    if (t >= rows) return;
-    char* const to = out + t * out_stride;
-    const Walk<T, W, true> walk(length, to);
-    Pack<T, W> zero;
-    zero.word = uint4{};
-    if (walk.in(w)) walk.store(zero, to, w);
+    const int64_t threads = (int64_t)gridDim.x * blockDim.x, me = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const auto clear = [&](char* row, int64_t at, int64_t step) {
+        const int lead = (int)(-reinterpret_cast<uintptr_t>(row) & 15u);
+        const int64_t head = min((int64_t)lead, row_bytes), words = (row_bytes - head) / 16;
+        uint4* const w = reinterpret_cast<uint4*>(row + head);
+#pragma unroll 4
+        for (int64_t i = at; i < words; i += step)
+            if (BMMC_WR_OK(w + i, 16)) w[i] = uint4{};
+        // the elements ahead of the first word and behind the last one
+        const int64_t tail = head + words * 16;
+        for (int64_t i = at; i < (head + row_bytes - tail) / (int64_t)sizeof(T); i += step) {
+            T* const e = reinterpret_cast<T*>(row + (i * (int64_t)sizeof(T) < head ? 0 : tail - head)) + i;
+            if (BMMC_WR_OK(e, sizeof(T))) *e = T{};
+        }
+    };
+    if (rows == 1) clear(out, me, threads);
+    else
+        for (int64_t r = me >> 5; r < rows; r += threads >> 5) clear(out + r * out_stride, threadIdx.x & 31, 32);
+    cudaGridDependencySynchronize();
 }
 
 // ---- host ----------------------------------------------------------------------
@@ -429,21 +583,35 @@ SortShape sort_shape(int64_t n, int64_t vocab) {
 
 int64_t up16(int64_t bytes) { return (bytes + 15) & ~(int64_t)15; }
 
-// The workspace: two arrays of keys and two of tokens, the blocks' counts, and
-// two sums a chunk.
+// Keys a thread takes where the sort is one cluster; 0: it is not.
+int cluster_rounds(int64_t n) {
+    for (int r : {2, 8, 16})
+        if (n <= (int64_t)kSortCluster * kSortThreads * r) return r;
+    return 0;
+}
+
+// Places of a chunk: fewer where there are few tokens, so that more blocks have
+// some.
+int chunk_of(int64_t n, int64_t hidden) { return n * ((hidden + 1023) / 1024) <= kSms * 256 ? 8 : kChunk; }
+
+// The workspace: the sorted keys and tokens (both twice where the sort is not one
+// cluster, with the blocks' counts), and two sums a chunk.
 struct Workspace {
     int64_t array, counts, partial;  // bytes
-    int partial_stride;              // floats
-    int64_t bytes() const { return 4 * array + counts + partial; }
+    int arrays, chunk, partial_stride;  // partial_stride: floats
+    int64_t bytes() const { return arrays * array + counts + partial; }
 };
 
 Workspace workspace_of(int64_t n, int64_t vocab, int64_t hidden) {
-    const SortShape s = sort_shape(n, vocab);
     Workspace w;
+    const bool cluster = cluster_rounds(n);
     w.array = up16(n * 4);
-    w.counts = up16((int64_t)s.blocks * (4 << s.digit));
+    w.arrays = cluster ? 2 : 4;
+    const SortShape s = sort_shape(n, vocab);
+    w.counts = cluster ? 0 : up16((int64_t)s.blocks * (4 << s.digit));
     w.partial_stride = (int)((hidden + 7) & ~(int64_t)7);
-    const int64_t chunks = (n + kChunk - 1) / kChunk;
+    w.chunk = chunk_of(n, hidden);
+    const int64_t chunks = (n + w.chunk - 1) / w.chunk;
     w.partial = chunks < 3 ? 0 : chunks * 2 * w.partial_stride * 4;  // a long run has three
     return w;
 }
@@ -484,6 +652,26 @@ bmmc_status sort_tokens(const SortShape& s, const Id* ids, int64_t n, int64_t vo
     return BMMC_OK;
 }
 
+// The sort as one cluster.
+template <class Id, int R>
+bmmc_status sort_together(const SortShape& s, const Id* ids, int64_t n, int64_t vocab, uint32_t* keys, uint32_t* order,
+                          const chk::Spans& spans, cudaStream_t st) {
+    (void)spans;
+    const int tile = kSortThreads * R, blocks = (int)((n + tile - 1) / tile);
+    const size_t smem = ((2 << s.digit) + 32 + (kSortThreads / 64 << s.digit) + 2 * tile) * 4;
+    const auto kernel = sort_cluster_kernel<Id, R>;
+    if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+        cudaGetLastError();
+        return BMMC_ERR_CUDA;
+    }
+    cudaLaunchAttribute together{};
+    together.id = cudaLaunchAttributeClusterDimension;
+    together.val.clusterDim.x = blocks;
+    together.val.clusterDim.y = together.val.clusterDim.z = 1;
+    return launch(kernel, dim3(blocks), dim3(kSortThreads), smem, st, &together, ids, (int)n, vocab, s.passes, s.digit, keys,
+                  order BMMC_SPANS_ARG(spans));
+}
+
 }  // namespace
 
 extern "C" {
@@ -512,14 +700,19 @@ bmmc_status embedding_lookup(const void* table, int64_t table_stride, int64_t vo
         using T = decltype(e);
         constexpr int W = decltype(width)::value;
         constexpr bool A = decltype(across)::value;
-        const Cover c = cover(tokens, way.words, tokens * way.words <= kFewWords ? 128 : 256);
-        const auto go = [&](auto id) {
+        const auto go = [&](auto id, auto each) {
             using Id = decltype(id);
-            s = launch(lookup_kernel<T, W, A, Id>, c.grid, c.block, 0, static_cast<cudaStream_t>(stream), nullptr,
+            constexpr int K = decltype(each)::value;
+            const Cover c = cover(tokens, (way.words + K - 1) / K, 128);
+            s = launch(lookup_kernel<T, W, A, K, Id>, c.grid, c.block, 0, static_cast<cudaStream_t>(stream), nullptr,
                        static_cast<const char*>(table), table_stride * es, vocab, static_cast<const Id*>(ids), tokens,
                        (int)hidden, scale, static_cast<char*>(out), out_stride * es BMMC_SPANS_ARG(spans));
         };
-        id_bytes == 4 ? go(int32_t{}) : go(int64_t{});
+        const auto with = [&](auto id) {
+            if (tokens * way.words > kFewWords && way.words >= 4 * 32) go(id, std::integral_constant<int, 4>{});
+            else go(id, std::integral_constant<int, 1>{});
+        };
+        id_bytes == 4 ? with(int32_t{}) : with(int64_t{});
     });
     return s;
 }
@@ -558,37 +751,54 @@ bmmc_status embedding_backward(const void* grad, int64_t grad_stride, const void
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const chk::Spans spans = spans_of({from, names, scratch, to}, {to, scratch});
     (void)spans;
-    if (!accumulate) {
-        const int words = (int)((hidden + 2 * (16 / os - 1)) / (16 / os));
-        const Cover c = cover(vocab, words, 256);
-        s = os == 4 ? launch(clear_rows_kernel<uint32_t>, c.grid, c.block, 0, st, nullptr, static_cast<char*>(out),
-                             out_stride * os, vocab, (int)hidden BMMC_SPANS_ARG(spans))
-                    : launch(clear_rows_kernel<uint16_t>, c.grid, c.block, 0, st, nullptr, static_cast<char*>(out),
-                             out_stride * os, vocab, (int)hidden BMMC_SPANS_ARG(spans));
-        if (s != BMMC_OK || !tokens) return s;
-    }
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    const auto clear = [&](cudaLaunchAttribute* attribute) {
+        const bool flat = vocab == 1 || out_stride == hidden;
+        const int64_t rows = flat ? 1 : vocab, bytes = (flat ? vocab : 1) * hidden * os;
+        const int64_t blocks = std::min<int64_t>((vocab * hidden * os + 4095) / 4096, kSms * 4);
+        const auto go = [&](auto kernel) {
+            return launch(kernel, dim3((unsigned)blocks), dim3(256), 0, st, attribute, static_cast<char*>(out), out_stride * os,
+                          rows, bytes BMMC_SPANS_ARG(spans));
+        };
+        return os == 4 ? go(clear_rows_kernel<uint32_t>) : go(clear_rows_kernel<uint16_t>);
+    };
+    if (!tokens) return clear(nullptr);
     char* const at = static_cast<char*>(workspace);
-    uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(at), reinterpret_cast<uint32_t*>(at + w.array)};
-    uint32_t* order[2] = {reinterpret_cast<uint32_t*>(at + 2 * w.array), reinterpret_cast<uint32_t*>(at + 3 * w.array)};
-    int* const counts = reinterpret_cast<int*>(at + 4 * w.array);
-    float* const partial = reinterpret_cast<float*>(at + 4 * w.array + w.counts);
+    const auto array = [&](int i) { return reinterpret_cast<uint32_t*>(at + i * w.array); };
+    int* const counts = reinterpret_cast<int*>(at + w.arrays * w.array);
+    float* const partial = reinterpret_cast<float*>(at + w.arrays * w.array + w.counts);
     const SortShape shape = sort_shape(tokens, vocab);
-    s = id_bytes == 4 ? sort_tokens(shape, static_cast<const int32_t*>(ids), tokens, vocab, keys, order, counts, spans, st)
-                      : sort_tokens(shape, static_cast<const int64_t*>(ids), tokens, vocab, keys, order, counts, spans, st);
+    const uint32_t *key = array(0), *token = array(1);
+    const auto sorted = [&](const auto* names) {
+        using Id = std::remove_cv_t<std::remove_pointer_t<decltype(names)>>;
+        switch (cluster_rounds(tokens)) {
+            case 2: return sort_together<Id, 2>(shape, names, tokens, vocab, array(0), array(1), spans, st);
+            case 8: return sort_together<Id, 8>(shape, names, tokens, vocab, array(0), array(1), spans, st);
+            case 16: return sort_together<Id, 16>(shape, names, tokens, vocab, array(0), array(1), spans, st);
+        }
+        uint32_t *keys[2] = {array(0), array(2)}, *order[2] = {array(1), array(3)};
+        key = keys[(shape.passes - 1) & 1], token = order[(shape.passes - 1) & 1];
+        return sort_tokens(shape, names, tokens, vocab, keys, order, counts, spans, st);
+    };
+    s = id_bytes == 4 ? sorted(static_cast<const int32_t*>(ids)) : sorted(static_cast<const int64_t*>(ids));
+    // beside the sort where that is one cluster; behind it otherwise
+    if (s == BMMC_OK && !accumulate) s = clear(cluster_rounds(tokens) ? &early : nullptr);
     if (s != BMMC_OK) return s;
-    const uint32_t *key = keys[(shape.passes - 1) & 1], *token = order[(shape.passes - 1) & 1];
-    const int64_t chunks = (tokens + kChunk - 1) / kChunk;
+    const int64_t chunks = (tokens + w.chunk - 1) / w.chunk;
     const bool words = word_bytes(2, {(uint64_t)(uintptr_t)grad, (uint64_t)(uintptr_t)out, (uint64_t)(grad_stride * es),
                                       (uint64_t)(out_stride * os), (uint64_t)(hidden * es), (uint64_t)(hidden * os)}) == 16;
+    const SumTo o{static_cast<char*>(out), out_stride * os, vocab, scale, (int)hidden, accumulate, partial, w.partial_stride};
     const auto sum = [&](auto kernel, int W) {
-        const int row = (int)((hidden + W - 1) / W), x = row < kSumThreads ? (row + 31) / 32 * 32 : kSumThreads;
+        const int row = (int)((hidden + W - 1) / W), parts = (row + kSumThreads - 1) / kSumThreads;
+        const int x = ((row + parts - 1) / parts + 31) / 32 * 32;
         return launch(kernel, dim3((unsigned)chunks, (unsigned)((row + x - 1) / x)), dim3(x), 0, st, nullptr,
-                      static_cast<const char*>(grad), grad_stride * es, key, token, tokens, vocab, (int)hidden, scale,
-                      accumulate, static_cast<char*>(out), out_stride * os, partial, w.partial_stride BMMC_SPANS_ARG(spans));
+                      static_cast<const char*>(grad), grad_stride * es, key, token, tokens, w.chunk, o BMMC_SPANS_ARG(spans));
     };
-    const auto typed = [&](auto t, auto o) {
+    const auto typed = [&](auto t, auto to) {
         using T = decltype(t);
-        using O = decltype(o);
+        using O = decltype(to);
         constexpr int W = 16 / sizeof(T);
         return words ? sum(sum_rows_kernel<T, O, W, true>, W) : sum(sum_rows_kernel<T, O, W, false>, W);
     };
@@ -596,10 +806,9 @@ bmmc_status embedding_backward(const void* grad, int64_t grad_stride, const void
     else if (type == BMMC_F16) s = out_type == BMMC_F32 ? typed(__half{}, float{}) : typed(__half{}, __half{});
     else s = out_type == BMMC_F32 ? typed(__nv_bfloat16{}, float{}) : typed(__nv_bfloat16{}, __nv_bfloat16{});
     if (s != BMMC_OK || chunks < 3) return s;
-    const dim3 grid((unsigned)((chunks + kOwners - 1) / kOwners), (unsigned)std::min<int64_t>((hidden + 127) / 128, kMostParts));
+    const dim3 grid((unsigned)((chunks + 31) / 32), (unsigned)std::min<int64_t>((hidden + 127) / 128, kMostParts));
     const auto join = [&](auto kernel) {
-        return launch(kernel, grid, dim3(256), 0, st, nullptr, key, tokens, vocab, (int)hidden, scale, accumulate,
-                      static_cast<char*>(out), out_stride * os, (const float*)partial, w.partial_stride BMMC_SPANS_ARG(spans));
+        return launch(kernel, grid, dim3(256), 0, st, &early, key, tokens, w.chunk, o BMMC_SPANS_ARG(spans));
     };
     if (out_type == BMMC_F32) return join(join_parts_kernel<float>);
     return out_type == BMMC_F16 ? join(join_parts_kernel<__half>) : join(join_parts_kernel<__nv_bfloat16>);
