@@ -533,32 +533,47 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const uint32_t* __restr
     }
 }
 
-// Rows of zeros; rows without gaps are one long one, in words from the first
-// aligned address on.  A wave of blocks, which started beside the sort and ends
-// behind it (what comes next on the stream may count on both).
+// Rows of zeros.  Rows without gaps are one long one, whose words of 16 bytes are
+// dealt out to short blocks; rows with gaps have a warp each.  The grid starts
+// beside the sort; its last block waits for that, so that what comes next on the
+// stream may count on both.
+constexpr int kClearWords = 4;  // of a thread
+
 template <class T>
 __global__ void __launch_bounds__(256) clear_rows_kernel(char* __restrict__ out, int64_t out_stride, int64_t rows,
                                                          int64_t row_bytes BMMC_SPANS_PARAM) {
     BMMC_SPANS_ENTER_GLOBAL();
-    const int64_t threads = (int64_t)gridDim.x * blockDim.x, me = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const auto clear = [&](char* row, int64_t at, int64_t step) {
-        const int lead = (int)(-reinterpret_cast<uintptr_t>(row) & 15u);
-        const int64_t head = min((int64_t)lead, row_bytes), words = (row_bytes - head) / 16;
-        uint4* const w = reinterpret_cast<uint4*>(row + head);
-#pragma unroll 4
-        for (int64_t i = at; i < words; i += step)
-            if (BMMC_WR_OK(w + i, 16)) w[i] = uint4{};
-        // the elements ahead of the first word and behind the last one
-        const int64_t tail = head + words * 16;
+    const auto head_of = [&](const char* row) { return min((int64_t)(-reinterpret_cast<uintptr_t>(row) & 15u), row_bytes); };
+    // the elements ahead of the first word and behind the last one
+    const auto ends = [&](char* row, int at, int step) {
+        const int64_t head = head_of(row), tail = head + (row_bytes - head) / 16 * 16;
         for (int64_t i = at; i < (head + row_bytes - tail) / (int64_t)sizeof(T); i += step) {
             T* const e = reinterpret_cast<T*>(row + (i * (int64_t)sizeof(T) < head ? 0 : tail - head)) + i;
             if (BMMC_WR_OK(e, sizeof(T))) *e = T{};
         }
     };
-    if (rows == 1) clear(out, me, threads);
-    else
-        for (int64_t r = me >> 5; r < rows; r += threads >> 5) clear(out + r * out_stride, threadIdx.x & 31, 32);
-    cudaGridDependencySynchronize();
+    if (rows == 1) {
+        const int64_t words = (row_bytes - head_of(out)) / 16;
+        uint4* const w = reinterpret_cast<uint4*>(out + head_of(out));
+        const int64_t i0 = (int64_t)blockIdx.x * blockDim.x * kClearWords + threadIdx.x;
+#pragma unroll
+        for (int k = 0; k < kClearWords; ++k) {
+            const int64_t i = i0 + k * blockDim.x;
+            if (i < words && BMMC_WR_OK(w + i, 16)) w[i] = uint4{};
+        }
+        if (blockIdx.x == 0) ends(out, threadIdx.x, blockDim.x);
+    } else {
+        const int lane = threadIdx.x & 31;
+        const int64_t r = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+        if (r < rows) {
+            char* const row = out + r * out_stride;
+            uint4* const w = reinterpret_cast<uint4*>(row + head_of(row));
+            for (int64_t i = lane; i < (row_bytes - head_of(row)) / 16; i += 32)
+                if (BMMC_WR_OK(w + i, 16)) w[i] = uint4{};
+            ends(row, lane, 32);
+        }
+    }
+    if (blockIdx.x + 1 == gridDim.x) cudaGridDependencySynchronize();
 }
 
 // ---- host ----------------------------------------------------------------------
@@ -585,7 +600,7 @@ int64_t up16(int64_t bytes) { return (bytes + 15) & ~(int64_t)15; }
 
 // Keys a thread takes where the sort is one cluster; 0: it is not.
 int cluster_rounds(int64_t n) {
-    for (int r : {2, 8, 16})
+    for (int r : {1, 2, 4, 8, 16})
         if (n <= (int64_t)kSortCluster * kSortThreads * r) return r;
     return 0;
 }
@@ -757,7 +772,7 @@ bmmc_status embedding_backward(const void* grad, int64_t grad_stride, const void
     const auto clear = [&](cudaLaunchAttribute* attribute) {
         const bool flat = vocab == 1 || out_stride == hidden;
         const int64_t rows = flat ? 1 : vocab, bytes = (flat ? vocab : 1) * hidden * os;
-        const int64_t blocks = std::min<int64_t>((vocab * hidden * os + 4095) / 4096, kSms * 4);
+        const int64_t blocks = flat ? bytes / (256 * kClearWords * 16) + 1 : (vocab + 7) / 8;
         const auto go = [&](auto kernel) {
             return launch(kernel, dim3((unsigned)blocks), dim3(256), 0, st, attribute, static_cast<char*>(out), out_stride * os,
                           rows, bytes BMMC_SPANS_ARG(spans));
@@ -774,6 +789,8 @@ bmmc_status embedding_backward(const void* grad, int64_t grad_stride, const void
     const auto sorted = [&](const auto* names) {
         using Id = std::remove_cv_t<std::remove_pointer_t<decltype(names)>>;
         switch (cluster_rounds(tokens)) {
+            case 1: return sort_together<Id, 1>(shape, names, tokens, vocab, array(0), array(1), spans, st);
+            case 4: return sort_together<Id, 4>(shape, names, tokens, vocab, array(0), array(1), spans, st);
             case 2: return sort_together<Id, 2>(shape, names, tokens, vocab, array(0), array(1), spans, st);
             case 8: return sort_together<Id, 8>(shape, names, tokens, vocab, array(0), array(1), spans, st);
             case 16: return sort_together<Id, 16>(shape, names, tokens, vocab, array(0), array(1), spans, st);
