@@ -213,13 +213,17 @@ __global__ void __launch_bounds__(held_threads(N)) balance_held_kernel(const Rou
     cudaTriggerProgrammaticLaunchCompletion();
     const Slots<unsigned> routed(s_routed, 32);
     using L = Logits<T, N, WORDS>;
+    // two rows ahead where a warp has one row in words (256 experts in 32 bits: one
+    // ahead 22.2 us, two 21.0; 61 of 16 bits: 14.6 and 17.2)
+    constexpr bool kDeep = FULL && WORDS;
     for (int e = threadIdx.x; e <= E; e += blockDim.x) hist.set(e, 0);
     float acc[N] = {};
     const int64_t lo = (int64_t)blockIdx.x * per_block, hi = min(r.tokens, lo + per_block);
     for (int64_t t0 = lo; t0 < hi; t0 += blockDim.x) {
         Walker w(r, t0, (int)min((int64_t)blockDim.x, hi - t0));
-        L next;
+        L next, after;
         next.load(w.row, w.here() ? E : 0, r.lanes, w.in);
+        if (kDeep) after.load(w.row + w.hop, w.i + w.step < w.n ? E : 0, r.lanes, w.in);
         __syncthreads();
         look_at_choices<true>(r, t0, w.n, routed, hist);
         __syncthreads();
@@ -227,7 +231,12 @@ __global__ void __launch_bounds__(held_threads(N)) balance_held_kernel(const Rou
             const L row = next;
             const bool counts_in = w.here() && is_there(routed, w.i);
             w.next();
-            next.load(w.row, w.here() ? E : 0, r.lanes, w.in);
+            if (kDeep) {
+                next = after;
+                after.load(w.row + w.hop, w.i + w.step < w.n ? E : 0, r.lanes, w.in);
+            } else {
+                next.load(w.row, w.here() ? E : 0, r.lanes, w.in);
+            }
             float v[N];
             const float over = softmax_of<FULL>(row, v, r.lanes);
             if (counts_in) {
@@ -372,7 +381,7 @@ __global__ void __launch_bounds__(1024) balance_join_kernel(const float* __restr
     const Slots<float> part_sums(reinterpret_cast<float*>(s_mem), parts * width);
     const Slots<int> part_counts(s_mem + parts * width, parts * width);
     const auto cluster = cooperative_groups::this_cluster();
-    const int rank = (int)cluster.block_rank(), blocks = (int)gridDim.x;
+    const int rank = (int)cluster.block_rank(), blocks = kCluster;
     cudaGridDependencySynchronize();
     for (int i = threadIdx.x; i < parts * width; i += 1024) {
         const int part = i / width, e = i - part * width;
@@ -386,6 +395,13 @@ __global__ void __launch_bounds__(1024) balance_join_kernel(const float* __restr
         }
         part_sums.set(i, sum), part_counts.set(i, count);
     }
+    __syncthreads();
+    for (int e = threadIdx.x; e < width; e += 1024) {
+        float sum = 0.0f;
+        int count = 0;
+        for (int k = 0; k < parts; ++k) sum += part_sums.get(k * width + e), count += part_counts.get(k * width + e);
+        part_sums.set(e, sum), part_counts.set(e, count);
+    }
     cluster.sync();
     float dot = 0.0f;
     int all = 0, there = 0;
@@ -393,12 +409,10 @@ __global__ void __launch_bounds__(1024) balance_join_kernel(const float* __restr
         for (int e = threadIdx.x; e < width; e += 1024) {
             float sum = 0.0f;
             int count = 0;
-            for (int k = 0; k < parts; ++k) {
-#pragma unroll 8
-                for (int b = 0; b < blocks; ++b) {
-                    if (part_sums.ok(k * width + e)) sum += *cluster.map_shared_rank(part_sums.p + k * width + e, b);
-                    if (part_counts.ok(k * width + e)) count += *cluster.map_shared_rank(part_counts.p + k * width + e, b);
-                }
+#pragma unroll
+            for (int b = 0; b < kCluster; ++b) {
+                if (part_sums.ok(e)) sum += *cluster.map_shared_rank(part_sums.p + e, b);
+                if (part_counts.ok(e)) count += *cluster.map_shared_rank(part_counts.p + e, b);
             }
             if (BMMC_WR_OK(out_counts + e, 4)) out_counts[e] = count;
             if (e == experts) there = count;
@@ -540,7 +554,7 @@ struct Shape {
 };
 
 Shape shape_of(int64_t tokens, int experts) {
-    Shape s{1, kThreads, false, std::max(1, 1024 / (experts + 1))};
+    Shape s{1, kThreads, false, std::min(16, std::max(1, 1024 / (experts + 1)))};
     if (experts > kHeldExperts) {
         const int64_t b = (tokens + kWarps - 1) / kWarps;
         s.blocks = (int)std::min<int64_t>(b < 1 ? 1 : b, 2 * kSms);
@@ -591,7 +605,7 @@ bmmc_status by_held(int type, const Held& h, bool words, F&& f) {
 
 template <class K>
 bool allow(K kernel, size_t smem) {
-    if (smem <= 48 * 1024 || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess)
+    if (smem <= 40 * 1024 || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess)
         return true;
     cudaGetLastError();
     return false;

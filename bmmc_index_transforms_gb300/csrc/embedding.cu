@@ -600,7 +600,7 @@ int64_t up16(int64_t bytes) { return (bytes + 15) & ~(int64_t)15; }
 
 // Keys a thread takes where the sort is one cluster; 0: it is not.
 int cluster_rounds(int64_t n) {
-    for (int r : {1, 2, 4, 8, 16})
+    for (int r : {1, 2, 4})
         if (n <= (int64_t)kSortCluster * kSortThreads * r) return r;
     return 0;
 }
@@ -647,7 +647,7 @@ bmmc_status sort_tokens(const SortShape& s, const Id* ids, int64_t n, int64_t vo
         const int shift = pass * s.digit, from = (pass & 1) ^ 1, to = pass & 1;
         bmmc_status status;
         const auto run = [&](auto in, auto count, auto place) {
-            if (smem > 48 * 1024 && cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+            if (smem > 40 * 1024 && cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
                 cudaGetLastError();
                 return BMMC_ERR_CUDA;
             }
@@ -675,7 +675,7 @@ bmmc_status sort_together(const SortShape& s, const Id* ids, int64_t n, int64_t 
     const int tile = kSortThreads * R, blocks = (int)((n + tile - 1) / tile);
     const size_t smem = ((2 << s.digit) + 32 + (kSortThreads / 64 << s.digit) + 2 * tile) * 4;
     const auto kernel = sort_cluster_kernel<Id, R>;
-    if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+    if (smem > 40 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
         cudaGetLastError();
         return BMMC_ERR_CUDA;
     }
@@ -792,8 +792,6 @@ bmmc_status embedding_backward(const void* grad, int64_t grad_stride, const void
             case 1: return sort_together<Id, 1>(shape, names, tokens, vocab, array(0), array(1), spans, st);
             case 4: return sort_together<Id, 4>(shape, names, tokens, vocab, array(0), array(1), spans, st);
             case 2: return sort_together<Id, 2>(shape, names, tokens, vocab, array(0), array(1), spans, st);
-            case 8: return sort_together<Id, 8>(shape, names, tokens, vocab, array(0), array(1), spans, st);
-            case 16: return sort_together<Id, 16>(shape, names, tokens, vocab, array(0), array(1), spans, st);
         }
         uint32_t *keys[2] = {array(0), array(2)}, *order[2] = {array(1), array(3)};
         key = keys[(shape.passes - 1) & 1], token = order[(shape.passes - 1) & 1];

@@ -86,7 +86,7 @@ struct QuantisedParams {
     MoveParams p;
     Scales scales[2];
     int dims[3];
-    int stage;  // floats of a warp's staged head
+    int stage;  // floats of a warp's staged heads
 };
 
 constexpr int kMostThreads = 256;
@@ -95,14 +95,22 @@ constexpr int kHeadsAtOnce = 2;  // heads whose words a thread has in flight
 // W values times `over` as W codes, written as one word.
 template <class Q, int W>
 __device__ __forceinline__ void put_codes(char* to, const float (&y)[W], float over) {
+    if (!BMMC_WR_OK(to, W)) return;
+    if constexpr (W == 1) {
+        *reinterpret_cast<unsigned char*>(to) = (unsigned char)Q::encode(__fmul_rn(y[0], over), 0.0f);
+        return;
+    } else if constexpr (W == 2) {
+        *reinterpret_cast<unsigned short*>(to) = (unsigned short)Q::encode(__fmul_rn(y[0], over), __fmul_rn(y[1], over));
+        return;
+    } else {
     unsigned c[W / 4];
 #pragma unroll
     for (int i = 0; i < W; i += 4)
         c[i / 4] = Q::encode(__fmul_rn(y[i], over), __fmul_rn(y[i + 1], over)) |
                    Q::encode(__fmul_rn(y[i + 2], over), __fmul_rn(y[i + 3], over)) << 16;
-    if (!BMMC_WR_OK(to, W)) return;
     if constexpr (W == 8) *reinterpret_cast<uint2*>(to) = make_uint2(c[0], c[1]);
     else *reinterpret_cast<unsigned*>(to) = c[0];
+    }
 }
 
 // A word's elements (and, TWO, those half a head on) turned.
@@ -215,7 +223,7 @@ __device__ __forceinline__ void append_part(const QuantisedParams& qp, int64_t t
 // them, which find its largest element by exchange.  Nothing of a head is kept
 // anywhere but in registers.
 template <class T, class Q, bool ADJACENT>
-__global__ void __launch_bounds__(kMostThreads, 3) append_words_kernel(const __grid_constant__ QuantisedParams qp BMMC_SPANS_PARAM) {
+__global__ void __launch_bounds__(kMostThreads, 4) append_words_kernel(const __grid_constant__ QuantisedParams qp BMMC_SPANS_PARAM) {
     extern __shared__ float2 s_turn[];  // [tokens of the block][pairs] cos, sin
     __shared__ int64_t s_place[2][kMaxTokensPerBlock];
     __shared__ float s_position[kMaxTokensPerBlock];
@@ -292,91 +300,190 @@ bmmc_status launch_append_words(QuantisedParams& qp, const chk::Spans& spans, cu
     return launch(kernel, grid, dim3(threads), (size_t)per_block * p.pairs * sizeof(float2), st, nullptr, qp BMMC_SPANS_ARG(spans));
 }
 
-// Any heads: a warp turns a head, an element a lane, stages it in shared
-// memory in 32 bits, and writes its values with their scale.
-template <class T, class Q>
-__global__ void __launch_bounds__(kThreads) append_heads_kernel(const __grid_constant__ QuantisedParams qp BMMC_SPANS_PARAM) {
-    extern __shared__ float2 s_turn[];  // [tokens of the block][pairs] cos, sin; then a head a warp
+// W floats of shared memory as words of up to 16 bytes, which warps move without
+// meeting in a bank.
+template <int W>
+struct FloatWord;
+template <> struct FloatWord<8> { using type = float4; };
+template <> struct FloatWord<4> { using type = float4; };
+template <> struct FloatWord<2> { using type = float2; };
+template <> struct FloatWord<1> { using type = float; };
+
+constexpr int kRowFloats = 1024;  // of a warp's heads in shared memory, or one head
+constexpr int kRowBatch = 32;     // most heads of a warp at a time
+
+// Any heads, in words of W elements: a warp brings some heads into shared memory
+// in 32 bits, turns their pairs there by element, finds their scales, and writes
+// them in words of W codes.
+template <class T, class Q, int W>
+__global__ void __launch_bounds__(kThreads) append_rows_kernel(const __grid_constant__ QuantisedParams qp BMMC_SPANS_PARAM) {
+    extern __shared__ float4 s_stage[];  // a warp's heads each, then [tokens of the block][pairs] cos, sin
     __shared__ int64_t s_place[2][kMaxTokensPerBlock];
     __shared__ float s_position[kMaxTokensPerBlock];
     __shared__ int s_slot[2][kMaxTokensPerBlock];
-    BMMC_SPANS_ENTER(s_turn, chk::dyn_smem_bytes(), s_place, sizeof(s_place), s_position, sizeof(s_position), s_slot,
-                     sizeof(s_slot));
-    using Code = typename Q::Code;
+    __shared__ struct {
+        const char* src[kRowBatch];
+        char* dst[kRowBatch];      // NULL: not written
+        float* scale[kRowBatch];   // where it goes
+        float over[kRowBatch];
+        int turns[kRowBatch];      // where its token's turns start
+    } s_rows[kWarps];
+    BMMC_SPANS_ENTER(s_stage, chk::dyn_smem_bytes(), s_place, sizeof(s_place), s_position, sizeof(s_position), s_slot,
+                     sizeof(s_slot), s_rows, sizeof(s_rows));
+    using F = typename FloatWord<W>::type;
+    constexpr int kF = W * 4 / (int)sizeof(F);  // words of floats
+    using Word = Pack<T, W>;
     const MoveParams& p = qp.p;
-    const int tid = threadIdx.x, lane = tid & 31, per_block = blockDim.x >> p.group_log2;
-    const Slots<float2> turns(s_turn, per_block * p.pairs);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, per_block = blockDim.x >> p.group_log2;
+    const Slots<float4> all(s_stage, kWarps * qp.stage / 4 + (per_block * p.pairs + 1) / 2);
+    const Slots<float2> turns(reinterpret_cast<float2*>(s_stage + kWarps * qp.stage / 4), per_block * p.pairs);
+    const Slots<float> stage(reinterpret_cast<float*>(s_stage) + warp * qp.stage, qp.stage);
+    const Slots<F> staged(reinterpret_cast<F*>(s_stage + warp * qp.stage / 4), qp.stage * 4 / (int)sizeof(F));
     const Slots<int64_t> places(&s_place[0][0], 2 * kMaxTokensPerBlock);
     const Slots<float> place_numbers(s_position, kMaxTokensPerBlock);
     const Slots<int> slots(&s_slot[0][0], 2 * kMaxTokensPerBlock);
-    const Slots<float> stage(reinterpret_cast<float*>(s_turn + per_block * p.pairs) + (tid >> 5) * qp.stage, qp.stage);
+    auto& mine = s_rows[warp];
+    const Slots<const char*> src(mine.src, kRowBatch);
+    const Slots<char*> dst(mine.dst, kRowBatch);
+    const Slots<float*> scales(mine.scale, kRowBatch);
+    const Slots<float> over(mine.over, kRowBatch);
+    const Slots<int> turns_of(mine.turns, kRowBatch);
     const int64_t t0 = (int64_t)blockIdx.x * per_block;
     const int nt = (int)min((int64_t)per_block, p.tokens - t0);
-    begin_block(p, t0, nt, 0, p.parts, turns, places, place_numbers, slots);
-    int rows = 0;
-    for (int q = 0; q < p.parts; ++q) rows += nt * p.part[q].heads;
-    for (int r = tid >> 5; r < rows; r += kWarps) {
-        int q = 0, i = r;
-        while (i >= nt * p.part[q].heads) i -= nt * p.part[q++].heads;
+    const int first_part = gridDim.y > 1 ? blockIdx.y : 0, last_part = gridDim.y > 1 ? first_part + 1 : p.parts;
+    begin_block(p, t0, nt, first_part, last_part, turns, places, place_numbers, slots);
+    for (int q = first_part; q < last_part; ++q) {
         const Heads& h = p.part[q];
-        const int k = i / h.heads, head = i - k * h.heads, dim = qp.dims[q], pairs = h.turned ? p.pairs : 0;
-        const int64_t to = h.place ? places.get((h.place - 1) * kMaxTokensPerBlock + k) : (t0 + k) * h.dst_token;
-        if (to < 0) continue;
-        const T* const src = reinterpret_cast<const T*>(h.src + (t0 + k) * h.src_token + head * h.src_head);
-        char* const dst = h.dst + to + head * h.dst_head;
-        const auto value = [&](int e) { return BMMC_RD_OK(src + e, sizeof(T)) ? to_f32(src[e]) : 0.0f; };
-        const auto keep = [&](int e, float y) {
-            if (h.place) stage.set(e, y);
-            else if (BMMC_WR_OK(dst + e * sizeof(T), sizeof(T))) reinterpret_cast<T*>(dst)[e] = from_f32<T>(y);
-        };
-        float most = 0.0f;
-        // (queries turned in place: a pair's elements are read before they are written)
-        for (int j = lane; j < pairs; j += 32) {
-            const int a = p.adjacent ? 2 * j : j, b = a + (p.adjacent ? 1 : pairs);
-            const float2 turn = turns.get(k * p.pairs + j);
-            const float x = value(a), y = value(b), u = turned_first(x, y, turn), v = turned_second(x, y, turn);
-            keep(a, u), keep(b, v);
-            most = larger(larger(most, u), v);
+        const int dim = qp.dims[q];
+        for (int r0 = warp * h.batch; r0 < nt * h.heads; r0 += kWarps * h.batch) {
+            const int rows = min(h.batch, nt * h.heads - r0);
+            if (lane < rows) {
+                const int k = (r0 + lane) / h.heads, head = r0 + lane - k * h.heads;
+                const int64_t to = h.place ? places.get((h.place - 1) * kMaxTokensPerBlock + k) : (t0 + k) * h.dst_token;
+                src.set(lane, h.src + (t0 + k) * h.src_token + head * h.src_head);
+                dst.set(lane, to < 0 ? nullptr : h.dst + to + head * h.dst_head);
+                turns_of.set(lane, k * p.pairs);
+                if (h.place && to >= 0)
+                    scales.set(lane, qp.scales[h.place - 1].at(slots.get(k), slots.get(kMaxTokensPerBlock + k), head));
+            }
+            __syncwarp();
+#pragma unroll 4
+            for (int x = lane; x < rows * h.words; x += 32) {
+                const int row = h.words == 1 ? x : (int)__umulhi(x, h.words_magic);
+                const char* const from = src.get(row) + (x - row * h.words) * (int)sizeof(Word);
+                Word y;
+                if (BMMC_RD_OK(from, sizeof(Word))) y.load(from);
+#pragma unroll
+                for (int i = 0; i < kF; ++i) {
+                    F f;
+                    float* const v = reinterpret_cast<float*>(&f);
+#pragma unroll
+                    for (int j = 0; j < W / kF; ++j) v[j] = y.get(i * (W / kF) + j);
+                    staged.set(x * kF + i, f);
+                }
+            }
+            __syncwarp();
+            if (h.turned && p.pairs) {
+#pragma unroll 2
+                for (int x = lane; x < rows * p.pairs; x += 32) {
+                    const int row = quotient(x, p.pairs, p.pairs_magic), i = x - row * p.pairs;
+                    const int a = row * dim + (p.adjacent ? 2 * i : i), b = a + (p.adjacent ? 1 : p.pairs);
+                    const float2 r = turns.get(turns_of.get(row) + i);
+                    const float u = stage.get(a), v = stage.get(b);
+                    stage.set(a, turned_first(u, v, r));
+                    stage.set(b, turned_second(u, v, r));
+                }
+                __syncwarp();
+            }
+            if (h.place) {
+#pragma unroll 2
+                for (int row = 0; row < rows; ++row) {
+                    float most = 0.0f;
+                    for (int e = lane; e < dim; e += 32) most = larger(most, stage.get(row * dim + e));
+                    for (int d = 16; d; d >>= 1) most = larger(most, __shfl_xor_sync(~0u, most, d));
+                    if (lane == 0) {
+                        const float scale = scale_of<Q>(most);
+                        over.set(row, __frcp_rn(scale));
+                        float* const to = scales.get(row);
+                        if (dst.get(row) && BMMC_WR_OK(to, 4)) *to = scale;
+                    }
+                }
+                __syncwarp();
+            }
+#pragma unroll 2
+            for (int x = lane; x < rows * h.words; x += 32) {
+                const int row = h.words == 1 ? x : (int)__umulhi(x, h.words_magic);
+                char* const row_to = dst.get(row);
+                if (!row_to) continue;
+                float v[W];
+#pragma unroll
+                for (int i = 0; i < kF; ++i) {
+                    const F f = staged.get(x * kF + i);
+#pragma unroll
+                    for (int j = 0; j < W / kF; ++j) v[i * (W / kF) + j] = reinterpret_cast<const float*>(&f)[j];
+                }
+                if (h.place) {
+                    put_codes<Q, W>(row_to + (x - row * h.words) * W, v, over.get(row));
+                } else {
+                    Word y;
+                    y.set(v);
+                    char* const to = row_to + (x - row * h.words) * (int)sizeof(Word);
+                    if (BMMC_WR_OK(to, sizeof(Word))) y.store(to);
+                }
+            }
+            __syncwarp();
         }
-        for (int e = 2 * pairs + lane; e < dim; e += 32) {
-            const float y = value(e);
-            keep(e, y);
-            most = larger(most, y);
-        }
-        if (!h.place) continue;
-        for (int d = 16; d; d >>= 1) most = larger(most, __shfl_xor_sync(~0u, most, d));
-        const float scale = scale_of<Q>(most), over = __frcp_rn(scale);
-        __syncwarp();
-        for (int e = lane; e < dim; e += 32)
-            if (BMMC_WR_OK(dst + e, 1)) reinterpret_cast<Code*>(dst)[e] = (Code)Q::encode(__fmul_rn(stage.get(e), over), 0.0f);
-        float* const s = qp.scales[h.place - 1].at(slots.get(k), slots.get(kMaxTokensPerBlock + k), head);
-        if (lane == 0 && BMMC_WR_OK(s, 4)) *s = scale;
-        __syncwarp();
     }
 }
 
-template <class T, class Q>
-bmmc_status launch_append(QuantisedParams& qp, const chk::Spans& spans, cudaStream_t st) {
+template <class T, class Q, int W>
+bmmc_status launch_append_rows(QuantisedParams& qp, const chk::Spans& spans, cudaStream_t st) {
     (void)spans;
     MoveParams& p = qp.p;
     int per_block = p.tokens >= kSms * 32 ? 4 : 1;
     while (per_block > 1 && per_block * p.pairs * sizeof(float2) > 32 * 1024) per_block >>= 1;
-    p.group_log2 = per_block == 4 ? 5 : per_block == 2 ? 6 : 7;
-    qp.stage = std::max(qp.dims[0], qp.dims[1]);
-    const size_t smem = (size_t)per_block * p.pairs * sizeof(float2) + (size_t)kWarps * qp.stage * 4;
-    const auto kernel = append_heads_kernel<T, Q>;
+    p.group_log2 = 0;  // threads of a token: the kernel takes as many tokens as there is room for turns
+    while ((kThreads >> p.group_log2) > per_block) ++p.group_log2;
+    qp.stage = kRowFloats;
+    for (int q = 0; q < p.parts; ++q) qp.stage = std::max(qp.stage, (qp.dims[q] + 3) & ~3);
+    for (int q = 0; q < p.parts; ++q) {
+        Heads& h = p.part[q];
+        h.words = qp.dims[q] / W;
+        h.words_magic = (unsigned)((((uint64_t)1 << 32) + h.words - 1) / h.words);
+        // no more heads a warp than its share
+        h.batch = std::max(1, std::min({qp.stage / qp.dims[q], kRowBatch, (per_block * h.heads + kWarps - 1) / kWarps}));
+        const bool dense = p.device && W * sizeof(T) == 16 && (h.heads < 2 || h.src_head == (int64_t)qp.dims[q] * (int)sizeof(T));
+        h.ahead = dense ? std::min((unsigned)(h.heads * qp.dims[q] * sizeof(T)), 65536u) : 0u;
+    }
+    const size_t smem = (size_t)kWarps * qp.stage * 4 + (size_t)per_block * p.pairs * sizeof(float2);
+    const auto kernel = append_rows_kernel<T, Q, W>;
     if (smem > 40 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
         cudaGetLastError();
         return BMMC_ERR_CUDA;
     }
-    return launch(kernel, dim3((unsigned)((p.tokens + per_block - 1) / per_block)), dim3(kThreads), smem, st, nullptr,
-                  qp BMMC_SPANS_ARG(spans));
+    const bool split = p.tokens * p.parts <= kSms * 8;
+    return launch(kernel, dim3((unsigned)((p.tokens + per_block - 1) / per_block), split ? p.parts : 1), dim3(kThreads), smem, st,
+                  nullptr, qp BMMC_SPANS_ARG(spans));
+}
+
+// Words of as many elements as bits (of the heads, es bytes each) and cache_bits
+// (of the caches) are multiples of.
+template <class T, class Q>
+bmmc_status launch_append(QuantisedParams& qp, uint64_t bits, uint64_t cache_bits, const chk::Spans& spans, cudaStream_t st) {
+    constexpr int es = sizeof(T);
+    int W = word_bytes(es, {bits}) / es;
+    while (W > 1 && (cache_bits & (uint64_t)(W - 1))) W >>= 1;
+    if constexpr (es == 2)
+        if (W == 8) return launch_append_rows<T, Q, 8>(qp, spans, st);
+    if (W == 4) return launch_append_rows<T, Q, 4>(qp, spans, st);
+    return W == 2 ? launch_append_rows<T, Q, 2>(qp, spans, st) : launch_append_rows<T, Q, 1>(qp, spans, st);
 }
 
 // ---- read ----------------------------------------------------------------------
 
 constexpr int kReadThreads = 256;
-constexpr int kReadRows = 8;   // rows of a block, at most
+constexpr int kReadRows = 64;  // rows of a block, at most
+constexpr int kReadEach = 8;   // rows of a thread, at most
 constexpr int kReadAhead = 4;  // rows whose words a thread has in flight
 
 struct ReadParams {
@@ -436,8 +543,9 @@ struct Coded {
 };
 
 // A block takes some rows: its warps find their places, then a thread takes the
-// same word of each, several rows at a time.  Pure movement.
-template <class T, class Q, int W>
+// same word of each (SIDE: of some; the others go to threads beside it), several
+// rows at a time.  Pure movement.
+template <class T, class Q, int W, bool SIDE>
 __global__ void __launch_bounds__(kReadThreads) read_words_kernel(const __grid_constant__ ReadParams rp BMMC_SPANS_PARAM) {
     __shared__ int64_t s_place[2][kReadRows];
     __shared__ int s_page[kReadRows], s_slot[kReadRows];
@@ -447,10 +555,10 @@ __global__ void __launch_bounds__(kReadThreads) read_words_kernel(const __grid_c
     const Slots<int64_t> places(&s_place[0][0], 2 * kReadRows);
     const Slots<int> pages(s_page, kReadRows), slots(s_slot, kReadRows);
     const MoveParams& p = rp.p;
-    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int tid = threadIdx.y * blockDim.x + threadIdx.x, lane = tid & 31, warps = (int)(blockDim.x * blockDim.y) >> 5;
     const int64_t t0 = (int64_t)blockIdx.x * rp.rows;
     const int n = (int)min((int64_t)rp.rows, p.tokens - t0);
-    for (int i = threadIdx.x >> 5; i < n; i += warps) {
+    for (int i = tid >> 5; i < n; i += warps) {
         const Place place = place_of(p, t0 + i, find_sequence_warp(p.starts, p.sequences, t0 + i, lane));
         if (lane == 0) {
             places.set(i, place.byte[0]), places.set(kReadRows + i, place.byte[1]);
@@ -464,32 +572,33 @@ __global__ void __launch_bounds__(kReadThreads) read_words_kernel(const __grid_c
         for (int j = threadIdx.x; j < h.heads * rp.words[q]; j += blockDim.x) {
             const int head = rp.words[q] == 1 ? j : (int)__umulhi(j, rp.magic[q]), at = (j - head * rp.words[q]) * W;
             const char* const src = h.src + head * h.src_head + at * (Word::kBytes / W);
-            char* to = h.dst + t0 * h.dst_token + head * h.dst_head + at * (int)sizeof(T);
-            for (int r = 0; r < n; r += kReadAhead) {
+            const int first = SIDE ? threadIdx.y : 0, step = SIDE ? blockDim.y : 1;
+            char* to = h.dst + (t0 + first) * h.dst_token + head * h.dst_head + at * (int)sizeof(T);
+            for (int r = first; r < n; r += kReadAhead * step) {
                 Word word[kReadAhead];
                 float scale[kReadAhead];
                 bool there[kReadAhead];
 #pragma unroll
                 for (int u = 0; u < kReadAhead; ++u) {
-                    const int page = r + u < n ? pages.get(r + u) : -1;
+                    const int i = r + u * step, page = i < n ? pages.get(i) : -1;
                     there[u] = page >= 0;
-                    const char* const from = src + (there[u] ? places.get(q * kReadRows + r + u) : 0);
+                    const char* const from = src + (there[u] ? places.get(q * kReadRows + i) : 0);
                     there[u] = there[u] && BMMC_RD_OK(from, Word::kBytes);
                     if (there[u]) word[u].load(from);
                     scale[u] = 0.0f;
                     if (kCoded && there[u]) {
-                        const float* const s = rp.scales[q].at(page, slots.get(r + u), head);
+                        const float* const s = rp.scales[q].at(page, slots.get(i), head);
                         if (BMMC_RD_OK(s, 4)) scale[u] = *s;
                     }
                 }
 #pragma unroll
                 for (int u = 0; u < kReadAhead; ++u) {
-                    if (r + u >= n) break;
+                    if (r + u * step >= n) break;
                     Pack<T, W> y;
                     if (there[u]) y = word[u].value(scale[u]);
                     else y.word = typename Pack<T, W>::Word{};
                     if (BMMC_WR_OK(to, sizeof(y))) y.store(to);
-                    to += h.dst_token;
+                    to += step * h.dst_token;
                 }
             }
         }
@@ -508,11 +617,14 @@ bmmc_status launch_read_words(ReadParams& rp, const chk::Spans& spans, cudaStrea
         rp.magic[q] = (unsigned)((((uint64_t)1 << 32) + rp.words[q] - 1) / rp.words[q]);
         most = std::max(most, rp.p.part[q].heads * rp.words[q]);
     }
-    int threads = 32;
-    while (threads < kReadThreads && threads < most) threads <<= 1;
-    rp.rows = 1;  // more where the blocks still fill the machine
-    while (rp.rows < kReadRows && tokens * threads >= kSms * 2048 * rp.rows * 2) rp.rows <<= 1;
-    return launch(read_words_kernel<T, Q, W>, dim3((unsigned)((tokens + rp.rows - 1) / rp.rows)), dim3(threads), 0, st, nullptr,
+    // threads of a row, and rows side by side; several rows a thread where the
+    // blocks still fill the machine
+    int x = 8, each = 1;
+    while (x < kReadThreads && x < most) x <<= 1;
+    const int y = std::max(1, 64 / x);
+    while (each < kReadEach && tokens * x >= kSms * 2048 * each * 2) each <<= 1;
+    rp.rows = y * each;
+    return launch(y > 1 ? read_words_kernel<T, Q, W, true> : read_words_kernel<T, Q, W, false>, dim3((unsigned)((tokens + rp.rows - 1) / rp.rows)), dim3(x, y), 0, st, nullptr,
                   rp BMMC_SPANS_ARG(spans));
 }
 
@@ -602,7 +714,8 @@ bmmc_status paged_append_quantised(const paged_append_quantised_args_t* args, vo
     }
     return by_cache_type(type, args->cache_type, [&](auto t, auto q) {
         if (words) return launch_append_words<decltype(t), decltype(q)>(qp, spans, static_cast<cudaStream_t>(stream));
-        return launch_append<decltype(t), decltype(q)>(qp, spans, static_cast<cudaStream_t>(stream));
+        return launch_append<decltype(t), decltype(q)>(qp, c.in_bits | c.q_bits, c.cache_bits | c.dims[0] | c.dims[1], spans,
+                                                       static_cast<cudaStream_t>(stream));
     });
 }
 
