@@ -211,6 +211,9 @@ __global__ void __launch_bounds__(held_threads(N)) balance_held_kernel(const Rou
     const Slots<int> mem(s_mem, (warps + 1) * E + 1), hist = mem.part(0, E + 1);  // counts; [E]: tokens
     const Slots<float> all(reinterpret_cast<float*>(s_mem + E + 1), warps * E);    // each warp's sums
     cudaTriggerProgrammaticLaunchCompletion();
+    const Slots<float> dots(s_dot, 32);
+    const Slots<int> alls(s_all, 32);
+    const Slots<int> theres(s_there, 32);
     const Slots<unsigned> routed(s_routed, 32);
     using L = Logits<T, N, WORDS>;
     // two rows ahead where a warp has one row in words (256 experts in 32 bits: one
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(held_threads(N)) balance_held_kernel(const Rou
     }
     if (gridDim.x > 1) cluster.sync();  // no block leaves while its sums are read
     if (cluster.block_rank() == 0)
-        finish_loss(dot, choices, there, E, loss, Slots<float>(s_dot, 32), Slots<int>(s_all, 32), Slots<int>(s_there, 32));
+        finish_loss(dot, choices, there, E, loss, dots, alls, theres);
 }
 
 // More experts: by a warp a row, whose logits are read three times, the sums
@@ -378,6 +381,9 @@ __global__ void __launch_bounds__(1024) balance_join_kernel(const float* __restr
     __shared__ int s_all[32], s_there[32];
     BMMC_SPANS_ENTER(s_mem, chk_dynamic_bytes(), s_dot, sizeof(s_dot), s_all, sizeof(s_all), s_there, sizeof(s_there));
     const int width = experts + 1;
+    const Slots<float> dots(s_dot, 32);
+    const Slots<int> alls(s_all, 32);
+    const Slots<int> theres(s_there, 32);
     const Slots<float> part_sums(reinterpret_cast<float*>(s_mem), parts * width);
     const Slots<int> part_counts(s_mem + parts * width, parts * width);
     const auto cluster = cooperative_groups::this_cluster();
@@ -421,7 +427,7 @@ __global__ void __launch_bounds__(1024) balance_join_kernel(const float* __restr
     }
     cluster.sync();  // no block leaves while its sums are read
     if (rank == 0)
-        finish_loss(dot, all, there, experts, loss, Slots<float>(s_dot, 32), Slots<int>(s_all, 32), Slots<int>(s_there, 32));
+        finish_loss(dot, all, there, experts, loss, dots, alls, theres);
 }
 
 // The counts' sum, by a block: all of its threads take part.
@@ -453,10 +459,11 @@ __global__ void __launch_bounds__(256) balance_backward_held_kernel(const float*
     __shared__ unsigned s_routed[8];
     BMMC_SPANS_ENTER(s_all, sizeof(s_all), s_routed, sizeof(s_routed));
     const Slots<unsigned> routed(s_routed, 8);
+    const Slots<int> alls(s_all, 8);
     using L = Logits<T, N, WORDS>;
     const int E = r.experts;
     const int64_t lo = (int64_t)blockIdx.x * per_block, hi = min(r.tokens, lo + per_block);
-    const int all = sum_of_counts(counts, E, Slots<int>(s_all, 8));
+    const int all = sum_of_counts(counts, E, alls);
     const float factor = factor_of(grad, counts, E), each = all ? 1.0f / (float)all : 0.0f;
     const int in = threadIdx.x & (r.lanes - 1);
     float f[N];
@@ -510,7 +517,8 @@ __global__ void __launch_bounds__(kThreads) balance_backward_long_kernel(const f
     BMMC_SPANS_ENTER(s_mem, chk_dynamic_bytes(), s_all, sizeof(s_all));
     const int E = r.experts, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Slots<float> share(reinterpret_cast<float*>(s_mem), E);
-    const int all = sum_of_counts(counts, E, Slots<int>(s_all, kWarps));
+    const Slots<int> alls(s_all, kWarps);
+    const int all = sum_of_counts(counts, E, alls);
     const float factor = factor_of(grad, counts, E), each = all ? 1.0f / (float)all : 0.0f;
     for (int e = threadIdx.x; e < E; e += kThreads) share.set(e, count_at(counts, e) * each);
     __syncthreads();

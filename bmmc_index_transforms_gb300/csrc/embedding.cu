@@ -399,7 +399,8 @@ __global__ void __launch_bounds__(kSumThreads) sum_rows_kernel(const char* __res
     __shared__ int s_key[2 * kChunk + 1], s_token[2 * kChunk];
     __shared__ float s_sum[WORDS ? 1 : kSumThreads * W];
     BMMC_SPANS_ENTER(s_key, sizeof(s_key), s_token, sizeof(s_token), s_sum, sizeof(s_sum));
-    const Slots<int> ids(s_key, 2 * kChunk + 1), tokens(s_token, 2 * kChunk);
+    const Slots<int> ids(s_key, 2 * kChunk + 1);
+    const Slots<int> tokens(s_token, 2 * kChunk);
     const Slots<float> sums(s_sum, WORDS ? 1 : kSumThreads * W);
     cudaTriggerProgrammaticLaunchCompletion();  // the join waits for the sums by itself
     const Runs runs{keys, n};

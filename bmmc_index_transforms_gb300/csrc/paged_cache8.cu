@@ -83,7 +83,7 @@ struct Scales {
 // ---- append --------------------------------------------------------------------
 
 struct QuantisedParams {
-    MoveParams p;
+    MoveParams moves;
     Scales scales[2];
     int dims[3];
     int stage;  // floats of a warp's staged heads
@@ -145,7 +145,7 @@ __device__ __forceinline__ void append_part(const QuantisedParams& qp, int64_t t
     constexpr bool kTurned = PART != 1, kPlaced = PART != 2;
     constexpr bool kTwo = kTurned && !ADJACENT;  // an item that is turned has two words
     constexpr int kTurns = kTwo ? W : W / 2;
-    const MoveParams& p = qp.p;
+    const MoveParams& p = qp.moves;
     const Heads& h = p.part[PART];
     const int down = (in * h.magic) >> 16, step = (1 << p.group_log2) / h.across, j0 = in - down * h.across;
     there = there && down < step;
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kMostThreads, 4) append_words_kernel(const __g
     __shared__ int s_slot[2][kMaxTokensPerBlock];
     BMMC_SPANS_ENTER(s_turn, chk::dyn_smem_bytes(), s_place, sizeof(s_place), s_position, sizeof(s_position), s_slot,
                      sizeof(s_slot));
-    const MoveParams& p = qp.p;
+    const MoveParams& p = qp.moves;
     const int tid = threadIdx.x, per_block = blockDim.x >> p.group_log2;
     const Slots<float2> turns(s_turn, per_block * p.pairs);
     const Slots<int64_t> places(&s_place[0][0], 2 * kMaxTokensPerBlock);
@@ -262,7 +262,7 @@ template <class T, class Q>
 bmmc_status launch_append_words(QuantisedParams& qp, const chk::Spans& spans, cudaStream_t st) {
     (void)spans;
     constexpr int W = 16 / sizeof(T);
-    MoveParams& p = qp.p;
+    MoveParams& p = qp.moves;
     int64_t most = std::max(1, p.pairs / kAhead);
     int least = 2;
     for (int q = 0; q < p.parts; ++q) {
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kThreads) append_rows_kernel(const __grid_cons
     using F = typename FloatWord<W>::type;
     constexpr int kF = W * 4 / (int)sizeof(F);  // words of floats
     using Word = Pack<T, W>;
-    const MoveParams& p = qp.p;
+    const MoveParams& p = qp.moves;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, per_block = blockDim.x >> p.group_log2;
     const Slots<float4> all(s_stage, kWarps * qp.stage / 4 + (per_block * p.pairs + 1) / 2);
     const Slots<float2> turns(reinterpret_cast<float2*>(s_stage + kWarps * qp.stage / 4), per_block * p.pairs);
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kThreads) append_rows_kernel(const __grid_cons
 template <class T, class Q, int W>
 bmmc_status launch_append_rows(QuantisedParams& qp, const chk::Spans& spans, cudaStream_t st) {
     (void)spans;
-    MoveParams& p = qp.p;
+    MoveParams& p = qp.moves;
     int per_block = p.tokens >= kSms * 32 ? 4 : 1;
     while (per_block > 1 && per_block * p.pairs * sizeof(float2) > 32 * 1024) per_block >>= 1;
     p.group_log2 = 0;  // threads of a token: the kernel takes as many tokens as there is room for turns
@@ -487,7 +487,7 @@ constexpr int kReadEach = 8;   // rows of a thread, at most
 constexpr int kReadAhead = 4;  // rows whose words a thread has in flight
 
 struct ReadParams {
-    MoveParams p;  // part[0], part[1]: from the caches to the rows; lengths: each sequence's first entry
+    MoveParams moves;  // part[0], part[1]: from the caches to the rows; lengths: each sequence's first entry
     Scales scales[2];
     int dims[2];
     int rows;           // of a block
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kReadThreads) read_words_kernel(const __grid_c
     using Word = std::conditional_t<kCoded, Coded<T, Q, W>, Held<T, Q, W>>;
     const Slots<int64_t> places(&s_place[0][0], 2 * kReadRows);
     const Slots<int> pages(s_page, kReadRows), slots(s_slot, kReadRows);
-    const MoveParams& p = rp.p;
+    const MoveParams& p = rp.moves;
     const int tid = threadIdx.y * blockDim.x + threadIdx.x, lane = tid & 31, warps = (int)(blockDim.x * blockDim.y) >> 5;
     const int64_t t0 = (int64_t)blockIdx.x * rp.rows;
     const int n = (int)min((int64_t)rp.rows, p.tokens - t0);
@@ -610,12 +610,12 @@ __global__ void __launch_bounds__(kReadThreads) read_words_kernel(const __grid_c
 template <class T, class Q, int W>
 bmmc_status launch_read_words(ReadParams& rp, const chk::Spans& spans, cudaStream_t st) {
     (void)spans;
-    const int64_t tokens = rp.p.tokens;
+    const int64_t tokens = rp.moves.tokens;
     int most = 1;
     for (int q = 0; q < 2; ++q) {
         rp.words[q] = rp.dims[q] / W;
         rp.magic[q] = (unsigned)((((uint64_t)1 << 32) + rp.words[q] - 1) / rp.words[q]);
-        most = std::max(most, rp.p.part[q].heads * rp.words[q]);
+        most = std::max(most, rp.moves.part[q].heads * rp.words[q]);
     }
     // threads of a row, and rows side by side; several rows a thread where the
     // blocks still fill the machine
@@ -697,9 +697,10 @@ bmmc_status paged_append_quantised(const paged_append_quantised_args_t* args, vo
             return BMMC_ERR_ALIAS;
     }
     if (may_overlap(scales[0], scales[1])) return BMMC_ERR_ALIAS;
+    if ((s = append_reachable(a, device)) != BMMC_OK) return s;
     if ((s = all_reachable(device, {args->k_scales.data, args->v_scales.data})) != BMMC_OK) return s;
-    qp.p = c.moves;
-    qp.p.adjacent = a.turns.flags & ROTARY_ADJACENT;
+    qp.moves = c.moves;
+    qp.moves.adjacent = a.turns.flags & ROTARY_ADJACENT;
     for (int i = 0; i < 3; ++i) qp.dims[i] = c.dims[i];
     const chk::Spans spans = spans_of({c.k, c.v, c.q, turn_rows(a.turns, a.tokens, 0), turn_rows(a.turns, a.tokens, 1),
                                        turn_rows(a.turns, a.tokens, 2), c.maps[0], c.maps[1], c.maps[2]},
@@ -709,7 +710,7 @@ bmmc_status paged_append_quantised(const paged_append_quantised_args_t* args, vo
     bool words = word_bytes(es, {c.in_bits, c.q_bits, pair_bits(a.turns, es)}) == 16 &&
                  !(c.cache_bits & (uint64_t)(W - 1));
     for (int i = 0; i < 2; ++i) {
-        const int64_t two = i == 0 && !qp.p.adjacent ? a.turns.pairs : 0;  // elements in an item's second word
+        const int64_t two = i == 0 && !qp.moves.adjacent ? a.turns.pairs : 0;  // elements in an item's second word
         words = words && (c.dims[i] - two) / W <= 32;
     }
     return by_cache_type(type, args->cache_type, [&](auto t, auto q) {
@@ -737,7 +738,7 @@ bmmc_status paged_read(const paged_read_args_t* a, void* stream) {
     const token_heads_t* to[2] = {&a->k, &a->v};
     const paged_cache_t *cache[2] = {&a->k_cache, &a->v_cache}, *scale[2] = {&a->k_scales, &a->v_scales};
     ReadParams rp{};
-    MoveParams& p = rp.p;
+    MoveParams& p = rp.moves;
     Rows in[7] = {}, out[2];
     uint64_t cache_bits = 0, out_bits = 0;
     bmmc_status s;

@@ -316,6 +316,12 @@ struct AppendCall {
     uint64_t in_bits = 0, cache_bits = 0, q_bits = 0;  // addresses and strides in bytes, or'ed
 };
 
+// The last check: whether the GPU reaches the arrays.
+inline bmmc_status append_reachable(const paged_append_args_t& a, bool device) {
+    return all_reachable(device, {a.k.data, a.v.data, a.q.data, a.q_out.data, a.k_cache.data, a.v_cache.data, a.starts, a.lengths,
+                                  a.table, a.turns.inv_freq, a.turns.pair_axes, a.turns.positions});
+}
+
 // es: bytes of an element of the new heads, cache_es: of the caches.
 inline bmmc_status read_append(const paged_append_args_t& a, int es, int cache_es, bool device, AppendCall& c) {
     MoveParams& p = c.moves;
@@ -370,9 +376,6 @@ inline bmmc_status read_append(const paged_append_args_t& a, int es, int cache_e
         for (const Rows& m : c.maps)
             if (may_overlap(m, w)) return BMMC_ERR_ALIAS;
     }
-    if ((s = all_reachable(device, {a.k.data, a.v.data, a.q.data, a.q_out.data, a.k_cache.data, a.v_cache.data, a.starts,
-                                    a.lengths, a.table, a.turns.inv_freq, a.turns.pair_axes, a.turns.positions})) != BMMC_OK)
-        return s;
     for (int i = 0; i < 2; ++i) {
         Heads& h = p.part[p.parts++];
         h = heads_of(*from[i], es, i == 0);

@@ -372,7 +372,8 @@ bmmc_status paged_append(const paged_append_args_t* a, void* stream) {
     if (!es) return BMMC_ERR_UNSUPPORTED_ELEM;
     if (!a->tokens) return BMMC_OK;
     AppendCall c;
-    const bmmc_status s = read_append(*a, es, es, device, c);
+    bmmc_status s = read_append(*a, es, es, device, c);
+    if (s == BMMC_OK) s = append_reachable(*a, device);
     if (s != BMMC_OK) return s;
     const uint64_t bits = c.in_bits | c.cache_bits | c.q_bits;
     const chk::Spans spans = spans_of({c.k, c.v, c.q, turn_rows(a->turns, a->tokens, 0), turn_rows(a->turns, a->tokens, 1),
