@@ -611,14 +611,6 @@ bmmc_status by_held(int type, const Held& h, bool words, F&& f) {
     });
 }
 
-template <class K>
-bool allow(K kernel, size_t smem) {
-    if (smem <= 40 * 1024 || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess)
-        return true;
-    cudaGetLastError();
-    return false;
-}
-
 }  // namespace
 
 extern "C" {
@@ -671,8 +663,9 @@ bmmc_status expert_balance(const void* logits, int64_t stride, int type, const v
     together.val.clusterDim.y = together.val.clusterDim.z = 1;
     if (experts > kHeldExperts) {
         s = by_logits(type, [&](auto t) {
-            const auto kernel = balance_long_kernel<decltype(t)>;
-            if (!allow(kernel, smem)) return BMMC_ERR_CUDA;
+            constexpr auto kernel = balance_long_kernel<decltype(t)>;
+            const bmmc_status allowed = allow_smem<kernel>(smem);
+            if (allowed != BMMC_OK) return allowed;
             return launch(kernel, dim3(shape.blocks), dim3(shape.threads), smem, st, nullptr, r, sums, parts BMMC_SPANS_ARG(spans));
         });
     } else {
@@ -681,8 +674,9 @@ bmmc_status expert_balance(const void* logits, int64_t stride, int type, const v
         const bool words = word_bytes(2, {(uint64_t)(uintptr_t)logits, (uint64_t)r.stride, (uint64_t)(experts * es)}) == 16;
         const int64_t per_block = (tokens + shape.blocks - 1) / shape.blocks;
         s = by_held(type, h, words, [&](auto t, auto n, auto w, auto full) {
-            const auto kernel = balance_held_kernel<decltype(t), decltype(n)::value, decltype(w)::value, decltype(full)::value>;
-            if (!allow(kernel, smem)) return BMMC_ERR_CUDA;
+            constexpr auto kernel = balance_held_kernel<decltype(t), decltype(n)::value, decltype(w)::value, decltype(full)::value>;
+            const bmmc_status allowed = allow_smem<kernel>(smem);
+            if (allowed != BMMC_OK) return allowed;
             return launch(kernel, dim3(shape.blocks), dim3(shape.threads), smem, st, shape.together ? &together : nullptr, r, per_block,
                           sums, parts, shape.together ? loss : (float*)nullptr BMMC_SPANS_ARG(spans));
         });

@@ -86,6 +86,7 @@ __device__ __forceinline__ uint32_t key_of(const Id* ids, int64_t i, int64_t voc
 // it has sorted.
 template <class Id, bool FIRST>
 struct Sorted {
+    static constexpr bool kFirst = FIRST;
     const Id* ids;
     const uint32_t *keys, *order;
     int64_t vocab;
@@ -262,8 +263,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_cluster_kernel(const Id* __
     const Slots<int> mem(s_mem, 2 * bins + 32 + kWarps * bins / 2 + 2 * kTile);
     const Slots<int> base = mem.part(0, bins), mine_of = mem.part(bins, bins), tmp = mem.part(2 * bins, 32);
     const Slots<unsigned short> hist(reinterpret_cast<unsigned short*>(s_mem + 2 * bins + 32), kWarps * bins);
-    const Slots<int> key_at = mem.part(2 * bins + 32 + kWarps * bins / 2, kTile);
-    const Slots<int> token_at = mem.part(2 * bins + 32 + kWarps * bins / 2 + kTile, kTile);
+    const Slots<uint2> placed(reinterpret_cast<uint2*>(s_mem + 2 * bins + 32 + kWarps * bins / 2), kTile);  // keys and tokens
     cudaTriggerProgrammaticLaunchCompletion();  // the rows may be cleared meanwhile
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = warp * R * 32 + lane;
     const Slots<unsigned short> mine = hist.part(warp * bins, bins);
@@ -322,21 +322,23 @@ __global__ void __launch_bounds__(kSortThreads) sort_cluster_kernel(const Id* __
             if (first + r * 32 >= here) continue;
             const int d = (key[r] >> shift) & (bins - 1);
             const int to = base.get(d) + mine.get(d) + rank[r], b = to / kTile, at = to - b * kTile;
-            if (key_at.ok(at) && b < blocks) *cluster.map_shared_rank(key_at.p + at, b) = (int)key[r];
-            if (token_at.ok(at) && b < blocks) *cluster.map_shared_rank(token_at.p + at, b) = (int)token[r];
+            if (placed.ok(at) && b < blocks) *cluster.map_shared_rank(placed.p + at, b) = make_uint2(key[r], token[r]);
         }
         cluster.sync();  // everything is in its place, and no block's counts are read any more
         if (pass + 1 == passes) break;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int i = first + r * 32;
-            if (i < here) key[r] = key_at.get(i), token[r] = token_at.get(i);
+            if (i >= here) continue;
+            const uint2 y = placed.get(i);
+            key[r] = y.x, token[r] = y.y;
         }
     }
     for (int i = threadIdx.x; i < here; i += kSortThreads) {
         const int64_t to = (int64_t)rank_in * kTile + i;
-        if (BMMC_WR_OK(keys + to, 4)) keys[to] = key_at.get(i);
-        if (BMMC_WR_OK(order + to, 4)) order[to] = token_at.get(i);
+        const uint2 y = placed.get(i);
+        if (BMMC_WR_OK(keys + to, 4)) keys[to] = y.x;
+        if (BMMC_WR_OK(order + to, 4)) order[to] = y.y;
     }
 }
 
@@ -612,7 +614,7 @@ int64_t up16(int64_t bytes) { return (bytes + 15) & ~(int64_t)15; }
 // neither (35 us for 32768 tokens at eight keys a thread, and 28 for 100003 in
 // launches of their own).
 int cluster_rounds(int64_t n) {
-    for (int r : {1, 2, 4})
+    for (int r : {1, 2})
         if (n <= (int64_t)kSortThreads * r) return r;
     for (int r : {1, 2, 4})
         if (n <= (int64_t)kSortCluster * kSortThreads * r) return r;
@@ -659,27 +661,23 @@ bmmc_status sort_tokens(const SortShape& s, const Id* ids, int64_t n, int64_t vo
     const size_t smem = ((1 << s.digit) + 32) * 4 + (size_t)(kSortThreads / 32) * (2 << s.digit);
     for (int pass = 0; pass < s.passes; ++pass) {
         const int shift = pass * s.digit, from = (pass & 1) ^ 1, to = pass & 1;
-        bmmc_status status;
         cudaLaunchAttribute early{};
         early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
         early.val.programmaticStreamSerializationAllowed = 1;
-        const auto run = [&](auto in, auto count, auto place) {
-            if (smem > 40 * 1024 && cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-                cudaGetLastError();
-                return BMMC_ERR_CUDA;
-            }
+        const auto run = [&](auto in) {
+            using In = decltype(in);
+            constexpr auto place = digit_place_kernel<Id, In::kFirst>;
+            bmmc_status status = allow_smem<place>(smem);
+            if (status != BMMC_OK) return status;
             // (the first one waits for the work before the call, as any launch does)
-            status = launch(count, dim3(s.blocks), dim3(kSortThreads), 0, st, pass ? &early : nullptr, in, n, shift, s.digit, s.per_block,
-                            counts BMMC_SPANS_ARG(spans));
+            status = launch(digit_count_kernel<Id, In::kFirst>, dim3(s.blocks), dim3(kSortThreads), 0, st, pass ? &early : nullptr,
+                            in, n, shift, s.digit, s.per_block, counts BMMC_SPANS_ARG(spans));
             if (status != BMMC_OK) return status;
             return launch(place, dim3(s.blocks), dim3(kSortThreads), smem, st, &early, in, n, shift, s.digit, s.per_block,
                           (const int*)counts, keys[to], order[to] BMMC_SPANS_ARG(spans));
         };
-        if (pass == 0)
-            status = run(Sorted<Id, true>{ids, nullptr, nullptr, vocab}, digit_count_kernel<Id, true>, digit_place_kernel<Id, true>);
-        else
-            status = run(Sorted<Id, false>{nullptr, keys[from], order[from], vocab}, digit_count_kernel<Id, false>,
-                         digit_place_kernel<Id, false>);
+        const bmmc_status status = pass == 0 ? run(Sorted<Id, true>{ids, nullptr, nullptr, vocab})
+                                             : run(Sorted<Id, false>{nullptr, keys[from], order[from], vocab});
         if (status != BMMC_OK) return status;
     }
     return BMMC_OK;
@@ -692,11 +690,9 @@ bmmc_status sort_together(const SortShape& s, const Id* ids, int64_t n, int64_t 
     (void)spans;
     const int tile = kSortThreads * R, blocks = (int)((n + tile - 1) / tile);
     const size_t smem = ((2 << s.digit) + 32 + (kSortThreads / 64 << s.digit) + 2 * tile) * 4;
-    const auto kernel = sort_cluster_kernel<Id, R>;
-    if (smem > 40 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-        cudaGetLastError();
-        return BMMC_ERR_CUDA;
-    }
+    constexpr auto kernel = sort_cluster_kernel<Id, R>;
+    const bmmc_status allowed = allow_smem<kernel>(smem);
+    if (allowed != BMMC_OK) return allowed;
     cudaLaunchAttribute together{};
     together.id = cudaLaunchAttributeClusterDimension;
     together.val.clusterDim.x = blocks;

@@ -456,11 +456,9 @@ bmmc_status launch_append_rows(QuantisedParams& qp, const chk::Spans& spans, cud
         h.ahead = dense ? std::min((unsigned)(h.heads * qp.dims[q] * sizeof(T)), 65536u) : 0u;
     }
     const size_t smem = (size_t)kWarps * qp.stage * 4 + (size_t)per_block * p.pairs * sizeof(float2);
-    const auto kernel = append_rows_kernel<T, Q, W>;
-    if (smem > 40 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-        cudaGetLastError();
-        return BMMC_ERR_CUDA;
-    }
+    constexpr auto kernel = append_rows_kernel<T, Q, W>;
+    const bmmc_status allowed = allow_smem<kernel>(smem);
+    if (allowed != BMMC_OK) return allowed;
     const bool split = p.tokens * p.parts <= kSms * 8;
     return launch(kernel, dim3((unsigned)((p.tokens + per_block - 1) / per_block), split ? p.parts : 1), dim3(kThreads), smem, st,
                   nullptr, qp BMMC_SPANS_ARG(spans));

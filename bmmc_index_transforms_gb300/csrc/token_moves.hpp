@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <initializer_list>
 #include <type_traits>
@@ -175,6 +176,26 @@ template <class... P, class... A>
 bmmc_status launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                    cudaLaunchAttribute* attribute, const A&... args) {
     return launch_with(kernel, grid, block, smem, st, attribute, attribute ? 1 : 0, args...);
+}
+
+// Lets a kernel have `smem` bytes of dynamic shared memory, kMostSmem at most;
+// each device is told once.
+constexpr size_t kMostSmem = 200 * 1024;
+
+template <auto Kernel>
+bmmc_status allow_smem(size_t smem) {
+    static std::atomic<uint64_t> allowed{0};  // devices that were told, bit by bit (others are told every time)
+    if (smem <= 40 * 1024) return BMMC_OK;    // (48 KB with the static arrays are always allowed)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev < 64 && (allowed.load(std::memory_order_relaxed) >> dev & 1)) return BMMC_OK;
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostSmem);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return BMMC_ERR_CUDA;
+    }
+    if (dev < 64) allowed.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+    return BMMC_OK;
 }
 
 // How the words of the tokens' rows are dealt out: blocks of x * y threads

@@ -187,6 +187,15 @@ def test_append_ragged(counts, page, cached, D, interleaved, cache, dtype):
     _check_append(c, _freq(D // 2 - 3), interleaved, positions[:1].int())
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("Dk,Dv,pairs", [(512, 256, 256), (520, 264, 256), (1024, 1032, 512), (8192, 8190, 4096), (4097, 8191, 1025)])
+def test_append_and_read_of_wide_heads(Dk, Dv, pairs, interleaved):
+    c = _case(_gen(Dk), [3, 0, 5], 4, 2, 2, Dk, Dv, BF16, E4M3, False, 6)
+    _check_append(c, _freq(pairs), interleaved)
+    _check_append(c)
+    _check_read(c, F32, c["lengths"])
+
+
 @pytest.mark.parametrize("cache", [E4M3, I8])
 def test_append_skips_tokens_without_a_page(cache):
     c = _case(_gen(1), [6, 9, 0, 8], 4, 3, 2, 16, 16, F32, cache, False, 6)
