@@ -198,6 +198,18 @@ __device__ __forceinline__ void finish_loss(float dot, int choices, int tokens, 
 // Each block's sums of the shares of its tokens, and its counts.  In a small
 // call the blocks are one cluster, whose first joins them; in others each leaves
 // a row of `sums` and `counts` (loss NULL).
+//
+// The bytes could be moved in 10.1 us at 65521 tokens of 256 experts in 32 bits;
+// the two launches take 22.3.  A row is about 125 instructions of a warp (48 for
+// its 256 logits, the rest exchanges, loads and the walk), 7 us of issue slots
+// in all; the rest is latency: a block's start and its choices, the chain load -
+// largest - powers - sum - shares of 14 rows a warp, the block's own sum over its
+// warps, and the join (4 us).  One block of 32 warps an SM was taken for the join's
+// sake: blocks of 512 threads 23.8 us, of 256 27.6.  Two rows ahead instead of one
+// 22.7 (512 experts: 35.9 instead of 38.4).  A row read three times from memory by a warp,
+// its sums in shared memory, took 55 us; with expf instead of the instruction 24.
+// 131072 tokens of 61 experts of 16 bits 14.5 us, of 8 7.3; 509 tokens of 8, one
+// block, 3.7.
 template <class T, int N, bool WORDS, bool FULL>
 __global__ void __launch_bounds__(held_threads(N)) balance_held_kernel(const Router r, int64_t per_block, float* __restrict__ sums, int* __restrict__ counts,
                                                            float* __restrict__ loss BMMC_SPANS_PARAM) {
@@ -216,17 +228,13 @@ __global__ void __launch_bounds__(held_threads(N)) balance_held_kernel(const Rou
     const Slots<int> theres(s_there, 32);
     const Slots<unsigned> routed(s_routed, 32);
     using L = Logits<T, N, WORDS>;
-    // two rows ahead where a warp has one row in words (256 experts in 32 bits: one
-    // ahead 22.2 us, two 21.0; 61 of 16 bits: 14.6 and 17.2)
-    constexpr bool kDeep = FULL && WORDS;
     for (int e = threadIdx.x; e <= E; e += blockDim.x) hist.set(e, 0);
     float acc[N] = {};
     const int64_t lo = (int64_t)blockIdx.x * per_block, hi = min(r.tokens, lo + per_block);
     for (int64_t t0 = lo; t0 < hi; t0 += blockDim.x) {
         Walker w(r, t0, (int)min((int64_t)blockDim.x, hi - t0));
-        L next, after;
+        L next;
         next.load(w.row, w.here() ? E : 0, r.lanes, w.in);
-        if (kDeep) after.load(w.row + w.hop, w.i + w.step < w.n ? E : 0, r.lanes, w.in);
         __syncthreads();
         look_at_choices<true>(r, t0, w.n, routed, hist);
         __syncthreads();
@@ -234,12 +242,7 @@ __global__ void __launch_bounds__(held_threads(N)) balance_held_kernel(const Rou
             const L row = next;
             const bool counts_in = w.here() && is_there(routed, w.i);
             w.next();
-            if (kDeep) {
-                next = after;
-                after.load(w.row + w.hop, w.i + w.step < w.n ? E : 0, r.lanes, w.in);
-            } else {
-                next.load(w.row, w.here() ? E : 0, r.lanes, w.in);
-            }
+            next.load(w.row, w.here() ? E : 0, r.lanes, w.in);
             float v[N];
             const float over = softmax_of<FULL>(row, v, r.lanes);
             if (counts_in) {
@@ -450,6 +453,11 @@ __device__ __forceinline__ float factor_of(const float* grad, const int* counts,
     return n ? (BMMC_RD_OK(grad, 4) ? *grad : 0.0f) * ((float)experts / (float)n) : 0.0f;
 }
 
+// As above, with the shares' weighted sum between and the gradient written: 65521
+// tokens of 256 experts in 32 bits 25.2 us for 20.0 us of bytes (a wave of five
+// blocks of 256 threads an SM; 1214 shorter blocks, which each start by reading the
+// counts, 25.4).  131072 of 128 experts of 16 bits 23.0 (10.5): twice the logits for
+// the bytes, and the exchanges of half a warp.
 template <class T, int N, bool WORDS, bool FULL>
 __global__ void __launch_bounds__(256) balance_backward_held_kernel(const float* __restrict__ grad, const Router r,
                                                                     int64_t per_block,

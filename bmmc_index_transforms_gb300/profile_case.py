@@ -18,7 +18,10 @@ reversed, made contiguous) and lmad_permute (the shape's axes in the order
 auto / force / never chooses for the blocked copy).
 Moves of tokens (--tokens, --type; --choices, --experts, --hidden or --heads,
 --kv-heads, --dim): token_sort, token_dispatch, token_combine,
-token_combine_backward, token_rotary (positions on three axes), token_append
+token_combine_backward, token_rotary (positions on three axes), token_append,
+token_append8 and token_read8 (e4m3 pages), token_lookup and
+token_lookup_backward (--vocab; ids as frequent as words), token_balance,
+token_balance_backward
 (8 sequences, pages of 64 entries, queries turned with the keys).
 Prints the plan and the CUDA-event time of each repetition.
 """
@@ -26,6 +29,7 @@ Prints the plan and the CUDA-event time of each repetition.
 from __future__ import annotations
 
 import argparse
+import math
 import sys
 
 import torch
@@ -52,7 +56,9 @@ def main(argv=None):
                     choices=["random", "worst", "bitrev", "transpose", "dims5", "copy", "two_factor",
                              "complement", "window", "lmad_slice_2d", "lmad_slice_3d", "lmad_reversed_rows",
                              "lmad_transpose", "lmad_permute", "token_sort", "token_dispatch", "token_combine",
-                             "token_combine_backward", "token_rotary", "token_append"])
+                             "token_combine_backward", "token_rotary", "token_append", "token_lookup",
+                             "token_lookup_backward", "token_balance", "token_balance_backward", "token_append8",
+                             "token_read8"])
     ap.add_argument("--n", type=int, default=26)
     ap.add_argument("--elem", type=int, default=4)
     ap.add_argument("--seed", type=int, default=0)
@@ -65,7 +71,7 @@ def main(argv=None):
     ap.add_argument("--perm", default="", help="lmad_permute: axis order of the destination")
     ap.add_argument("--blocked", default="auto", choices=["auto", "force", "never"])
     ap.add_argument("--type", default="bf16", choices=["f32", "f16", "bf16"])
-    for name, value in (("tokens", 4096), ("choices", 8), ("experts", 64), ("hidden", 4096), ("heads", 32),
+    for name, value in (("tokens", 4096), ("vocab", 131072), ("choices", 8), ("experts", 64), ("hidden", 4096), ("heads", 32),
                         ("kv-heads", 8), ("dim", 128)):
         ap.add_argument(f"--{name}", type=int, default=value)
     a = ap.parse_args(argv)
@@ -156,7 +162,22 @@ def token_call(a):
     dtype = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[a.type]
     T, K, H, es = a.tokens, a.choices, a.hidden, 4 if a.type == "f32" else 2
     new = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=dtype)  # noqa: E731
-    if a.kind in ("token_rotary", "token_append"):
+    if a.kind in ("token_lookup", "token_lookup_backward"):
+        u = torch.rand(T, generator=g, device="cuda", dtype=torch.float64)
+        ids = (torch.exp(u * math.log(a.vocab + 1)) - 1).long().clamp(max=a.vocab - 1)
+        if a.kind == "token_lookup":
+            table = new(a.vocab, H)
+            return lambda: bm.embedding_lookup(table, ids), (T + int(ids.unique().numel())) * H * es
+        grad = new(T, H)
+        return lambda: bm.embedding_backward(grad, ids, a.vocab), (T + a.vocab) * H * es
+    if a.kind in ("token_balance", "token_balance_backward"):
+        logits = new(T, a.experts)
+        ids = logits.float().topk(K, dim=1)[1].int()
+        if a.kind == "token_balance":
+            return lambda: bm.expert_balance(logits, ids), T * (a.experts * es + K * 4)
+        counts, by = bm.expert_balance(logits, ids)[1], torch.ones((), device="cuda")
+        return lambda: bm.expert_balance_backward(by, logits, ids, counts), T * (2 * a.experts * es + K * 4)
+    if a.kind in ("token_rotary", "token_append", "token_append8", "token_read8"):
         pairs = a.dim // 2
         freq = 10000.0 ** (-torch.arange(pairs, device="cuda") / pairs)
         axes = (torch.arange(pairs, device="cuda") * 3 // pairs).int()
@@ -170,6 +191,15 @@ def token_call(a):
         columns = (T // 8 + 1000) // 64 + 2
         table = torch.randperm(8 * columns, generator=g, device="cuda").int().view(8, columns)
         lengths = torch.randint(0, 1000, (8,), generator=g, device="cuda").int()
+        if a.kind in ("token_append8", "token_read8"):
+            caches = [torch.zeros(8 * columns, 64, a.kv_heads, a.dim, device="cuda", dtype=torch.float8_e4m3fn) for _ in range(2)]
+            k_scales, v_scales = (torch.ones(8 * columns, 64, a.kv_heads, device="cuda") for _ in range(2))
+            scales = dict(k_scales=k_scales, v_scales=v_scales)
+            moved = 2 * T * a.kv_heads * (a.dim * (es + 1) + 4)
+            if a.kind == "token_read8":
+                return lambda: bm.paged_read(*caches, table, starts, T, dtype=dtype, **scales), moved
+            return lambda: bm.paged_append(k, v, *caches, table, lengths, starts=starts, q=q, inv_freq=freq,
+                                           **scales), moved + 2 * q.numel() * es
         caches = [new(8 * columns, 64, a.kv_heads, a.dim) for _ in range(2)]
         return lambda: bm.paged_append(k, v, *caches, table, lengths, starts=starts, q=q, positions=positions,
                                        inv_freq=freq, pair_axes=axes), 2 * qkv.numel() * es
