@@ -39,8 +39,10 @@ __device__ __forceinline__ int64_t row_named(Id id, int64_t vocab) {
 // Pure movement but for one product: K words of one token a thread, all on their
 // way once the id is known.  16384 tokens of 4096 bf16, as frequent as words, of a
 // table of 131072: 31.1 us, 90 % of the copy rate over the rows that differ (with one
-// word a thread 40.9); rows of 4092 34.8, of 4095, cut out of two words each, 46.  64
-// tokens 1.5 us, a launch; there a word a thread has the shorter way.
+// word a thread 40.9); rows of 4092 34.8, of 4095, cut out of two words each, 46.
+// 65536 rows of 1000 29.2 us, of 520 17.5, of 513 24.7, of 200 7.2 (25.2, 13.2, 13.0, 5.1 of
+// bytes; a word a thread in whole warps a row took 39.6, 35.2, 35.7 and 10.3).  64 tokens
+// 1.5 us, a launch; there a word a thread has the shorter way.
 template <class T, int W, bool ACROSS, int K, class Id>
 __global__ void __launch_bounds__(256) lookup_kernel(const char* __restrict__ table, int64_t table_stride, int64_t vocab,
                                                      const Id* __restrict__ ids, int64_t tokens, int length, float scale,
@@ -723,6 +725,10 @@ bmmc_status sort_together(const SortShape& s, const Id* ids, int64_t n, int64_t 
 
 extern "C" {
 
+// Words of a row from which on a thread of a large lookup takes four (65536 rows
+// of 25 words: 7.2 us, one a thread 8.4; of 9 words no difference).
+constexpr int kFourWords = 16;
+
 bmmc_status embedding_lookup(const void* table, int64_t table_stride, int64_t vocab, const void* ids, int id_bytes,
                              int64_t tokens, int64_t hidden, int type, float scale, void* out, int64_t out_stride,
                              void* stream) {
@@ -750,13 +756,18 @@ bmmc_status embedding_lookup(const void* table, int64_t table_stride, int64_t vo
         const auto go = [&](auto id, auto each) {
             using Id = decltype(id);
             constexpr int K = decltype(each)::value;
-            const Cover c = cover(tokens, (way.words + K - 1) / K, 128);
+            const int each_words = (way.words + K - 1) / K;
+            Cover c = cover(tokens, each_words, 128);
+            if (tokens * way.words > kFewWords && each_words < 96) {  // short rows: side by side, without idle lanes
+                c.block = dim3(each_words, 256 / each_words);
+                c.grid = dim3((unsigned)((tokens + c.block.y - 1) / c.block.y));
+            }
             s = launch(lookup_kernel<T, W, A, K, Id>, c.grid, c.block, 0, static_cast<cudaStream_t>(stream), nullptr,
                        static_cast<const char*>(table), table_stride * es, vocab, static_cast<const Id*>(ids), tokens,
                        (int)hidden, scale, static_cast<char*>(out), out_stride * es BMMC_SPANS_ARG(spans));
         };
         const auto with = [&](auto id) {
-            if (tokens * way.words > kFewWords && way.words >= 4 * 32) go(id, std::integral_constant<int, 4>{});
+            if (tokens * way.words > kFewWords && way.words >= kFourWords) go(id, std::integral_constant<int, 4>{});
             else go(id, std::integral_constant<int, 1>{});
         };
         id_bytes == 4 ? with(int32_t{}) : with(int64_t{});
