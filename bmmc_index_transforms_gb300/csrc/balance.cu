@@ -90,8 +90,7 @@ __device__ __forceinline__ float group_sum(float v, int lanes) {
 
 // exp(d), d <= 0, by the instruction for powers of two: within 2 ulp and 2^-23
 // of the argument, which is what the rounding of a difference of logits is worth
-// too; below 2^-126 zero.  (expf took twice the instructions, and the kernels
-// are bound by those.)
+// too; below 2^-126 zero.
 __device__ __forceinline__ float power(float d) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d * 1.44269504088896341f));
@@ -207,12 +206,13 @@ __device__ __forceinline__ void finish_loss(float dot, int choices, int tokens, 
 // warps, and the join (4 us).  One block of 32 warps an SM was taken for the join's
 // sake: blocks of 512 threads 23.8 us, of 256 27.6.  Two rows ahead instead of one
 // 22.7 (512 experts: 35.9 instead of 38.4).  A row read three times from memory by a warp,
-// its sums in shared memory, took 55 us; with expf instead of the instruction 24.
+// its sums in shared memory, took 130 us.
 // 131072 tokens of 61 experts of 16 bits 14.5 us, of 8 7.3; 509 tokens of 8, one
 // block, 3.7.
 template <class T, int N, bool WORDS, bool FULL>
-__global__ void __launch_bounds__(held_threads(N)) balance_held_kernel(const Router r, int64_t per_block, float* __restrict__ sums, int* __restrict__ counts,
-                                                           float* __restrict__ loss BMMC_SPANS_PARAM) {
+__global__ void __launch_bounds__(held_threads(N)) balance_held_kernel(const Router r, int64_t per_block,
+                                                                       float* __restrict__ sums, int* __restrict__ counts,
+                                                                       float* __restrict__ loss BMMC_SPANS_PARAM) {
     extern __shared__ int s_mem[];
     __shared__ float s_dot[32];
     __shared__ int s_all[32], s_there[32];

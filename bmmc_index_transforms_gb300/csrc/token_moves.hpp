@@ -1,7 +1,6 @@
 // Host-side checks shared by the entry points that move tokens by maps held
 // on the device (experts.cu, rotary.cu, paged_cache8.cu, embedding.cu,
-// balance.cu).  Each includes bounds.cuh before this
-// header.
+// balance.cu).  Each includes bounds.cuh before this header.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -631,8 +631,10 @@ bmmc_status expert_combine_backward(const void *grad, int64_t grad_stride, const
  *   counts[e] = c[e], e < experts; counts[experts] = n.
  * Logits of other tokens are not looked at.  An expert with the logit -inf has
  * the share 0, also in a row of nothing else.  workspace: what
- * expert_balance_workspace asks for (host only), free to reuse once the call's
- * work is done. */
+ * expert_balance_workspace asks for (host only; 0 for small calls), 16-byte
+ * aligned, free to reuse once the call's work is done; NO_SCRATCH where it is
+ * missing.  choices <= EXPERT_MAX_CHOICES, experts <= 4096, tokens * choices <
+ * 2^31. */
 bmmc_status expert_balance_workspace(int64_t tokens, int choices, int experts, size_t *bytes);
 bmmc_status expert_balance(const void *logits, int64_t stride, int type, const void *ids,
                            int id_bytes, int64_t tokens, int choices, int experts, float *loss,
@@ -661,7 +663,8 @@ bmmc_status embedding_lookup(const void *table, int64_t table_stride, int64_t vo
  * rows without a token left as they are.  out is of out_type, BMMC_F32 or
  * `type`; sums (and what is added to) are held in 32 bits, in an order that
  * depends on the ids only.  workspace: what embedding_backward_workspace asks
- * for (host only), 16-byte aligned, free to reuse once the call's work is done. */
+ * for (host only), 16-byte aligned, free to reuse once the call's work is done;
+ * NO_SCRATCH where it is missing.  vocab < 2^31 - 1. */
 bmmc_status embedding_backward_workspace(int64_t tokens, int64_t vocab, int64_t hidden,
                                          size_t *bytes);
 bmmc_status embedding_backward(const void *grad, int64_t grad_stride, const void *ids,
