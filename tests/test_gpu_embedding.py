@@ -300,3 +300,37 @@ def test_ids_that_change_under_a_captured_call():
         at, row = _named(ids, V)
         want = torch.zeros(V, H, dtype=torch.float64, device="cuda").index_add_(0, row, grad[at].double())
         assert torch.equal(got, want.float())
+
+
+@pytest.mark.parametrize("T", [700, 40000])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_backward_captured_and_behind_other_work(T, accumulate):
+    """The sort as one block and as several launches, captured and replayed
+    behind a kernel that writes the gradient, and before one that reads the result."""
+    g = _gen(T)
+    V, H = 300, 72
+    grad, ids = _rows(g, T, H, BF16, whole=True), _ids(g, T, V, "rare")
+    at, row = _named(ids, V)
+    want = torch.zeros(V, H, dtype=torch.float64, device="cuda").index_add_(0, row, grad[at].double()).float()
+    held, out = torch.empty_like(grad), torch.zeros(V, H, device="cuda")
+    total = torch.zeros(V, H, device="cuda")
+
+    def run():
+        held.copy_(grad)
+        bm.embedding_backward(held, ids, out=out, accumulate=accumulate)
+        total.add_(out)
+        held.zero_()
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            run()
+    out.zero_()
+    total.zero_()
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, 6 * want if accumulate else want)
+    assert torch.equal(total, 21 * want if accumulate else 6 * want)
