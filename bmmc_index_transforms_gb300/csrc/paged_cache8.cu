@@ -497,7 +497,7 @@ struct ReadParams {
     int dims[2];
     int rows;           // of a block
     int words[2];       // of a head
-    unsigned magic[2];  // 2^32 / words rounded up
+    uint64_t magic[2];  // wide_magic_of(words)
 };
 
 // W elements of the result from what the cache holds: themselves, or W codes
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kReadThreads) read_words_kernel(const __grid_c
         constexpr int q = decltype(which)::value;
         const Heads& h = p.part[q];
         for (int j = threadIdx.x; j < h.heads * rp.words[q]; j += blockDim.x) {
-            const int head = rp.words[q] == 1 ? j : (int)__umulhi(j, rp.magic[q]), at = (j - head * rp.words[q]) * W;
+            const int head = wide_quotient(j, rp.magic[q]), at = (j - head * rp.words[q]) * W;
             const char* const src = h.src + head * h.src_head + at * (Word::kBytes / W);
             const int first = SIDE ? threadIdx.y : 0, step = SIDE ? blockDim.y : 1;
             char* to = h.dst + (t0 + first) * h.dst_token + head * h.dst_head + at * (int)sizeof(T);
@@ -623,7 +623,7 @@ bmmc_status launch_read_words(ReadParams& rp, const chk::Spans& spans, cudaStrea
     int most = 1;
     for (int q = 0; q < 2; ++q) {
         rp.words[q] = rp.dims[q] / W;
-        rp.magic[q] = (unsigned)((((uint64_t)1 << 32) + rp.words[q] - 1) / rp.words[q]);
+        rp.magic[q] = wide_magic_of(rp.words[q]);
         most = std::max(most, rp.moves.part[q].heads * rp.words[q]);
     }
     // threads of a row, and rows side by side; several rows a thread where the

@@ -15,6 +15,13 @@ namespace bmmc {
 inline unsigned magic_of(int d) { return d > 1 ? (unsigned)((((uint64_t)1 << 32) + d - 1) / d) : 0; }
 __device__ __forceinline__ int quotient(int x, int d, unsigned magic) { return d == 1 ? x : (int)__umulhi(x, magic); }
 
+// The same for x < 2^24 and d <= 2^13 (elements of an entry, and of a head), with
+// wide_magic_of(d) = 2^38 / d rounded up: (2^38 + e) / d with e < d.  The quotient
+// is then x / d + x * e / (d * 2^38), and as x * e < 2^37 the second term is less
+// than 1 / d: it does not reach the next whole number.
+inline uint64_t wide_magic_of(int d) { return (((uint64_t)1 << 38) + d - 1) / d; }
+__host__ __device__ __forceinline__ int wide_quotient(int x, uint64_t magic) { return (int)((uint64_t)x * magic >> 38); }
+
 // A shared array, or a part of one, whose elements are reached by number.  In
 // bounds-checked builds each number is tested against the length, and each
 // address against the arrays that the kernel registered; otherwise it is a
