@@ -375,8 +375,9 @@ __global__ void __launch_bounds__(kThreads) balance_long_kernel(const Router r, 
 
 // The rows of sums and counts joined by one cluster: its blocks take every
 // eighth row, in each of them a few threads an expert, and the first block adds
-// what they have, in order.
-__global__ void __launch_bounds__(1024) balance_join_kernel(const float* __restrict__ sums, const int* __restrict__ counts,
+// what they have, in order.  The rows are still being written when this kernel
+// starts: they are read by __ldcg, behind the wait.
+__global__ void __launch_bounds__(1024) balance_join_kernel(const float* sums, const int* counts,
                                                             int rows, int experts, int parts, float* __restrict__ loss,
                                                             int* __restrict__ out_counts BMMC_SPANS_PARAM) {
     extern __shared__ int s_mem[];  // [parts][experts + 1] of each

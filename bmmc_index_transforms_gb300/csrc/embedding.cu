@@ -88,6 +88,15 @@ __device__ __forceinline__ uint32_t key_of(const Id* ids, int64_t i, int64_t voc
     return (uint32_t)(row < 0 ? vocab : row);
 }
 
+// The kernels of a gradient are launched early, one behind another: each waits for
+// the one before it as a whole before it reads or writes anything.  While it waits,
+// what it is going to read (counts, keys, order, partial sums) is still being
+// written: those are no __restrict__ const parameters, which the compiler may read
+// ahead of the wait or by loads that are not told of the writes.  Ordinary loads
+// stay behind the wait, which shows them what was written; __ldcg in their place took
+// the gradient of 2039 x 1031 23.3 us instead of 22.4, of 32768 rows of 4096 220.8 instead
+// of 219.4.
+
 // What a pass sorts: the tokens by their ids (FIRST), or what the pass before
 // it has sorted.
 template <class Id, bool FIRST>
@@ -166,16 +175,13 @@ __device__ __forceinline__ unsigned same_digit(int d, int bits) {
     return same;
 }
 
-// (The kernels of the sort are launched early, one behind another: each waits for
-// the one before it as a whole before it reads or writes anything.)
-//
 // One pass of the sort, stable: every block puts its part in place, a tile at
 // a time.  A key's rank among the equal digits of its warp comes from ballots
 // and the warp's running counts; sums over the warps and the counts of the
 // blocks ahead complete its place.
 template <class Id, bool FIRST>
 __global__ void __launch_bounds__(kSortThreads) digit_place_kernel(Sorted<Id, FIRST> in, int64_t n, int shift, int digit,
-                                                                   int64_t per_block, const int* __restrict__ counts,
+                                                                   int64_t per_block, const int* counts,
                                                                    uint32_t* __restrict__ keys,
                                                                    uint32_t* __restrict__ order BMMC_SPANS_PARAM) {
     constexpr int kWarps = kSortThreads / 32;
@@ -420,9 +426,8 @@ __device__ __forceinline__ void put_words(const float (&v)[W], O* p, bool accumu
 // elements (32768 rows of 4095 bf16 into 32768: 168 us, of 4096 116).
 template <class T, class O, int W, bool WORDS>
 __global__ void __launch_bounds__(kSumThreads) sum_rows_kernel(const char* __restrict__ grad, int64_t grad_stride,
-                                                               const uint32_t* __restrict__ keys,
-                                                               const uint32_t* __restrict__ order, int64_t n, int chunk,
-                                                               const SumTo o BMMC_SPANS_PARAM) {
+                                                               const uint32_t* keys, const uint32_t* order, int64_t n,
+                                                               int chunk, const SumTo o BMMC_SPANS_PARAM) {
     __shared__ int s_key[2 * kChunk + 1], s_token[2 * kChunk];
     __shared__ float s_sum[WORDS ? 1 : kSumThreads * W];
     BMMC_SPANS_ENTER(s_key, sizeof(s_key), s_token, sizeof(s_token), s_sum, sizeof(s_sum));
@@ -516,7 +521,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_rows_kernel(const char* __res
 // start there, and takes 128 columns of each: its warps add every eighth part,
 // then the eight sums are added in order.
 template <class O>
-__global__ void __launch_bounds__(256) join_parts_kernel(const uint32_t* __restrict__ keys, int64_t n, int chunk,
+__global__ void __launch_bounds__(256) join_parts_kernel(const uint32_t* keys, int64_t n, int chunk,
                                                          const SumTo o BMMC_SPANS_PARAM) {
     __shared__ float s_sum[8 * 128];
     BMMC_SPANS_ENTER(s_sum, sizeof(s_sum));
