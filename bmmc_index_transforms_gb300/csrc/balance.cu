@@ -71,7 +71,8 @@ struct Logits {
 template <bool FULL>
 __device__ __forceinline__ float group_max(float v, int lanes) {
     if constexpr (FULL) {
-        asm("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(v));
+        // (volatile: all of the lanes meet in it, wherever the compiler puts what surrounds it)
+        asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(v));
     } else {
         for (int d = lanes >> 1; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, d));
     }
