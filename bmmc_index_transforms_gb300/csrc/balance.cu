@@ -89,20 +89,31 @@ __device__ __forceinline__ float group_sum(float v, int lanes) {
     return v;
 }
 
-// exp(d), d <= 0, by the instruction for powers of two: within 2 ulp and 2^-23
-// of the argument, which is what the rounding of a difference of logits is worth
-// too; below 2^-126 zero.
+// exp(d), d <= 0, by the instruction for powers of two, 2^e with e the rounded
+// d * log2(e), times 1 + r where r = d - e * ln(2) is what the rounding left out
+// (below 2^-17, so that its square does not count).  Without it the result is off by
+// |d| * 2^-24 of itself, which the rounding of a difference of logits is worth only
+// where these have 32 bits: differences of 16-bit logits are mostly exact.  With it, by
+// the instruction's 2 ulp, a rounding and |d| * 2^-28 for ln(2) in 32 bits; below
+// 2^-126 it is zero.  Far differences (-inf, whose r would be NaN) are cut off at -200,
+// where it is zero anyway; NaN stays.  65521 x 256 22.2 us without r, 22.8 with it, 131072 x
+// 128 of 16 bits 19.6 and 20.8; expf in its place is as exact, takes 22.1 and 26.5, and
+// the gradients 30.7 and 26.3 instead of 25.4 and 24.7.
 __device__ __forceinline__ float power(float d) {
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d * 1.44269504088896341f));
-    return y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(d), "f"(-200.0f));
+    const float e = d * 1.44269504088896341f;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(e));
+    return fmaf(y, fmaf(e, -0.693147180559945309f, d), y);
 }
 
-// One over the sum of a row's powers, within 1 ulp; zero for a row whose logits
-// are all -inf.
+// One over the sum of a row's powers: the instruction's value, within 1 ulp, and one
+// step of Newton's iteration, which leaves the rounding; zero for a row whose
+// logits are all -inf.
 __device__ __forceinline__ float over_sum(float sum) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(sum));
+    y = fmaf(y, fmaf(-sum, y, 1.0f), y);
     return sum == 0.0f ? 0.0f : y;
 }
 
@@ -200,16 +211,16 @@ __device__ __forceinline__ void finish_loss(float dot, int choices, int tokens, 
 // a row of `sums` and `counts` (loss NULL).
 //
 // The bytes could be moved in 10.1 us at 65521 tokens of 256 experts in 32 bits;
-// the two launches take 22.3.  A row is about 125 instructions of a warp (48 for
-// its 256 logits, the rest exchanges, loads and the walk), 7 us of issue slots
+// the two launches take 22.7.  A row is about 150 instructions of a warp (72 for
+// its 256 logits, the rest exchanges, loads and the walk), 8.5 us of issue slots
 // in all; the rest is latency: a block's start and its choices, the chain load -
 // largest - powers - sum - shares of 14 rows a warp, the block's own sum over its
 // warps, and the join (4 us).  One block of 32 warps an SM was taken for the join's
-// sake: blocks of 512 threads 23.8 us, of 256 27.6.  Two rows ahead instead of one
-// 22.7 (512 experts: 35.9 instead of 38.4).  A row read three times from memory by a warp,
-// its sums in shared memory, took 130 us.
-// 131072 tokens of 61 experts of 16 bits 14.5 us, of 8 7.3; 509 tokens of 8, one
-// block, 3.7.
+// sake (before the powers carried their remainder 22.3 us; blocks of 512 threads 23.8,
+// of 256 27.6; two rows ahead instead of one 22.7, and with 512 experts 35.9 instead of
+// 38.4).  A row read three times from memory by a warp, its sums in shared memory, took
+// 130 us.  131072 tokens of 61 experts of 16 bits 15.2 us, of 8 7.5; 509 tokens of 8, one
+// block, 3.6.
 template <class T, int N, bool WORDS, bool FULL>
 __global__ void __launch_bounds__(held_threads(N)) balance_held_kernel(const Router r, int64_t per_block,
                                                                        float* __restrict__ sums, int* __restrict__ counts,
@@ -456,10 +467,10 @@ __device__ __forceinline__ float factor_of(const float* grad, const int* counts,
 }
 
 // As above, with the shares' weighted sum between and the gradient written: 65521
-// tokens of 256 experts in 32 bits 25.2 us for 20.0 us of bytes (a wave of five
+// tokens of 256 experts in 32 bits 25.4 us for 20.0 us of bytes (a wave of five
 // blocks of 256 threads an SM; 1214 shorter blocks, which each start by reading the
-// counts, 25.4).  131072 of 128 experts of 16 bits 23.0 (10.5): twice the logits for
-// the bytes, and the exchanges of half a warp.
+// counts, took 0.2 us more).  131072 of 128 experts of 16 bits 24.6 (10.5): twice the
+// logits for the bytes, and the exchanges of half a warp.
 template <class T, int N, bool WORDS, bool FULL>
 __global__ void __launch_bounds__(256) balance_backward_held_kernel(const float* __restrict__ grad, const Router r,
                                                                     int64_t per_block,
