@@ -662,6 +662,16 @@ bmmc_status read_scales(const paged_cache_t& s, int64_t pages, int64_t page_size
     return BMMC_OK;
 }
 
+// Whether two arrays [pages][page_size][heads] of runs of run_* bytes, with strides
+// in elements of *_bytes, lie between each other: by page, entry or head.
+bool lies_between(const paged_cache_t& a, int64_t run_a, int a_bytes, const paged_cache_t& b, int64_t run_b, int b_bytes,
+                  int64_t pages, int64_t page_size, int64_t heads) {
+    const int64_t sizes[3] = {pages, page_size, heads};
+    const int64_t strides_a[3] = {a.page_stride * a_bytes, a.slot_stride * a_bytes, a.head_stride * a_bytes};
+    const int64_t strides_b[3] = {b.page_stride * b_bytes, b.slot_stride * b_bytes, b.head_stride * b_bytes};
+    return lie_between(run_a, run_b, sizes, strides_a, strides_b, (int64_t)((uintptr_t)b.data - (uintptr_t)a.data));
+}
+
 // Whether two results lie between each other, by token or by head.
 bool heads_between(const token_heads_t& k, const token_heads_t& v, int64_t tokens, int es) {
     if ((tokens > 1 && k.token_stride != v.token_stride) || (k.heads > 1 && k.head_stride != v.head_stride)) return false;
@@ -698,14 +708,21 @@ bmmc_status paged_append_quantised(const paged_append_quantised_args_t* args, vo
     for (int i = 0; i < 2; ++i)
         if ((s = read_scales(*from[i], a.pages, a.page_size, a.k.heads, qp.scales[i], scales[i])) != BMMC_OK) return s;
     for (const Rows& r : scales) {
-        for (const Rows& w : c.written)
-            if (may_overlap(r, w)) return BMMC_ERR_ALIAS;
         for (const Rows& m : c.maps)
             if (may_overlap(r, m)) return BMMC_ERR_ALIAS;
-        if (may_overlap(r, c.k) || may_overlap(r, c.v) || may_overlap(r, c.q) || meets_turns(r, a.turns, a.tokens))
+        if (may_overlap(r, c.k) || may_overlap(r, c.v) || may_overlap(r, c.q) || may_overlap(r, c.written[2]) ||
+            meets_turns(r, a.turns, a.tokens))
             return BMMC_ERR_ALIAS;
     }
-    if (may_overlap(scales[0], scales[1])) return BMMC_ERR_ALIAS;
+    // scales may lie between the caches' values (behind each head's, or behind an entry's) and between each other
+    const paged_cache_t* values[2] = {&a.k_cache, &a.v_cache};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2; ++j)
+            if (may_overlap(scales[i], c.written[j]) &&
+                !lies_between(*from[i], 4, 4, *values[j], c.dims[j], 1, a.pages, a.page_size, a.k.heads))
+                return BMMC_ERR_ALIAS;
+    if (may_overlap(scales[0], scales[1]) && !lies_between(*from[0], 4, 4, *from[1], 4, 4, a.pages, a.page_size, a.k.heads))
+        return BMMC_ERR_ALIAS;
     if ((s = append_reachable(a, device)) != BMMC_OK) return s;
     if ((s = all_reachable(device, {args->k_scales.data, args->v_scales.data})) != BMMC_OK) return s;
     qp.moves = c.moves;

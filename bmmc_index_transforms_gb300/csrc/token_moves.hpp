@@ -99,6 +99,7 @@ bool lie_between(int64_t run_a, int64_t run_b, const int64_t (&sizes)[N], const 
         __int128 rest = 0;
         for (int j = k + 1; j < N; ++j)
             if (sizes[order[j]] > 1) rest += (__int128)(sizes[order[j]] - 1) * strides[order[j]];
+        if (run_a + rest > s || run_b + rest > s) return false;  // (no nest: only where runs have gaps, see below)
         const int64_t d = (distance % s + s) % s;  // from a row of a to the row of b that starts behind it
         if (d >= run_a + rest) {
             if (d + run_b + rest <= s) return true;
@@ -109,6 +110,21 @@ bool lie_between(int64_t run_a, int64_t run_b, const int64_t (&sizes)[N], const 
         }
     }
     return distance >= run_a || distance + run_b <= 0;
+}
+
+// The same for two arrays of the same sizes whose strides may differ: a dimension
+// with two strides is taken as a part of the runs, gaps and all.
+template <int N>
+bool lie_between(int64_t run_a, int64_t run_b, const int64_t (&sizes)[N], const int64_t (&a)[N], const int64_t (&b)[N],
+                 int64_t distance) {
+    int64_t nest[N];
+    for (int i = 0; i < N; ++i) {
+        nest[i] = a[i] == b[i] ? sizes[i] : 1;
+        if (nest[i] == sizes[i]) continue;
+        run_a += (sizes[i] - 1) * a[i];
+        run_b += (sizes[i] - 1) * b[i];
+    }
+    return lie_between(run_a, run_b, nest, a, distance);
 }
 
 // Whether the elements of an array with these sizes and strides (elements;

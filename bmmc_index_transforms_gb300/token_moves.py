@@ -556,7 +556,8 @@ def paged_append(k, v, k_cache, v_cache, page_table, lengths, *, starts=None, q=
 
     Caches of 8 bits (float8_e4m3fn or int8) come with k_scales and v_scales,
     float32 [pages, page_size, kv_heads], or [pages, kv_heads, page_size] if
-    head_major, of any strides: a head is written as values times a scale, its
+    head_major, of any strides (also in the caches' own gaps: behind a head's
+    values, or an entry's): a head is written as values times a scale, its
     largest element over the type's (448 or 127).  paged_read reads them back."""
     if _torch is None:
         _setup()

@@ -748,7 +748,11 @@ typedef struct {
     int64_t cache_type;                /* BMMC_E4M3 or BMMC_I8 */
     paged_cache_t k_scales, v_scales;  /* floats, [pages][page_size][heads] in any order of strides:
                                           the scale of a head at data[p * page_stride + slot *
-                                          slot_stride + h * head_stride] */
+                                          slot_stride + h * head_stride].  They may lie in the gaps of
+                                          the caches (behind a head's values, or an entry's) and of
+                                          each other where the strides that lead past these are the
+                                          same in bytes; arrays that are not told apart are refused
+                                          with ALIAS */
 } paged_append_quantised_args_t;
 
 /* Append to caches of 8 bits: a head y (keys turned; 32 bits) has the scale
