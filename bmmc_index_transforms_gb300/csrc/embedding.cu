@@ -519,7 +519,10 @@ __global__ void __launch_bounds__(kSumThreads) sum_rows_kernel(const char* __res
 
 // Joins the parts of the long runs: a block looks at 32 chunks for runs that
 // start there, and takes 128 columns of each: its warps add every eighth part,
-// then the eight sums are added in order.
+// then the eight sums are added in order.  However long a run, a block for 128 columns
+// has it alone: the gradient of 100003 rows of 1280 bf16 into 131072 takes 138 us with ids
+// as frequent as words, 227 where one id is half of them, and 287 where all are one;
+// of 1048576 rows 774, 1675 and 2660.
 template <class O>
 __global__ void __launch_bounds__(256) join_parts_kernel(const uint32_t* keys, int64_t n, int chunk,
                                                          const SumTo o BMMC_SPANS_PARAM) {
@@ -636,8 +639,9 @@ SortShape sort_shape(int64_t n, int64_t vocab) {
 int64_t up16(int64_t bytes) { return (bytes + 15) & ~(int64_t)15; }
 
 // Keys a thread takes where the sort is one block, or else one cluster; 0: it is
-// neither (35 us for 32768 tokens at eight keys a thread, and 28 for 100003 in
-// launches of their own).
+// neither.  Eight blocks of four keys a thread end at 32768 tokens, which take 19 us
+// (as four blocks of eight keys a thread 35); 100003 in launches of their own take 28.
+// Eight blocks of eight keys, up to 65536, were not timed.
 int cluster_rounds(int64_t n) {
     for (int r : {1, 2})
         if (n <= (int64_t)kSortThreads * r) return r;

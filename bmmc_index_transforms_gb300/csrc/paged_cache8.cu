@@ -217,8 +217,10 @@ __device__ __forceinline__ void append_part(const QuantisedParams& qp, int64_t t
 // threads each, and a thread its word (two, where a pair's elements lie half a
 // head apart) of one head after another, two at a time, its cosines and sines
 // in registers.  The threads of a head are neighbouring lanes, a power of two of
-// them, which find its largest element by exchange.  Nothing of a head is kept
-// anywhere but in registers.
+// them, which find its largest element by exchange.  A head stays in registers from
+// load to store; under the 64 of a thread the variants of 16-bit heads with pairs half
+// a head apart keep some of the rest aside (bf16: 76 bytes written, 124 read a thread;
+// f16: 52 and 84; 80 registers, which hold all, were slower, see below).
 //
 // 16001 tokens of 32 + 8 + 8 heads of 128 bf16 into e4m3 pages 68 us for 53 us of
 // bytes (the same heads into pages of their own type 63 for 58): 53 million warp
@@ -226,7 +228,9 @@ __device__ __forceinline__ void append_part(const QuantisedParams& qp, int64_t t
 // products and conversions themselves; and the start of a block.  One head at a time
 // instead of two 78 us, twice the threads a token 102, half of them 74; 80 registers
 // a thread 69.  Staged by element in shared memory it took 208.  256 single tokens
-// 4.2 us.
+// 4.2 us.  Keys and values alone into whole numbers, unturned, 40 us for 14.6 of bytes:
+// 64 % of the issue slots, 115 instructions of a warp a head (it has two at a time), the
+// block's start included, and 42 % of the warps there.
 template <class T, class Q, bool ADJACENT>
 __global__ void __launch_bounds__(kMostThreads, 4) append_words_kernel(const __grid_constant__ QuantisedParams qp BMMC_SPANS_PARAM) {
     extern __shared__ float2 s_turn[];  // [tokens of the block][pairs] cos, sin

@@ -18,11 +18,11 @@ reversed, made contiguous) and lmad_permute (the shape's axes in the order
 auto / force / never chooses for the blocked copy).
 Moves of tokens (--tokens, --type; --choices, --experts, --hidden or --heads,
 --kv-heads, --dim): token_sort, token_dispatch, token_combine,
-token_combine_backward, token_rotary (positions on three axes), token_append,
-token_append8 and token_read8 (e4m3 pages), token_lookup and
+token_combine_backward, token_rotary (positions on three axes), token_append
+(8 sequences, pages of 64 entries, queries turned with the keys),
+token_append8 and token_read8 (the same with e4m3 pages), token_lookup and
 token_lookup_backward (--vocab; ids as frequent as words), token_balance,
-token_balance_backward
-(8 sequences, pages of 64 entries, queries turned with the keys).
+token_balance_backward.
 Prints the plan and the CUDA-event time of each repetition.
 """
 
