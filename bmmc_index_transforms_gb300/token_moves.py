@@ -637,6 +637,8 @@ def paged_read(k_cache, v_cache, page_table, starts, num_rows=None, *, firsts=No
         if k_out is None:
             _no(where, "num_rows or k_out is needed")
         num_rows = k_out.shape[0]
+    if num_rows < 0:
+        _no(where, f"num_rows {num_rows} is negative")
     heads = k_cache.shape[1 if head_major else 2]
     B, columns, table_stride = _table(page_table, where)
     if starts.dtype is not _int32 or starts.shape != (B + 1,) or not starts.is_contiguous():
