@@ -621,22 +621,23 @@ def paged_read(k_cache, v_cache, page_table, starts, num_rows=None, *, firsts=No
     receives sequence b's entry firsts[b] + j (without firsts: j), up to row
     starts[b + 1] - 1; zeros where a row belongs to no sequence or its entry
     has no page.  The result is of the caches' type or, from caches of 8 bits,
-    of ``dtype`` (or that of k_out and v_out, where they are given)."""
+    of ``dtype``; where k_out or v_out is given, type and rows may be left to it."""
     if _torch is None:
         _setup()
     where = "paged_read"
     cache_type = _cache_types.get(k_cache.dtype)
     if k_cache.dim() != 4 or v_cache.dim() != 4:
         _no(where, "the caches must be 4-D")
-    out_dtype = dtype if dtype is not None else k_out.dtype if k_out is not None else k_cache.dtype
+    given = k_out if k_out is not None else v_out
+    out_dtype = dtype if dtype is not None else given.dtype if given is not None else k_cache.dtype
     t = _types.get(out_dtype)
     if t is None or (cache_type is None and out_dtype != k_cache.dtype):
         _no(where, f"caches of {k_cache.dtype} are read back as "
                    f"{k_cache.dtype if cache_type is None else 'the float32, float16 or bfloat16 that dtype says'}")
     if num_rows is None:
-        if k_out is None:
-            _no(where, "num_rows or k_out is needed")
-        num_rows = k_out.shape[0]
+        if given is None:
+            _no(where, "num_rows, k_out or v_out is needed")
+        num_rows = given.shape[0]
     if num_rows < 0:
         _no(where, f"num_rows {num_rows} is negative")
     heads = k_cache.shape[1 if head_major else 2]
